@@ -20,7 +20,8 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (HQ_CENTER_CHANNEL, HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CODES_E2M3,
+from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU,
+                   HQ_CENTER_CHANNEL, HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CODES_E2M3,
                    HQ_CODES_I8, HQ_GEMM_AUTO, HQ_GEMM_I8, HQ_INT_ACT_GELU, HQ_INT_ACT_NONE,
                    HQ_INT_ACT_RELU, HQ_INT_ACT_SILU, HQ_INT_DH, HQ_INT_WH, HqDesc, HqError,
                    HqLayout, check, load)
@@ -365,6 +366,119 @@ def prepared_views(desc: Desc, prepared: torch.Tensor) -> dict:
     }
     if _channel(desc):
         out["weight"] = view(L.weight, desc.d_out * d, _TORCH[desc.w_dtype], (desc.d_out, d))
+    return out
+
+
+# ---- epilogues and dense layers ---------------------------------------------
+
+class _on:
+    """Makes ``device`` current for the launch of a call on its tensors."""
+    __slots__ = ("index", "prev")
+
+    def __init__(self, device: torch.device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.index != self.prev:
+            torch.cuda.set_device(self.index)
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.index != self.prev:
+            torch.cuda.set_device(self.prev)
+
+
+def _same_device(ref: torch.Tensor, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, X on {ref.device}")
+
+
+@dataclasses.dataclass(frozen=True)
+class Epilogue:
+    """Y = residual + gate * phi(V) behind a layer's output V (hq_epilogue).
+    ``act``: HQ_ACT_*; ``residual`` [T, d_out] (may be the call's ``out``);
+    ``gate`` [samples, d_out], one row per ``gate_rows`` rows of Y (rows of
+    the gate may be strided: one part of a modulation table)."""
+    act: int = HQ_ACT_NONE
+    residual: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    gate_rows: int = 0
+
+    def _c(self, X: torch.Tensor, T: int, d_out: int, dtype: torch.dtype):
+        g, r, ld = self.gate, self.residual, 0
+        if r is not None:
+            _need(r, "residual", dtype, (T, d_out))
+        if g is not None:
+            if not isinstance(g, torch.Tensor) or not g.is_cuda or g.dtype != dtype:
+                raise ValueError(f"gate must be a CUDA (HIP) tensor of {dtype}")
+            rows = -(-T // self.gate_rows) if self.gate_rows > 0 else 0
+            if g.dim() != 2 or g.shape[1] != d_out or g.shape[0] < rows:
+                raise ValueError(f"gate must have shape (>= {rows}, {d_out}), got {tuple(g.shape)}")
+            if g.stride(1) != 1:
+                raise ValueError("gate rows must be contiguous")
+            ld = g.stride(0) if g.shape[0] > 1 else d_out
+        _same_device(X, residual=r, gate=g)
+        return ctypes.byref(_lib.HqEpilogue(self.act, r.data_ptr() if r is not None else None,
+                                            g.data_ptr() if g is not None else None,
+                                            self.gate_rows, ld))
+
+
+@dataclasses.dataclass(frozen=True)
+class LinearDesc:
+    """Dense-layer descriptor; mirrors hq_linear_desc (x_dtype = w_dtype)."""
+    d_in: int
+    d_out: int
+    x_dtype: int = F32
+    w_dtype: int = F32
+    y_dtype: int = F32
+
+    def __post_init__(self):
+        raw = _lib.HqLinearDesc(self.d_in, self.d_out, self.x_dtype, self.w_dtype, self.y_dtype)
+        object.__setattr__(self, "_raw", raw)
+        object.__setattr__(self, "_ref", ctypes.byref(raw))
+
+
+def linear_workspace_bytes(desc: LinearDesc, T: int) -> int:
+    """Workspace bytes of linear for T rows (0 for most shapes)."""
+    n = load().hq_linear_workspace_bytes(desc._ref, T)
+    if n == 0:
+        check(load().hq_linear_validate(desc._ref))
+        if T < 0:
+            raise HqError(_lib.HQ_ERR_INVALID_ARG, "T must be >= 0")
+    return n
+
+
+def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
+           bias: Optional[torch.Tensor] = None, epilogue: Optional[Epilogue] = None,
+           out: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = residual + gate * phi(X weight^T + bias) for X [T, d_in] and weight
+    [d_out, d_in], both bf16 or both fp32 (hq_linear): the layers that are not
+    quantised. ``workspace`` (linear_workspace_bytes(desc, T) bytes) is
+    allocated when it is needed and not given."""
+    T = X.shape[0]
+    _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
+    _need(weight, "weight", _TORCH[desc.w_dtype], (desc.d_out, desc.d_in))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (desc.d_out,))
+    ydt = _TORCH[desc.y_dtype]
+    if out is None:
+        out = torch.empty(T, desc.d_out, dtype=ydt, device=X.device)
+    else:
+        _need(out, "out", ydt, (T, desc.d_out))
+    _same_device(X, weight=weight, bias=bias, out=out, workspace=workspace)
+    ep = None if epilogue is None else epilogue._c(X, T, desc.d_out, ydt)
+    lib = load()
+    if workspace is None:
+        n = lib.hq_linear_workspace_bytes(desc._ref, T)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+    with _on(X.device) as stream:
+        check(lib.hq_linear(desc._ref, _ptr(X), _ptr(weight), _ptr(bias), T, ep, _ptr(out),
+                            _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                            stream))
     return out
 
 

@@ -35,7 +35,18 @@ class HqIntLayout(ctypes.Structure):
         (n, ctypes.c_size_t) for n in ["lut", "mult_in", "shift_in"]]
 
 
+class HqEpilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("residual", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+                ("gate_ld", ctypes.c_int64)]
+
+
+class HqLinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ["d_in", "d_out", "x_dtype", "w_dtype", "y_dtype"]]
+
+
 HQ_CODES_I8, HQ_CODES_E2M3 = 0, 1
+HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_I8 = 0, 1
 HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CENTER_CHANNEL = 0, 1, 2
 HQ_INT_WH, HQ_INT_DH = 0, 1
@@ -47,6 +58,8 @@ HQ_OK, HQ_ERR_INVALID_ARG, HQ_ERR_UNSUPPORTED, HQ_ERR_WORKSPACE, HQ_ERR_BAD_PREP
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(HqDesc)
 _W = ctypes.POINTER(HqIntDesc)
+_E = ctypes.POINTER(HqEpilogue)
+_L = ctypes.POINTER(HqLinearDesc)
 _I64 = ctypes.c_int64
 _SIGS = {
     "hq_abi_version": (ctypes.c_int, []),
@@ -64,6 +77,9 @@ _SIGS = {
     "hq_check_prepared": (ctypes.c_int, [_D, _P, _P]),
     "hq_quant_linear": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
     "hq_quant_linear_noalloc": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P]),
+    "hq_linear_validate": (ctypes.c_int, [_L]),
+    "hq_linear_workspace_bytes": (ctypes.c_size_t, [_L, _I64]),
+    "hq_linear": (ctypes.c_int, [_L, _P, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
     "hq_channel_center": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     "hq_act_quantize": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P]),
     "hq_act_quantize_ws": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P,

@@ -287,6 +287,88 @@ int run_gemm_dequant(const hq_desc* d, const void* prepared, const void* codes,
   return HQ_OK;
 }
 
+// ---- dense layers and the epilogue --------------------------------------------
+
+// Row limit of the dense layer and the norm: tile and block counts stay below
+// 2^31 at every width.
+constexpr int64_t kMaxRows = int64_t(1) << 26;
+constexpr int kMaxWidth = 65536;
+
+inline size_t dtype_size(int dt) { return dt == HQ_BF16 ? 2 : 4; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+int check_dtype(int dt, const char* what) {
+  if (dt != HQ_F32 && dt != HQ_BF16)
+    return fail(HQ_ERR_INVALID_ARG, "%s %d is not an hq_dtype", what, dt);
+  return HQ_OK;
+}
+
+int check_linear_desc(const hq_linear_desc* d) {
+  if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
+  if (d->d_in <= 0 || d->d_out <= 0)
+    return fail(HQ_ERR_INVALID_ARG, "d_in and d_out must be positive (got %d, %d)", d->d_in,
+                d->d_out);
+  int st = check_dtype(d->x_dtype, "x_dtype");
+  if (st == HQ_OK) st = check_dtype(d->w_dtype, "w_dtype");
+  if (st == HQ_OK) st = check_dtype(d->y_dtype, "y_dtype");
+  if (st != HQ_OK) return st;
+  if (d->x_dtype != d->w_dtype)
+    return fail(HQ_ERR_UNSUPPORTED, "x_dtype and w_dtype must be the same (got %d, %d)",
+                d->x_dtype, d->w_dtype);
+  if (d->d_in % 8 || d->d_out % 8 || d->d_in > kMaxWidth || d->d_out > kMaxWidth)
+    return fail(HQ_ERR_UNSUPPORTED, "d_in and d_out must be multiples of 8 up to %d (got %d, %d)",
+                kMaxWidth, d->d_in, d->d_out);
+  return HQ_OK;
+}
+
+// Checks an epilogue for an output Y [T, d_out] of type y_dtype and lays it
+// out for the kernels (ep->bias is the caller's).
+int check_epilogue(const hq_epilogue* e, int64_t T, int64_t d_out, int y_dtype, void* Y,
+                   hq::LinEpi* ep) {
+  const size_t es = dtype_size(y_dtype), ny = size_t(T) * size_t(d_out) * es;
+  ep->Y = Y;
+  ep->y_bf16 = y_dtype == HQ_BF16;
+  ep->gate_rows = 1;
+  ep->act = hq::act_coef(hq::ACT_NONE);
+  if (!e) return HQ_OK;
+  if (e->act < HQ_ACT_NONE || e->act > HQ_ACT_GELU_TANH)
+    return fail(HQ_ERR_INVALID_ARG, "epilogue act %d is not an hq_act", e->act);
+  if (misaligned(e->residual) || misaligned(e->gate))
+    return fail(HQ_ERR_INVALID_ARG, "residual and gate must be 16-byte aligned");
+  if (e->gate) {
+    if (e->gate_rows < 1)
+      return fail(HQ_ERR_INVALID_ARG, "gate_rows must be >= 1 with a gate (got %lld)",
+                  (long long)e->gate_rows);
+    if (e->gate_ld < d_out || e->gate_ld % 8)
+      return fail(HQ_ERR_INVALID_ARG,
+                  "gate_ld must be a multiple of 8 and at least d_out (got %lld, d_out %lld)",
+                  (long long)e->gate_ld, (long long)d_out);
+    ep->gate = e->gate;
+    ep->gate_rows = e->gate_rows < T ? e->gate_rows : T;
+    ep->gate_ld = e->gate_ld;
+    const size_t rows = size_t((T - 1) / ep->gate_rows);
+    if (overlap(e->gate, (rows * size_t(e->gate_ld) + size_t(d_out)) * es, Y, ny))
+      return fail(HQ_ERR_INVALID_ARG, "gate overlaps Y");
+  }
+  if (e->residual && e->residual != Y && overlap(e->residual, ny, Y, ny))
+    return fail(HQ_ERR_INVALID_ARG, "residual overlaps Y (it may be Y itself)");
+  ep->residual = e->residual;
+  ep->act = hq::act_coef(e->act);
+  return HQ_OK;
+}
+
+int check_rows(int64_t T) {
+  if (T < 0) return fail(HQ_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > kMaxRows)
+    return fail(HQ_ERR_UNSUPPORTED, "T must be at most %lld (got %lld)", (long long)kMaxRows,
+                (long long)T);
+  return HQ_OK;
+}
+
 // ---- integer-only DH / WH layers ---------------------------------------------
 
 constexpr uint32_t kMagicInt = 0x31495148u;  // "HQI1"
@@ -772,6 +854,48 @@ int hq_gemm_dequant(const hq_desc* desc, const void* prepared, const void* codes
     return fail(HQ_ERR_INVALID_ARG, "Y, codes, s_x, mu, U and prepared must be 16-byte aligned");
   return run_gemm_dequant(desc, prepared, codes, s_x, mu, U, T, Y,
                           static_cast<hipStream_t>(stream));
+}
+
+int hq_linear_validate(const hq_linear_desc* desc) {
+  g_err.clear();
+  return check_linear_desc(desc);
+}
+
+size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T) {
+  g_err.clear();
+  if (check_linear_desc(desc) != HQ_OK || check_rows(T) != HQ_OK) return 0;
+  return align256(hq::linear_part_bytes(T, desc->d_out, desc->d_in, int(dtype_size(desc->x_dtype))));
+}
+
+int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,
+              int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  int st = check_linear_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
+  if (st != HQ_OK) return st;
+  if (T == 0) return HQ_OK;
+  if (!X || !weight || !Y) return fail(HQ_ERR_INVALID_ARG, "X, weight and Y must be non-NULL");
+  if (misaligned(X) || misaligned(weight) || misaligned(bias) || misaligned(Y) ||
+      misaligned(workspace))
+    return fail(HQ_ERR_INVALID_ARG, "X, weight, bias, Y and workspace must be 16-byte aligned");
+  const size_t es = dtype_size(desc->x_dtype), din = size_t(desc->d_in), dout = size_t(desc->d_out);
+  const size_t ny = size_t(T) * dout * dtype_size(desc->y_dtype);
+  if (overlap(X, size_t(T) * din * es, Y, ny) || overlap(weight, din * dout * es, Y, ny) ||
+      overlap(bias, 4 * dout, Y, ny))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps an input");
+  hq::LinEpi ep = {};
+  st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &ep);
+  if (st != HQ_OK) return st;
+  ep.bias = bias;
+  const size_t need = align256(hq::linear_part_bytes(T, desc->d_out, desc->d_in, int(es)));
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
+                workspace ? workspace_bytes : size_t(0), need);
+  const hipError_t e =
+      hq::launch_linear(X, desc->x_dtype == HQ_BF16, T, weight, desc->d_out, desc->d_in,
+                        need ? workspace : nullptr, ep, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HQ_OK : hip_fail(e, "linear kernel launch");
 }
 
 int hq_int_validate(const hq_int_desc* desc) {

@@ -1,0 +1,117 @@
+// Epilogue of a linear layer beyond its bias: y = r + g phi(v), shared by the
+// dense and the quantised products and (phi alone) by the group norm.
+//   v  the product with its bias, in fp32
+//   phi identity, ReLU max(x, 0), SiLU x / (1 + e^-x), GELU x Phi(x) (Gaussian
+//      CDF) or its tanh form x / (1 + e^-2u), u = sqrt(2/pi) (x + 0.044715 x^3)
+//   g  one row of [*, N] per gate_rows rows of the output (absent: 1)
+//   r  the residual [M, N] (absent: 0)
+// Everything is computed in fp32 and rounded once, when y is stored.
+#pragma once
+
+#include "hq_device.h"
+#include "hq_gemm_types.h"
+
+namespace hq {
+
+__device__ __forceinline__ float relu_f32(float x) { return x < 0.0f ? 0.0f : x; }  // keeps NaN
+
+// phi for a bf16 result. SiLU, GELU and its tanh form are all x / (1 + 2^(-x P(x^2))):
+// P is the constant log2(e) for SiLU, linear for the tanh form, and for GELU
+// the degree-6 fit of log2(Phi(x) / Phi(-x)) / x on |x| <= 5 (relative error
+// of phi at most 1.1e-4 there: 1/37 of a bf16 half step; beyond, x^2 is held
+// at 25 and phi differs from x or 0 by less than 1.5e-5 in absolute value).
+// One exp2 and one reciprocal per value, no branch between the three.
+__device__ __forceinline__ float act_fast(float x, const ActCoef& a) {
+  const float t = fminf(x * x, a.tmax);
+  float p = a.c[6];
+#pragma unroll
+  for (int k = 5; k >= 0; --k) p = fmaf(p, t, a.c[k]);
+  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-(x * p)));
+}
+
+// phi for an fp32 result: the library functions (a few ulp).
+__device__ __forceinline__ float act_full(float x, int act) {
+  if (act == ACT_SILU) return x / (1.0f + expf(-x));
+  if (act == ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+  const float u = 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);  // 2 sqrt(2/pi) (...)
+  return x / (1.0f + expf(-u));
+}
+
+// phi on N values; FULL: fp32 result. `act` is uniform over the launch.
+template <int N, bool FULL>
+__device__ __forceinline__ void apply_act(float (&v)[N], const ActCoef& a) {
+  if (a.act == ACT_NONE) return;
+  if (a.act == ACT_RELU) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = relu_f32(v[k]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = FULL ? act_full(v[k], a.act) : act_fast(v[k], a);
+}
+
+__device__ __forceinline__ void store8(float* __restrict__ p, const float v[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(uint16_t* __restrict__ p, const float v[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Eight consecutive outputs n .. n+7 (n a multiple of 8) of row m, from the
+// product v: bias, phi, gate, residual, one rounding, one 16- or 32-byte
+// store. The residual is read right before the store by the lane that writes
+// the same elements, so Y may be the residual's own buffer.
+template <typename TY>
+__device__ __forceinline__ void finish8_as(float (&v)[8], int64_t m, int64_t n, int64_t N,
+                                           const LinEpi& ep) {
+  if (ep.bias) {
+    float b[8];
+    load8(ep.bias + n, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += b[k];
+  }
+  apply_act<8, sizeof(TY) == 4>(v, ep.act);
+  if (ep.gate) {
+    float g[8];
+    load8(static_cast<const TY*>(ep.gate) + int64_t(uint32_t(m) / uint32_t(ep.gate_rows)) * ep.gate_ld + n, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= g[k];
+  }
+  if (ep.residual) {
+    float r[8];
+    load8(static_cast<const TY*>(ep.residual) + m * N + n, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += r[k];
+  }
+  store8(static_cast<TY*>(ep.Y) + m * N + n, v);
+}
+
+__device__ __forceinline__ void finish8(float (&v)[8], int64_t m, int64_t n, int64_t N,
+                                        const LinEpi& ep) {
+  if (ep.y_bf16) finish8_as<uint16_t>(v, m, n, N, ep);
+  else finish8_as<float>(v, m, n, N, ep);
+}
+
+// One output, the same steps.
+template <typename TY>
+__device__ __forceinline__ void finish1_as(float v, int64_t m, int64_t n, int64_t N,
+                                           const LinEpi& ep) {
+  auto val = [](const void* p, int64_t i) -> float {
+    if constexpr (sizeof(TY) == 4) return static_cast<const float*>(p)[i];
+    else return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  };
+  float a[1] = {v + (ep.bias ? ep.bias[n] : 0.0f)};
+  apply_act<1, sizeof(TY) == 4>(a, ep.act);
+  if (ep.gate) a[0] *= val(ep.gate, (m / ep.gate_rows) * ep.gate_ld + n);
+  if (ep.residual) a[0] += val(ep.residual, m * N + n);
+  if constexpr (sizeof(TY) == 4) static_cast<float*>(ep.Y)[m * N + n] = a[0];
+  else static_cast<uint16_t*>(ep.Y)[m * N + n] = f32_to_bf16(a[0]);
+}
+__device__ __forceinline__ void finish1(float v, int64_t m, int64_t n, int64_t N, const LinEpi& ep) {
+  if (ep.y_bf16) finish1_as<uint16_t>(v, m, n, N, ep);
+  else finish1_as<float>(v, m, n, N, ep);
+}
+
+}  // namespace hq

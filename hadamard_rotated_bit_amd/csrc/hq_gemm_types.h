@@ -31,4 +31,29 @@ struct GemmEpi {
   int prescaled;          // accumulators already carry s_x s_w (group-wise GEMM)
 };
 
+// Activations (the C ABI's hq_act).
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
+
+// An activation as its kernels take it: the kind and, for SiLU and the two
+// GELU forms, the polynomial P(t) = sum c_k t^k of phi(x) = x / (1 + 2^(-x P(x^2))),
+// t held at tmax (act_fast, hq_epilogue.h).
+struct ActCoef {
+  int act;
+  float tmax;
+  float c[7];
+};
+
+// Epilogue of the dense product: y = residual + gate phi(acc + bias).
+// residual [M, N], gate [*, gate_ld] (row m / gate_rows), Y [M, N].
+struct LinEpi {
+  const float* bias;      // [N] or NULL
+  const void* residual;   // or NULL
+  const void* gate;       // or NULL
+  int64_t gate_rows;      // >= 1 where gate is given, below 2^31
+  int64_t gate_ld;
+  void* Y;
+  int y_bf16;             // type of Y, residual and gate
+  ActCoef act;
+};
+
 }  // namespace hq

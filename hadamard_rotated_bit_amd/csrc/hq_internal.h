@@ -138,6 +138,15 @@ hipError_t launch_gemm_f6g(const uint8_t* A, int64_t M, const uint8_t* B, int64_
 hipError_t launch_gemm_f6(const uint8_t* A, int64_t M, const uint8_t* B, int64_t N, int K,
                           int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s);
 
+// Dense linear layer: Y = residual + gate phi(X W^T + bias), X [M, K] and
+// W [N, K] both bf16 or both fp32 (N, K multiples of 8). linear_part_bytes:
+// the partial sums of a product split over K (0: not split), given as `part`.
+size_t linear_part_bytes(int64_t M, int64_t N, int K, int esize);
+hipError_t launch_linear(const void* X, int bf16, int64_t M, const void* W, int64_t N, int K,
+                         void* part, const LinEpi& ep, hipStream_t s);
+// The activation `act` (hq_act) as the kernels take it.
+ActCoef act_coef(int act);
+
 // Integer-only DH / WH layers with integer requantisation.
 constexpr int WH_MAX_BLOCK = 256;       // largest output-side Hadamard order
 constexpr int WH_SHIFT_MAX = 48;        // largest shared requantisation shift

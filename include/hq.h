@@ -261,6 +261,72 @@ int hq_quant_linear(const hq_desc* desc, const void* prepared, const void* X, in
 int hq_quant_linear_noalloc(const hq_desc* desc, const void* prepared, const void* X,
                             int64_t T, void* Y, void* stream);
 
+/* ---- Epilogues and dense layers ----
+ *
+ * What a network runs around its low-bit layers: an activation behind a
+ * layer, a gate per sample and the residual stream it adds to, and the layers
+ * that stay in 16 or 32 bits (embedders, modulation tables, first and last
+ * layers, 1x1 convolutions):
+ *
+ *     Y[t, j] = R[t, j] + g[t / gate_rows, j] phi(V[t, j])
+ *
+ * with V the layer's output (with its bias), phi an hq_act, R the residual
+ * (absent: 0) and g the gate (absent: 1). V, phi, the gate and the sum are
+ * fp32; Y is rounded once. phi is computed to a few fp32 ulp for fp32 Y; for
+ * bf16 Y to a relative 1.1e-4 (GELU) or better, a small part of the rounding
+ * to bf16. NaN goes through every activation; infinities follow the formulas
+ * (SiLU and GELU of -inf are NaN, the product -inf * 0). */
+typedef enum {
+  HQ_ACT_NONE = 0,
+  HQ_ACT_RELU = 1,      /* max(x, 0)                                           */
+  HQ_ACT_SILU = 2,      /* x / (1 + e^-x)                                      */
+  HQ_ACT_GELU = 3,      /* x Phi(x), Phi the Gaussian CDF                      */
+  HQ_ACT_GELU_TANH = 4  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2     */
+} hq_act;
+
+/* Epilogue of one call (host struct, device pointers; read during the call
+ * only). A NULL epilogue is all absent.
+ *  act        hq_act.
+ *  residual   [T, d_out] in the output's type, or NULL. It may be Y itself
+ *             (the residual stream updated in place); any other overlap with
+ *             Y is rejected.
+ *  gate       [ceil(T / gate_rows), d_out] in the output's type with a row
+ *             pitch of gate_ld elements (a multiple of 8, >= d_out: one part
+ *             of a modulation table can be given in place), or NULL.
+ *  gate_rows  rows of Y per gate row, >= 1 (ignored without a gate). */
+typedef struct {
+  int32_t act;
+  const void* residual;
+  const void* gate;
+  int64_t gate_rows, gate_ld;
+} hq_epilogue;
+
+/* Dense layer descriptor: d_in and d_out multiples of 8 up to 65536; x_dtype
+ * (X) and w_dtype (weight) the same hq_dtype; y_dtype (Y, residual, gate) any. */
+typedef struct {
+  int32_t d_in, d_out, x_dtype, w_dtype, y_dtype;
+} hq_linear_desc;
+
+/* Bookkeeping, host-only: check a dense-layer descriptor. */
+int hq_linear_validate(const hq_linear_desc* desc);
+
+/* Bookkeeping, host-only: workspace bytes hq_linear needs for T rows (0 for
+ * most shapes: only products of few tiles are split over d_in); 0 if invalid. */
+size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T);
+
+/* The layer before quantisation, Y = X W + b of HadaNorm Eq. (1), for the
+ * layers that are not quantised: V = X weight^T + bias on the bf16 or fp32
+ * MFMA with fp32 accumulation, then the epilogue above.
+ *  X [T, d_in] x_dtype, weight [d_out, d_in] w_dtype, Y [T, d_out] y_dtype, all
+ *  row-major; bias f32 [d_out] or NULL (none); epilogue NULL or as above;
+ *  workspace at least hq_linear_workspace_bytes(desc, T) bytes (NULL when that
+ *  is 0), not shared with a concurrent call. T up to 2^26; T = 0 is a no-op.
+ *  Y must not overlap X, weight, bias or the gate. The same inputs always give
+ *  the same bits (sums have a fixed order for a given shape). */
+int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,
+              int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
+              size_t workspace_bytes, void* stream);
+
 /* ---- Stage entry points (the same kernels, for testing and profiling) ---- */
 
 /* Per-channel centring statistics (center = 2 only; T >= 1), the per-channel
