@@ -482,6 +482,66 @@ def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
     return out
 
 
+@dataclasses.dataclass(frozen=True)
+class NormDesc:
+    """Group-norm descriptor; mirrors hq_norm_desc."""
+    channels: int
+    groups: int
+    eps: float = 1e-5
+    act: int = HQ_ACT_NONE
+    x_dtype: int = F32
+    y_dtype: int = F32
+
+    def __post_init__(self):
+        raw = _lib.HqNormDesc(self.channels, self.groups, self.act, self.x_dtype, self.y_dtype,
+                              self.eps)
+        object.__setattr__(self, "_raw", raw)
+        object.__setattr__(self, "_ref", ctypes.byref(raw))
+
+
+def group_norm_workspace_bytes(desc: NormDesc, samples: int, positions: int) -> int:
+    """Workspace bytes of group_norm (0 where one launch does it)."""
+    n = load().hq_group_norm_workspace_bytes(desc._ref, samples, positions)
+    if n == 0:
+        check(load().hq_norm_validate(desc._ref))
+        if samples < 0 or positions < 0:
+            raise HqError(_lib.HQ_ERR_INVALID_ARG, "samples and positions must be >= 0")
+    return n
+
+
+def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+               beta: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """phi(group norm) of channels-last X [samples, positions, channels]
+    (hq_group_norm). ``out`` may be X itself when the types are the same;
+    ``workspace`` (group_norm_workspace_bytes bytes) is allocated when it is
+    needed and not given."""
+    if X.dim() != 3:
+        raise ValueError(f"X must be [samples, positions, channels], got {tuple(X.shape)}")
+    S, P = X.shape[0], X.shape[1]
+    _need(X, "X", _TORCH[desc.x_dtype], (S, P, desc.channels))
+    if gamma is not None:
+        _need(gamma, "gamma", torch.float32, (desc.channels,))
+    if beta is not None:
+        _need(beta, "beta", torch.float32, (desc.channels,))
+    ydt = _TORCH[desc.y_dtype]
+    if out is None:
+        out = torch.empty(S, P, desc.channels, dtype=ydt, device=X.device)
+    else:
+        _need(out, "out", ydt, (S, P, desc.channels))
+    _same_device(X, gamma=gamma, beta=beta, out=out, workspace=workspace)
+    lib = load()
+    if workspace is None:
+        n = lib.hq_group_norm_workspace_bytes(desc._ref, S, P)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+    with _on(X.device) as stream:
+        check(lib.hq_group_norm(desc._ref, _ptr(X), _ptr(gamma), _ptr(beta), S, P, _ptr(out),
+                                _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                                stream))
+    return out
+
+
 # ---- integer-only DH / WH layers with integer requantisation ---------------
 
 @dataclasses.dataclass(frozen=True)

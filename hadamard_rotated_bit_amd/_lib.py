@@ -45,6 +45,11 @@ class HqLinearDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ["d_in", "d_out", "x_dtype", "w_dtype", "y_dtype"]]
 
 
+class HqNormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ["channels", "groups", "act", "x_dtype", "y_dtype"]] + [("eps", ctypes.c_float)]
+
+
 HQ_CODES_I8, HQ_CODES_E2M3 = 0, 1
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_I8 = 0, 1
@@ -60,6 +65,7 @@ _D = ctypes.POINTER(HqDesc)
 _W = ctypes.POINTER(HqIntDesc)
 _E = ctypes.POINTER(HqEpilogue)
 _L = ctypes.POINTER(HqLinearDesc)
+_N = ctypes.POINTER(HqNormDesc)
 _I64 = ctypes.c_int64
 _SIGS = {
     "hq_abi_version": (ctypes.c_int, []),
@@ -80,6 +86,9 @@ _SIGS = {
     "hq_linear_validate": (ctypes.c_int, [_L]),
     "hq_linear_workspace_bytes": (ctypes.c_size_t, [_L, _I64]),
     "hq_linear": (ctypes.c_int, [_L, _P, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
+    "hq_norm_validate": (ctypes.c_int, [_N]),
+    "hq_group_norm_workspace_bytes": (ctypes.c_size_t, [_N, _I64, _I64]),
+    "hq_group_norm": (ctypes.c_int, [_N, _P, _P, _P, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
     "hq_channel_center": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     "hq_act_quantize": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P]),
     "hq_act_quantize_ws": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P,

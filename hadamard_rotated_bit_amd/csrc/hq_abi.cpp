@@ -369,6 +369,36 @@ int check_rows(int64_t T) {
   return HQ_OK;
 }
 
+int check_norm_desc(const hq_norm_desc* d) {
+  if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
+  if (d->channels <= 0 || d->groups <= 0)
+    return fail(HQ_ERR_INVALID_ARG, "channels and groups must be positive (got %d, %d)",
+                d->channels, d->groups);
+  int st = check_dtype(d->x_dtype, "x_dtype");
+  if (st == HQ_OK) st = check_dtype(d->y_dtype, "y_dtype");
+  if (st != HQ_OK) return st;
+  if (d->act < HQ_ACT_NONE || d->act > HQ_ACT_GELU_TANH)
+    return fail(HQ_ERR_INVALID_ARG, "act %d is not an hq_act", d->act);
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps))
+    return fail(HQ_ERR_INVALID_ARG, "eps must be finite and >= 0 (got %g)", double(d->eps));
+  if (d->channels % 8 || d->channels > hq::NORM_MAX_C)
+    return fail(HQ_ERR_UNSUPPORTED, "channels must be a multiple of 8 up to %d (got %d)",
+                hq::NORM_MAX_C, d->channels);
+  if (d->channels % d->groups)
+    return fail(HQ_ERR_UNSUPPORTED, "groups %d must divide channels %d", d->groups, d->channels);
+  return HQ_OK;
+}
+
+int check_positions(int64_t S, int64_t P) {
+  if (S < 0 || P < 0)
+    return fail(HQ_ERR_INVALID_ARG, "samples and positions must be >= 0 (got %lld, %lld)",
+                (long long)S, (long long)P);
+  if (S > kMaxRows || P > kMaxRows || (P > 0 && S > kMaxRows / P))
+    return fail(HQ_ERR_UNSUPPORTED, "samples x positions must be at most %lld (got %lld x %lld)",
+                (long long)kMaxRows, (long long)S, (long long)P);
+  return HQ_OK;
+}
+
 // ---- integer-only DH / WH layers ---------------------------------------------
 
 constexpr uint32_t kMagicInt = 0x31495148u;  // "HQI1"
@@ -896,6 +926,61 @@ int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, con
       hq::launch_linear(X, desc->x_dtype == HQ_BF16, T, weight, desc->d_out, desc->d_in,
                         need ? workspace : nullptr, ep, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? HQ_OK : hip_fail(e, "linear kernel launch");
+}
+
+int hq_norm_validate(const hq_norm_desc* desc) {
+  g_err.clear();
+  return check_norm_desc(desc);
+}
+
+size_t hq_group_norm_workspace_bytes(const hq_norm_desc* desc, int64_t samples,
+                                     int64_t positions) {
+  g_err.clear();
+  if (check_norm_desc(desc) != HQ_OK || check_positions(samples, positions) != HQ_OK) return 0;
+  return align256(hq::norm_part_bytes(samples, positions, desc->channels, desc->groups,
+                                      int(dtype_size(desc->x_dtype))));
+}
+
+int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, const float* beta,
+                  int64_t samples, int64_t positions, void* Y, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  int st = check_norm_desc(desc);
+  if (st == HQ_OK) st = check_positions(samples, positions);
+  if (st != HQ_OK) return st;
+  if (samples == 0 || positions == 0) return HQ_OK;
+  if (!X || !Y) return fail(HQ_ERR_INVALID_ARG, "X and Y must be non-NULL");
+  if (misaligned(X) || misaligned(Y) || misaligned(gamma) || misaligned(beta) ||
+      misaligned(workspace))
+    return fail(HQ_ERR_INVALID_ARG, "X, gamma, beta, Y and workspace must be 16-byte aligned");
+  const size_t n = size_t(samples) * size_t(positions) * size_t(desc->channels);
+  const size_t nx = n * dtype_size(desc->x_dtype), ny = n * dtype_size(desc->y_dtype);
+  const bool in_place = X == Y && desc->x_dtype == desc->y_dtype;
+  if (!in_place && overlap(X, nx, Y, ny))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps X (it may be X itself, in the same type)");
+  if (overlap(gamma, 4 * size_t(desc->channels), Y, ny) ||
+      overlap(beta, 4 * size_t(desc->channels), Y, ny))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps gamma or beta");
+  const size_t need = align256(hq::norm_part_bytes(samples, positions, desc->channels,
+                                                   desc->groups, int(dtype_size(desc->x_dtype))));
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
+                workspace ? workspace_bytes : size_t(0), need);
+  hq::NormArgs a = {};
+  a.x = X;
+  a.y = Y;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.P = positions;
+  a.C = desc->channels;
+  a.G = desc->groups;
+  a.eps = desc->eps;
+  a.x_bf16 = desc->x_dtype == HQ_BF16;
+  a.y_bf16 = desc->y_dtype == HQ_BF16;
+  a.act = hq::act_coef(desc->act);
+  a.part = need ? workspace : nullptr;
+  const hipError_t e = hq::launch_group_norm(a, samples, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HQ_OK : hip_fail(e, "group norm kernel launch");
 }
 
 int hq_int_validate(const hq_int_desc* desc) {

@@ -147,6 +147,25 @@ hipError_t launch_linear(const void* X, int bf16, int64_t M, const void* W, int6
 // The activation `act` (hq_act) as the kernels take it.
 ActCoef act_coef(int act);
 
+// Group norm of S samples [P, C] (channels last) with an activation. C a
+// multiple of 8 up to NORM_MAX_C, G dividing C. norm_part_bytes: the partial
+// statistics of the two-launch form (0: one launch), given as `part`.
+constexpr int NORM_MAX_C = 4096;
+struct NormArgs {
+  const void* x;
+  void* y;
+  const float* gamma;
+  const float* beta;
+  int64_t P;
+  int C, G;
+  float eps;
+  int x_bf16, y_bf16;
+  ActCoef act;
+  void* part;
+};
+size_t norm_part_bytes(int64_t S, int64_t P, int C, int G, int esize);
+hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s);
+
 // Integer-only DH / WH layers with integer requantisation.
 constexpr int WH_MAX_BLOCK = 256;       // largest output-side Hadamard order
 constexpr int WH_SHIFT_MAX = 48;        // largest shared requantisation shift

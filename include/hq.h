@@ -327,6 +327,42 @@ int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, con
               int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
               size_t workspace_bytes, void* stream);
 
+/* Group norm descriptor: channels a multiple of 8 up to 4096; groups dividing
+ * it (any width: channels / groups need not be a multiple of 8); act an
+ * hq_act; x_dtype and y_dtype any hq_dtype; eps >= 0. */
+typedef struct {
+  int32_t channels, groups, act, x_dtype, y_dtype;
+  float eps;
+} hq_norm_desc;
+
+/* Bookkeeping, host-only: check a group norm descriptor. */
+int hq_norm_validate(const hq_norm_desc* desc);
+
+/* Bookkeeping, host-only: workspace bytes hq_group_norm needs (0 where one
+ * launch does it); 0 if invalid. */
+size_t hq_group_norm_workspace_bytes(const hq_norm_desc* desc, int64_t samples,
+                                     int64_t positions);
+
+/* Group norm over channels-last data with an activation behind it (Wu and He,
+ * "Group Normalization", Eq. (1), (2), (6) and (7), groups of consecutive
+ * channels; what stands before a 1x1 convolution or a denoiser's linear
+ * layer):
+ *   Y = phi(gamma_c (X - mean) / sqrt(var + eps) + beta_c),
+ * mean and biased variance over the positions and the channels / groups
+ * channels of each sample and group, in fp32 without differences of large
+ * sums. groups = 1 with positions = 1 is layer norm over the channels;
+ * groups = channels is instance norm.
+ *  X [samples, positions, channels] x_dtype, Y the same shape in y_dtype, both
+ *  row-major (a token matrix [T, d] is samples x positions = T rows); gamma,
+ *  beta f32 [channels] or NULL (ones, zeros). Y may be X itself when the types
+ *  are the same. workspace at least hq_group_norm_workspace_bytes bytes (NULL
+ *  when that is 0), not shared with a concurrent call. samples x positions up
+ *  to 2^26; 0 of either is a no-op. A sample's NaN or infinity stays in its
+ *  own sample and group. The same inputs always give the same bits. */
+int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, const float* beta,
+                  int64_t samples, int64_t positions, void* Y, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* ---- Stage entry points (the same kernels, for testing and profiling) ---- */
 
 /* Per-channel centring statistics (center = 2 only; T >= 1), the per-channel
