@@ -184,10 +184,14 @@ def check_prepared(desc: Desc, prepared: torch.Tensor) -> None:
 
 def quant_linear(desc: Desc, prepared: torch.Tensor, X: torch.Tensor,
                  out: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Y = the quantised layer applied to X [T, d_in]."""
+                 workspace: Optional[torch.Tensor] = None,
+                 epilogue: Optional["Epilogue"] = None) -> torch.Tensor:
+    """Y = the quantised layer applied to X [T, d_in]; with ``epilogue``
+    (hq_quant_linear_epi) Y = residual + gate * phi(layer(X))."""
     T = X.shape[0]
     _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
+    if epilogue is not None:
+        return _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue)
     if out is None:
         out = torch.empty(T, desc.d_out, dtype=_TORCH[desc.y_dtype], device=X.device)
     else:
@@ -423,6 +427,24 @@ class Epilogue:
         return ctypes.byref(_lib.HqEpilogue(self.act, r.data_ptr() if r is not None else None,
                                             g.data_ptr() if g is not None else None,
                                             self.gate_rows, ld))
+
+
+def _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue):
+    ydt = _TORCH[desc.y_dtype]
+    if out is None:
+        out = torch.empty(T, desc.d_out, dtype=ydt, device=X.device)
+    else:
+        _need(out, "out", ydt, (T, desc.d_out))
+    _same_device(X, prepared=prepared, out=out, workspace=workspace)
+    ep = epilogue._c(X, T, desc.d_out, ydt)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(lib.hq_workspace_bytes(desc._ref, T), 1), dtype=torch.uint8,
+                                device=X.device)
+    with _on(X.device) as stream:
+        check(lib.hq_quant_linear_epi(desc._ref, _ptr(prepared), _ptr(X), T, ep, _ptr(out),
+                                      _ptr(workspace), workspace.nbytes, stream))
+    return out
 
 
 @dataclasses.dataclass(frozen=True)

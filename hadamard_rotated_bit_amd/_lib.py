@@ -83,6 +83,7 @@ _SIGS = {
     "hq_check_prepared": (ctypes.c_int, [_D, _P, _P]),
     "hq_quant_linear": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
     "hq_quant_linear_noalloc": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P]),
+    "hq_quant_linear_epi": (ctypes.c_int, [_D, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
     "hq_linear_validate": (ctypes.c_int, [_L]),
     "hq_linear_workspace_bytes": (ctypes.c_size_t, [_L, _I64]),
     "hq_linear": (ctypes.c_int, [_L, _P, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),

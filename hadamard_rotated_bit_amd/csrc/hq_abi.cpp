@@ -258,7 +258,7 @@ hipError_t launch_codes_gemm(const hq_desc* d, const void* a_codes, int64_t T, c
 // the per-token term vanishes (s_x stands in for the per-token vector).
 int run_gemm_dequant(const hq_desc* d, const void* prepared, const void* codes,
                      const float* s_x, const float* mu, const float* U, int64_t T, void* Y,
-                     hipStream_t s) {
+                     hipStream_t s, const hq::LinEpi* lin = nullptr) {
   hq_prepared_layout L;
   layout_of(d, &L);
   const bool chan = d->center == HQ_CENTER_CHANNEL;
@@ -277,6 +277,10 @@ int run_gemm_dequant(const hq_desc* d, const void* prepared, const void* codes,
   ep.Y = Y;
   ep.y_bf16 = d->y_dtype == HQ_BF16;
   ep.ldy = d->d_out;
+  if (lin) {
+    ep.ext = 1;
+    ep.lin = *lin;
+  }
   hipError_t e =
       d->group ? hq::launch_gemm_f6g(static_cast<const uint8_t*>(codes), T,
                                      at<uint8_t>(prepared, L.w_codes), d->d_out, d->d_in, s_x, T,
@@ -397,6 +401,40 @@ int check_positions(int64_t S, int64_t P) {
     return fail(HQ_ERR_UNSUPPORTED, "samples x positions must be at most %lld (got %lld x %lld)",
                 (long long)kMaxRows, (long long)S, (long long)P);
   return HQ_OK;
+}
+
+// The hot path, with the extended epilogue where `lin` is given.
+int run_quant_linear(const hq_desc* desc, const void* prepared, const void* X, int64_t T,
+                     const hq::LinEpi* lin, void* Y, void* workspace, size_t workspace_bytes,
+                     hipStream_t s) {
+  int st = check_desc(desc);
+  if (st != HQ_OK) return st;
+  if (T < 0) return fail(HQ_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
+  if (T == 0) return HQ_OK;
+  if (!prepared || !X || !Y || !workspace)
+    return fail(HQ_ERR_INVALID_ARG, "prepared, X, Y and workspace must be non-NULL");
+  if (misaligned(X) || misaligned(Y) || misaligned(workspace) || misaligned(prepared))
+    return fail(HQ_ERR_INVALID_ARG, "X, Y, workspace and prepared must be 16-byte aligned");
+  const Workspace w = workspace_of(desc, T);
+  if (workspace_bytes < w.total)
+    return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, w.total);
+  void* codes = at<uint8_t>(workspace, w.codes);
+  float* s_x = at<float>(workspace, w.s_x);
+  float* mu = at<float>(workspace, w.mu);
+  float* U = desc->rank ? at<float>(workspace, w.U) : nullptr;
+  float* lr_part = w.lr_part ? at<float>(workspace, w.lr_part) : nullptr;
+  if (desc->center == HQ_CENTER_CHANNEL) {
+    float* cmean = at<float>(workspace, w.mean);
+    float* bias_eff = at<float>(workspace, w.bias_eff);
+    st = run_center(desc, prepared, X, T, at<float>(workspace, w.partial), cmean, bias_eff, s);
+    if (st == HQ_OK)
+      st = run_act(desc, prepared, X, T, codes, s_x, nullptr, cmean, U, s, lr_part);
+    if (st != HQ_OK) return st;
+    return run_gemm_dequant(desc, prepared, codes, s_x, bias_eff, U, T, Y, s, lin);
+  }
+  st = run_act(desc, prepared, X, T, codes, s_x, mu, nullptr, U, s, lr_part);
+  if (st != HQ_OK) return st;
+  return run_gemm_dequant(desc, prepared, codes, s_x, mu, U, T, Y, s, lin);
 }
 
 // ---- integer-only DH / WH layers ---------------------------------------------
@@ -731,35 +769,29 @@ int hq_check_prepared(const hq_desc* desc, const void* prepared, void* stream) {
 int hq_quant_linear(const hq_desc* desc, const void* prepared, const void* X, int64_t T, void* Y,
                     void* workspace, size_t workspace_bytes, void* stream) {
   g_err.clear();
+  return run_quant_linear(desc, prepared, X, T, nullptr, Y, workspace, workspace_bytes,
+                          static_cast<hipStream_t>(stream));
+}
+
+int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X, int64_t T,
+                        const hq_epilogue* epilogue, void* Y, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  g_err.clear();
   int st = check_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
   if (st != HQ_OK) return st;
-  if (T < 0) return fail(HQ_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return HQ_OK;
-  if (!prepared || !X || !Y || !workspace)
-    return fail(HQ_ERR_INVALID_ARG, "prepared, X, Y and workspace must be non-NULL");
-  if (misaligned(X) || misaligned(Y) || misaligned(workspace) || misaligned(prepared))
-    return fail(HQ_ERR_INVALID_ARG, "X, Y, workspace and prepared must be 16-byte aligned");
-  const Workspace w = workspace_of(desc, T);
-  if (workspace_bytes < w.total)
-    return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, w.total);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  void* codes = at<uint8_t>(workspace, w.codes);
-  float* s_x = at<float>(workspace, w.s_x);
-  float* mu = at<float>(workspace, w.mu);
-  float* U = desc->rank ? at<float>(workspace, w.U) : nullptr;
-  float* lr_part = w.lr_part ? at<float>(workspace, w.lr_part) : nullptr;
-  if (desc->center == HQ_CENTER_CHANNEL) {
-    float* cmean = at<float>(workspace, w.mean);
-    float* bias_eff = at<float>(workspace, w.bias_eff);
-    st = run_center(desc, prepared, X, T, at<float>(workspace, w.partial), cmean, bias_eff, s);
-    if (st == HQ_OK)
-      st = run_act(desc, prepared, X, T, codes, s_x, nullptr, cmean, U, s, lr_part);
-    if (st != HQ_OK) return st;
-    return run_gemm_dequant(desc, prepared, codes, s_x, bias_eff, U, T, Y, s);
-  }
-  st = run_act(desc, prepared, X, T, codes, s_x, mu, nullptr, U, s, lr_part);
+  if (!X || !Y) return fail(HQ_ERR_INVALID_ARG, "X and Y must be non-NULL");
+  if (overlap(X, size_t(T) * size_t(desc->d_in) * dtype_size(desc->x_dtype), Y,
+              size_t(T) * size_t(desc->d_out) * dtype_size(desc->y_dtype)))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps X");
+  hq::LinEpi lin = {};
+  st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &lin);
   if (st != HQ_OK) return st;
-  return run_gemm_dequant(desc, prepared, codes, s_x, mu, U, T, Y, s);
+  // an epilogue of nothing is hq_quant_linear's own
+  const bool any = lin.act.act != hq::ACT_NONE || lin.residual || lin.gate;
+  return run_quant_linear(desc, prepared, X, T, any ? &lin : nullptr, Y, workspace,
+                          workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 int hq_channel_center(const hq_desc* desc, const void* prepared, const void* X, int64_t T,

@@ -15,9 +15,9 @@ namespace hq {
 
 __device__ __forceinline__ float relu_f32(float x) { return x < 0.0f ? 0.0f : x; }  // keeps NaN
 
-// phi for a bf16 result. SiLU, GELU and its tanh form are all x / (1 + 2^(-x P(x^2))):
-// P is the constant log2(e) for SiLU, linear for the tanh form, and for GELU
-// the degree-6 fit of log2(Phi(x) / Phi(-x)) / x on |x| <= 5 (relative error
+// SiLU, GELU and its tanh form are all x / (1 + 2^(-x P(x^2))): P is the
+// constant log2(e) for SiLU and linear for the tanh form (fp32 accuracy), and
+// for GELU with a bf16 result the degree-6 fit of log2(Phi(x) / Phi(-x)) / x on |x| <= 5 (relative error
 // of phi at most 1.1e-4 there: 1/37 of a bf16 half step; beyond, x^2 is held
 // at 25 and phi differs from x or 0 by less than 1.5e-5 in absolute value).
 // One exp2 and one reciprocal per value, no branch between the three.
@@ -29,12 +29,27 @@ __device__ __forceinline__ float act_fast(float x, const ActCoef& a) {
   return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-(x * p)));
 }
 
-// phi for an fp32 result: the library functions (a few ulp).
-__device__ __forceinline__ float act_full(float x, int act) {
-  if (act == ACT_SILU) return x / (1.0f + expf(-x));
-  if (act == ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752f * x);
-  const float u = 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);  // 2 sqrt(2/pi) (...)
-  return x / (1.0f + expf(-u));
+// GELU for an fp32 result: max(x, 0) - |x| h(|x|), h(a) = Phi(-a) =
+// e^(-a^2/2) times a degree-10 fit in t = 1 / (1 + 0.4 a) (relative error
+// 1.4e-8); no difference of near-equal numbers for any x. a is held at 40,
+// where h is 0 in fp32, so that +-inf give inf and 0.
+__device__ __forceinline__ float gelu_full(float x) {
+  const float a = fminf(fabsf(x), 40.0f);
+  const float d = fmaf(0.4f, a, 1.0f);
+  float t = __builtin_amdgcn_rcpf(d);
+  t = fmaf(t, fmaf(-d, t, 1.0f), t);
+  float p = 0.031375720731075134f;
+  p = fmaf(p, t, -0.17226340215955868f);
+  p = fmaf(p, t, 0.3716291512061377f);
+  p = fmaf(p, t, -0.3598523486270329f);
+  p = fmaf(p, t, 0.1077760623043252f);
+  p = fmaf(p, t, -0.020622834591990737f);
+  p = fmaf(p, t, 0.08922175130220084f);
+  p = fmaf(p, t, 0.133581291732006f);
+  p = fmaf(p, t, 0.15957620720558505f);
+  p = fmaf(p, t, 0.15957840770412896f);
+  const float h = p * t * __builtin_amdgcn_exp2f(-0.72134752044448170f * a * a);
+  return fmaf(-a, h, relu_f32(x));
 }
 
 // phi on N values; FULL: fp32 result. `act` is uniform over the launch.
@@ -46,8 +61,13 @@ __device__ __forceinline__ void apply_act(float (&v)[N], const ActCoef& a) {
     for (int k = 0; k < N; ++k) v[k] = relu_f32(v[k]);
     return;
   }
+  if (FULL && a.act == ACT_GELU) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = FULL ? act_full(v[k], a.act) : act_fast(v[k], a);
+    for (int k = 0; k < N; ++k) v[k] = gelu_full(v[k]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = act_fast(v[k], a);
 }
 
 __device__ __forceinline__ void store8(float* __restrict__ p, const float v[8]) {
@@ -112,6 +132,41 @@ __device__ __forceinline__ void finish1_as(float v, int64_t m, int64_t n, int64_
 __device__ __forceinline__ void finish1(float v, int64_t m, int64_t n, int64_t N, const LinEpi& ep) {
   if (ep.y_bf16) finish1_as<uint16_t>(v, m, n, N, ep);
   else finish1_as<float>(v, m, n, N, ep);
+}
+
+// The same for the quantised GEMMs' epilogues, whose lanes hold runs of four
+// columns of one row: element offsets of row m (clamped into the output: rows
+// past M are computed and never stored) in the residual and the gate.
+struct ExtRow {
+  int64_t r, g;
+};
+__device__ __forceinline__ ExtRow ext_row(const GemmEpi& ep, int64_t m, int64_t M) {
+  const LinEpi& l = ep.lin;
+  const int64_t mc = m < M ? m : M - 1;
+  return ExtRow{mc * ep.ldy, l.gate ? int64_t(uint32_t(mc) / uint32_t(l.gate_rows)) * l.gate_ld : 0};
+}
+__device__ __forceinline__ void load4(const uint16_t* __restrict__ p, float v[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+// Columns n .. n+3 (clamped into the output like the row), bf16 Y.
+__device__ __forceinline__ void ext4(float (&y)[4], const LinEpi& ep, const ExtRow& row, int64_t n,
+                                     int64_t N) {
+  apply_act<4, false>(y, ep.act);
+  const int64_t nc = n < N ? n : N - 4;
+  if (ep.gate) {
+    float g[4];
+    load4(static_cast<const uint16_t*>(ep.gate) + row.g + nc, g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] *= g[k];
+  }
+  if (ep.residual) {
+    float r[4];
+    load4(static_cast<const uint16_t*>(ep.residual) + row.r + nc, r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] += r[k];
+  }
 }
 
 }  // namespace hq

@@ -33,8 +33,12 @@ static hipError_t launch_cfg(const int8_t* A, int64_t M, const int8_t* B, int64_
   GemmEpi ep = {};
   if (epi) {
     ep = *epi;
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC>), grid, block, 0, s,
-                       A, M, B, N, K, nullptr, 0, ep);
+    if (ep.ext)
+      hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC, true>), grid, block,
+                         0, s, A, M, B, N, K, nullptr, 0, ep);
+    else
+      hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC>), grid, block, 0, s,
+                         A, M, B, N, K, nullptr, 0, ep);
   } else {
     hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, false, OCC>), grid, block, 0, s,
                        A, M, B, N, K, acc_out, ldc, ep);
@@ -47,9 +51,13 @@ static hipError_t launch_i8_persist(const int8_t* A, int64_t M, const int8_t* B,
                                     const GemmEpi& ep, int cus, hipStream_t s) {
   const int64_t ntiles = ((M + 255) / 256) * ((N + 191) / 192);
   const unsigned grid = unsigned(ntiles < cus ? ntiles : cus);
-  hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR>), dim3(grid), dim3(256), 0, s,
-                     reinterpret_cast<const uint8_t*>(A), M, reinterpret_cast<const uint8_t*>(B),
-                     N, K, ep);
+  const uint8_t *a = reinterpret_cast<const uint8_t*>(A), *b = reinterpret_cast<const uint8_t*>(B);
+  if (ep.ext)
+    hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR, true>), dim3(grid), dim3(256), 0,
+                       s, a, M, b, N, K, ep);
+  else
+    hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR, false>), dim3(grid), dim3(256),
+                       0, s, a, M, b, N, K, ep);
   return hipGetLastError();
 }
 

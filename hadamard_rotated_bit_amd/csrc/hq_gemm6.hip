@@ -15,8 +15,12 @@ static hipError_t launch_f6_cfg(const uint8_t* A, int64_t M, const uint8_t* B, i
   GemmEpi ep = {};
   if (epi) {
     ep = *epi;
-    hipLaunchKernelGGL((gemm_f6_kernel<BM, BN, WM, WN, 3, 4, true, F6_GROUP>), grid, block, 0, s,
-                       A, M, B, N, K, nullptr, 0, ep);
+    if (ep.ext)
+      hipLaunchKernelGGL((gemm_f6_kernel<BM, BN, WM, WN, 3, 4, true, F6_GROUP, 1, true>), grid,
+                         block, 0, s, A, M, B, N, K, nullptr, 0, ep);
+    else
+      hipLaunchKernelGGL((gemm_f6_kernel<BM, BN, WM, WN, 3, 4, true, F6_GROUP>), grid, block, 0,
+                         s, A, M, B, N, K, nullptr, 0, ep);
   } else {
     hipLaunchKernelGGL((gemm_f6_kernel<BM, BN, WM, WN, 3, 4, false, F6_GROUP>), grid, block, 0, s,
                        A, M, B, N, K, acc_out, ldc, ep);
@@ -32,8 +36,12 @@ static hipError_t launch_f6_persist(const uint8_t* A, int64_t M, const uint8_t* 
                                     int K, const GemmEpi& ep, int cus, hipStream_t s) {
   const int64_t ntiles = ((M + 255) / 256) * ((N + 191) / 192);
   const unsigned grid = unsigned(ntiles < cus ? ntiles : cus);
-  hipLaunchKernelGGL((gemm_f6_persist<256, 192, 128, 96, 4, F6_GROUP, LR>), dim3(grid), dim3(256),
-                     0, s, A, M, B, N, K, ep);
+  if (ep.ext)
+    hipLaunchKernelGGL((gemm_f6_persist<256, 192, 128, 96, 4, F6_GROUP, LR, true>), dim3(grid),
+                       dim3(256), 0, s, A, M, B, N, K, ep);
+  else
+    hipLaunchKernelGGL((gemm_f6_persist<256, 192, 128, 96, 4, F6_GROUP, LR, false>), dim3(grid),
+                       dim3(256), 0, s, A, M, B, N, K, ep);
   return hipGetLastError();
 }
 

@@ -101,7 +101,7 @@ __device__ __forceinline__ void group_tiles(v16f (&acc)[TM][TN], const Frag6 (&a
   }
 }
 
-template <int BM, int BN, int WM, int WN, int GM, int RG, int S = 3, int OCC = 2>
+template <int BM, int BN, int WM, int WN, int GM, int RG, int S, int OCC, bool EXT>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_f6g_kernel(
     const uint8_t* __restrict__ A, int64_t M, const uint8_t* __restrict__ B, int64_t N, int K,
@@ -275,6 +275,10 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_f6g_kernel(
 #undef HG_READ
 #undef HG_ISSUE
 
+  if constexpr (EXT) {
+    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
+    return;
+  }
   if (ep.y_bf16) {
     // bf16 output staged through LDS (whole row segments per store). The
     // accumulators already carry both scales, so the staged parameter block
@@ -314,8 +318,14 @@ hipError_t launch_gemm_f6g(const uint8_t* A, int64_t M, const uint8_t* B, int64_
   const int64_t ntiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   GemmEpi ep = *epi;
   ep.prescaled = 1;
-  hipLaunchKernelGGL((gemm_f6g_kernel<BM, BN, 64, 64, 4, F6_GROUP, 2, 3>), dim3(unsigned(ntiles)),
-                     dim3(256), 0, s, A, M, B, N, K, ep, s_xg, ld_sx, s_wg, ld_sw);
+  if (ep.ext)
+    hipLaunchKernelGGL((gemm_f6g_kernel<BM, BN, 64, 64, 4, F6_GROUP, 2, 3, true>),
+                       dim3(unsigned(ntiles)), dim3(256), 0, s, A, M, B, N, K, ep, s_xg, ld_sx,
+                       s_wg, ld_sw);
+  else
+    hipLaunchKernelGGL((gemm_f6g_kernel<BM, BN, 64, 64, 4, F6_GROUP, 2, 3, false>),
+                       dim3(unsigned(ntiles)), dim3(256), 0, s, A, M, B, N, K, ep, s_xg, ld_sx,
+                       s_wg, ld_sw);
   return hipGetLastError();
 }
 

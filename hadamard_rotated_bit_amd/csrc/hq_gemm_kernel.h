@@ -3,6 +3,7 @@
 #pragma once
 
 #include "hq_device.h"
+#include "hq_epilogue.h"
 #include "hq_gemm_types.h"
 
 namespace hq {
@@ -164,6 +165,91 @@ __device__ __forceinline__ void gemm_epilogue(AccT (&acc)[TM][TN], uint8_t* smem
   }
 }
 
+// Dequant epilogue followed by Y = residual + gate phi(y) (hq_epilogue.h): the
+// values of gemm_epilogue, staged in fp32 per 32-row slice in a part of the
+// idle LDS that belongs to the wave and taken back as rows of eight columns
+// per lane, so that residual, gate and Y move in whole row segments and phi is
+// written once, in a rolled loop (unrolled over the accumulators its code
+// overflowed the registers). LDSB: bytes of LDS there are.
+template <int BM, int BN, int TM, int TN, int NW, int LDSB, typename AccT>
+__device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* smem, int tid,
+                                                  int lane, int64_t m0, int64_t n0, int wm0,
+                                                  int wn0, int64_t M, int64_t N,
+                                                  const GemmEpi& ep) {
+  constexpr int PB = 4 * (3 * BN + 2 * BM);
+  constexpr int PITCH = 32 * TN + 4;          // floats: a row and one 16-byte pad
+  static_assert(PB + NW * 32 * PITCH * 4 <= LDSB && PB % 16 == 0, "staging fits");
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  float* P = reinterpret_cast<float*>(smem);
+  float* const stg = reinterpret_cast<float*>(smem + PB) + (tid >> 6) * 32 * PITCH;
+  wait_vm_lgkm0<0>();
+  __builtin_amdgcn_s_barrier();
+  for (int idx = tid; idx < BN; idx += NW * 64) {
+    const int64_t nc = n0 + idx < N ? n0 + idx : N - 1;
+    P[idx] = ep.prescaled ? 1.0f : ep.s_w[nc];
+    P[BN + idx] = ep.c[nc];
+    P[2 * BN + idx] = ep.bias[nc];
+  }
+  for (int idx = tid; idx < BM; idx += NW * 64) {
+    const int64_t mc = m0 + idx < M ? m0 + idx : M - 1;
+    P[3 * BN + idx] = ep.prescaled ? 1.0f : ep.s_x[mc];
+    P[3 * BN + BM + idx] = ep.mu[mc];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int ml = wm0 + i * 32 + lrow;
+    const int64_t mc = m0 + ml < M ? m0 + ml : M - 1;
+    const float sx = P[3 * BN + ml], mu = P[3 * BN + BM + ml];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int64_t nb = n0 + wn0 + j * 32;
+      v16f lr = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k0 = 0; k0 < ep.rank; k0 += 16) {
+        float f[8];
+        load8(ep.U + mc * ep.rank + k0 + 8 * lhalf, f);
+        const v8bf uh = pack_bf16x8(f, false), ul = pack_bf16x8(f, true);
+        const int64_t nr = nb + lrow < N ? nb + lrow : N - 1;
+        const int64_t off = nr * ep.rank + k0 + 8 * lhalf;
+        const v8bf wh = *reinterpret_cast<const v8bf*>(ep.l2_hi + off);
+        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, uh, lr, 0, 0, 0);
+        if (!ep.l2_lo_zero) {
+          const v8bf wl = *reinterpret_cast<const v8bf*>(ep.l2_lo + off);
+          lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wl, uh, lr, 0, 0, 0);
+        }
+        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, ul, lr, 0, 0, 0);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int cl = j * 32 + 8 * g + 4 * lhalf;
+        const float4 sw = *reinterpret_cast<const float4*>(P + wn0 + cl);
+        const float4 cb = *reinterpret_cast<const float4*>(P + BN + wn0 + cl);
+        const float4 bb = *reinterpret_cast<const float4*>(P + 2 * BN + wn0 + cl);
+        const AccT& a = acc[i][j];
+        float4 y;
+        y.x = fmaf(float(a[4 * g + 0]), sx * sw.x, fmaf(mu, cb.x, bb.x)) + lr[4 * g + 0];
+        y.y = fmaf(float(a[4 * g + 1]), sx * sw.y, fmaf(mu, cb.y, bb.y)) + lr[4 * g + 1];
+        y.z = fmaf(float(a[4 * g + 2]), sx * sw.z, fmaf(mu, cb.z, bb.z)) + lr[4 * g + 2];
+        y.w = fmaf(float(a[4 * g + 3]), sx * sw.w, fmaf(mu, cb.w, bb.w)) + lr[4 * g + 3];
+        *reinterpret_cast<float4*>(stg + lrow * PITCH + cl) = y;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int LPR = 4 * TN;               // lanes per row
+#pragma unroll 1
+    for (int q = lane; q < 32 * LPR; q += 64) {
+      const int r = q / LPR, c = 8 * (q - r * LPR);
+      const int64_t m = m0 + wm0 + 32 * i + r, n = n0 + wn0 + c;
+      if (m < M && n < N) {
+        float v[8];
+        load8(stg + r * PITCH + c, v);
+        finish8(v, m, n, N, ep.lin);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // Dequant epilogue with bf16 output staged through LDS (same values as
 // gemm_epilogue), with the block's parameters already in LDS at P (laid out
 // as in gemm_epilogue, outside the first BM (2 BN + 8) bytes): each lane writes its 4-channel runs (8 bytes) into a
@@ -307,7 +393,8 @@ __device__ __forceinline__ void gemm_epilogue_bf16_staged(AccT (&acc)[TM][TN], u
 // OCC is the number of waves per SIMD the register allocation must allow
 // (OCC = 2 with 4-wave blocks keeps two blocks resident per CU, whose
 // independent barriers interleave on every SIMD).
-template <int BM, int BN, int BK, int WM, int WN, int S, int GM, bool DEQ, int OCC = 1>
+template <int BM, int BN, int BK, int WM, int WN, int S, int GM, bool DEQ, int OCC = 1,
+          bool EXT = false>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_i8_kernel(
     const int8_t* __restrict__ A, int64_t M, const int8_t* __restrict__ B, int64_t N, int K,
@@ -433,7 +520,10 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_i8_kernel(
 #undef HQ_WAIT_STAGE
 #undef HQ_ISSUE_STAGE
 
-  gemm_epilogue<BM, BN, TM, TN, NW, DEQ>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, Cout, ldc, ep);
+  if constexpr (EXT)
+    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
+  else
+    gemm_epilogue<BM, BN, TM, TN, NW, DEQ>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, Cout, ldc, ep);
 }
 
 }  // namespace hq

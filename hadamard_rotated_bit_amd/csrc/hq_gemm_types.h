@@ -11,26 +11,6 @@ namespace hq {
 // range) measured no faster than 4-row groups.
 constexpr int F6_GROUP = 4;
 
-// Dequant epilogue of the GEMMs: y = s_x s_w acc + b + mu c (+ U L2), stored
-// as bf16 or fp32 at Y with row pitch ldy.
-struct GemmEpi {
-  const float* s_x;       // [M]
-  const float* mu;        // [M]
-  const float* s_w;       // [N]
-  const float* c;         // [N]
-  const float* bias;      // [N]
-  const float* U;         // [M, rank] or NULL
-  const uint16_t* l2_hi;  // [N, rank]
-  const uint16_t* l2_lo;
-  int l2_lo_zero;         // l2_lo is all zero (L2 given in bf16 is its own hi
-                          // part): its products are skipped
-  int rank;
-  void* Y;                // [M, ldy]
-  int y_bf16;
-  int64_t ldy;
-  int prescaled;          // accumulators already carry s_x s_w (group-wise GEMM)
-};
-
 // Activations (the C ABI's hq_act).
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
@@ -54,6 +34,30 @@ struct LinEpi {
   void* Y;
   int y_bf16;             // type of Y, residual and gate
   ActCoef act;
+};
+
+// Dequant epilogue of the GEMMs: y = s_x s_w acc + b + mu c (+ U L2), stored
+// as bf16 or fp32 at Y with row pitch ldy.
+struct GemmEpi {
+  const float* s_x;       // [M]
+  const float* mu;        // [M]
+  const float* s_w;       // [N]
+  const float* c;         // [N]
+  const float* bias;      // [N]
+  const float* U;         // [M, rank] or NULL
+  const uint16_t* l2_hi;  // [N, rank]
+  const uint16_t* l2_lo;
+  int l2_lo_zero;         // l2_lo is all zero (L2 given in bf16 is its own hi
+                          // part): its products are skipped
+  int rank;
+  void* Y;                // [M, ldy]
+  int y_bf16;
+  int64_t ldy;
+  int prescaled;          // accumulators already carry s_x s_w (group-wise GEMM)
+  // Y = residual + gate phi(y), in the kernels instantiated for it (lin.bias
+  // is NULL and lin.Y = Y; ldy = N):
+  int ext;
+  LinEpi lin;
 };
 
 }  // namespace hq

@@ -385,7 +385,7 @@ hipError_t launch_linear(const void* X, int bf16, int64_t M, const void* W, int6
                       static_cast<float*>(part), ep, s);
 }
 
-// GELU: degree-6 weighted least-maximum fit of log2(Phi(x) / Phi(-x)) / x in
+// GELU (bf16 results): degree-6 weighted least-maximum fit of log2(Phi(x) / Phi(-x)) / x in
 // x^2 on |x| <= 5; the other two are exact forms.
 ActCoef act_coef(int act) {
   ActCoef a = {};
@@ -395,7 +395,7 @@ ActCoef act_coef(int act) {
     a.tmax = 0.0f;
     a.c[0] = log2e;
   } else if (act == ACT_GELU_TANH) {
-    a.tmax = 64.0f;
+    a.tmax = 1e6f;   // 2^(-x P) is 0 or infinite long before; keeps x^2 finite
     a.c[0] = 1.5957691216057308f * log2e;
     a.c[1] = 1.5957691216057308f * 0.044715f * log2e;
   } else if (act == ACT_GELU) {

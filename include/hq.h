@@ -274,8 +274,8 @@ int hq_quant_linear_noalloc(const hq_desc* desc, const void* prepared, const voi
  * (absent: 0) and g the gate (absent: 1). V, phi, the gate and the sum are
  * fp32; Y is rounded once. phi is computed to a few fp32 ulp for fp32 Y; for
  * bf16 Y to a relative 1.1e-4 (GELU) or better, a small part of the rounding
- * to bf16. NaN goes through every activation; infinities follow the formulas
- * (SiLU and GELU of -inf are NaN, the product -inf * 0). */
+ * to bf16. NaN goes through every activation, +inf stays +inf; -inf gives 0
+ * with ReLU and, where the formula reads -inf * 0, NaN or 0. */
 typedef enum {
   HQ_ACT_NONE = 0,
   HQ_ACT_RELU = 1,      /* max(x, 0)                                           */
@@ -300,6 +300,16 @@ typedef struct {
   const void* gate;
   int64_t gate_rows, gate_ld;
 } hq_epilogue;
+
+/* hq_quant_linear with an epilogue behind the layer: HadaNorm Eq. (1) as there
+ * (with its low-rank branch, scales and centring), V the dequantised output
+ * with its bias, then Y = residual + gate phi(V) in the GEMM's epilogue (no
+ * second pass over Y). Arguments, workspace (hq_workspace_bytes) and errors as
+ * hq_quant_linear; epilogue NULL, or with everything absent, is that call
+ * exactly. T up to 2^26; Y must not overlap X or the gate. */
+int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X, int64_t T,
+                        const hq_epilogue* epilogue, void* Y, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* Dense layer descriptor: d_in and d_out multiples of 8 up to 65536; x_dtype
  * (X) and w_dtype (weight) the same hq_dtype; y_dtype (Y, residual, gate) any. */
