@@ -264,6 +264,210 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   }
 }
 
+// ---- large bf16 products --------------------------------------------------------
+//
+// 256 x (64 NP) tile, eight waves of 64 x (32 NP) (4 x 2), 128 bytes of K per
+// stage, two stage buffers. Waves w and w + 4 share a SIMD; the second half of
+// the block runs one barrier interval behind the first, so on every SIMD one
+// wave reads LDS and issues stage loads while the other's MFMAs run (and has
+// priority for them). A k-step is NP phases, one 32-column strip of B each:
+//   L_p  issue this phase's stage loads, read strip p of B (and in the last
+//        two phases one half of the next k-step's A, which replaces the set
+//        the MFMAs use by a second one), wait, barrier
+//   M_p  8 MFMAs (64 rows x 32 columns x 64 k), barrier
+// A piece of a buffer is refilled as soon as its last reader has passed a
+// barrier: strip p of stage kt + 2 in phase p + 1 (the last strip in the first
+// phase of the next k-step), the two 32-row halves of A in phases 0 and 1. Every load thus
+// has 2 NP - 1 (B) or NP + 2 (A) phases to land; the waits count the newer
+// loads (they retire in order), the same sequence in every k-step (stages past
+// the end are issued against an empty descriptor and move nothing).
+// LDS rows and their swizzle are those of linear_tile_kernel; the rows of A
+// are stored half by half (rows 64 r + 32 i + .. of half i together), those of
+// B strip by strip, so that each piece is one contiguous range.
+template <int OFF>
+__device__ __forceinline__ void lds_frag4(v4i (&f)[4], const uint32_t (&p)[4], uint32_t base) {
+  asm volatile(
+      "ds_read_b128 %0, %4 offset:%8\n ds_read_b128 %1, %5 offset:%8\n"
+      "ds_read_b128 %2, %6 offset:%8\n ds_read_b128 %3, %7 offset:%8\n s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+      : "v"(p[0] + base), "v"(p[1] + base), "v"(p[2] + base), "v"(p[3] + base), "n"(OFF)
+      : "memory");
+}
+template <int OFFA, int OFFB>
+__device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[4], uint32_t base_a,
+                                          v4i (&g)[4], const uint32_t (&q)[4], uint32_t base_b) {
+  asm volatile(
+      "ds_read_b128 %0, %8 offset:%16\n ds_read_b128 %1, %9 offset:%16\n"
+      "ds_read_b128 %2, %10 offset:%16\n ds_read_b128 %3, %11 offset:%16\n"
+      "ds_read_b128 %4, %12 offset:%17\n ds_read_b128 %5, %13 offset:%17\n"
+      "ds_read_b128 %6, %14 offset:%17\n ds_read_b128 %7, %15 offset:%17\n s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(g[0]), "=&v"(g[1]), "=&v"(g[2]),
+        "=&v"(g[3])
+      : "v"(p[0] + base_a), "v"(p[1] + base_a), "v"(p[2] + base_a), "v"(p[3] + base_a),
+        "v"(q[0] + base_b), "v"(q[1] + base_b), "v"(q[2] + base_b), "v"(q[3] + base_b),
+        "n"(OFFA), "n"(OFFB)
+      : "memory");
+}
+
+// Loads that may still be in flight when phase p ends, for what phase p + 1
+// reads to have landed (1 per B strip, 2 per half of A; see the order above).
+template <int NP>
+constexpr int pp_wait(int p) {
+  if (p == NP - 1) return 2 * NP + 4;      // strip 0 of the next k-step
+  if (p == NP - 2) return NP == 4 ? 9 : 7;   // half 1 of the next A
+  if (p == NP - 3) return NP == 4 ? 11 : 7;  // half 0 of the next A
+  return 12;                               // NP = 4, p = 0: strip 1
+}
+
+template <int NP>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_pp_kernel(
+    const uint16_t* __restrict__ X, int64_t M, const uint16_t* __restrict__ W, int64_t N, int K,
+    LinEpi ep) {
+  static_assert(NP == 3 || NP == 4, "waits are counted for 3 and 4 strips");
+  constexpr int BM = 256, WN = 32 * NP, BN = 2 * WN;
+  constexpr int ASZ = 128 * BM, STAGE = ASZ + 128 * BN;
+  constexpr int SPITCH = 4 * WN + 16;
+  constexpr int LDSB = 2 * STAGE > 8 * 32 * SPITCH ? 2 * STAGE : 8 * 32 * SPITCH;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDSB];
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  int64_t m0, n0;
+  f6_tile_origin<BM, BN, 4>(int(blockIdx.x), M, N, &m0, &n0);
+  const int wm = wv >> 1, wn = wv & 1;
+  const int ldb = 2 * K;
+  const int KT = (ldb + 127) / 128;
+  const int64_t rows_a = (M - m0) < BM ? (M - m0) : BM;
+  const int64_t rows_b = (N - n0) < BN ? (N - n0) : BN;
+  const uint8_t* const abase = reinterpret_cast<const uint8_t*>(X) + m0 * ldb;
+  const uint8_t* const bbase = reinterpret_cast<const uint8_t*>(W) + n0 * ldb;
+  const int nrec_a = int(rows_a * ldb), nrec_b = int(rows_b * ldb);
+
+  const int chunk = (lane & 7) ^ (((wv & 1) * 4 + (lane >> 4)) & 7);
+  const uint32_t sub = uint32_t((wv & 3) * 8 + (lane >> 3));
+  const uint32_t va = (uint32_t(wv >> 2) * 64 + sub) * uint32_t(ldb) + 16 * chunk;
+  const uint32_t vb = (uint32_t(wv >> 2) * WN + sub) * uint32_t(ldb) + 16 * chunk;
+  auto issue_a = [&](int i, int kt) {
+    const int kb = kt * 128;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(abase, kt < KT ? nrec_a : 0);
+    const bool in = kb + 16 * chunk < ldb;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      lds_dma16_buf(r, in ? va + uint32_t((q * 128 + i * 32) * ldb + kb) : 0x80000000u, 0u,
+                    smem + (kt & 1) * STAGE + i * (ASZ / 2) + (q * 8 + wv) * 1024);
+  };
+  auto issue_b = [&](int j, int kt) {
+    const int kb = kt * 128;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(bbase, kt < KT ? nrec_b : 0);
+    const bool in = kb + 16 * chunk < ldb;
+    lds_dma16_buf(r, in ? vb + uint32_t(32 * j * ldb + kb) : 0x80000000u, 0u,
+                  smem + (kt & 1) * STAGE + ASZ + j * 8192 + wv * 1024);
+  };
+
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(smem));
+  uint32_t pa[4], pb[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t co = lds0 + uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
+    pa[s] = co + uint32_t((wm * 32 + lrow) * 128);
+    pb[s] = co + uint32_t((wn * 32 + lrow) * 128);
+  }
+
+  v16f acc[2][NP];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  v4i af[2][2][4], bf[4];
+
+  // the order of a steady k-step, from stage 0 on
+  issue_a(0, 0);
+  issue_b(0, 0);
+  issue_a(1, 0);
+#pragma unroll
+  for (int j = 1; j < NP; ++j) issue_b(j, 0);
+  issue_a(0, 1);
+  issue_b(0, 1);
+  issue_a(1, 1);
+#pragma unroll
+  for (int j = 1; j < NP - 1; ++j) issue_b(j, 1);
+  wait_vm_lgkm0<2 * NP + 2>();   // both halves of A and strip 0 of stage 0
+  __builtin_amdgcn_s_barrier();
+  lds_frag4<0>(af[0][0], pa, 0u);
+  lds_frag4<ASZ / 2>(af[0][1], pa, 0u);
+  __builtin_amdgcn_s_barrier();
+  if (wv >= 4) __builtin_amdgcn_s_barrier();
+
+  auto phase = [&](auto pc, auto setc, int kt) {
+    constexpr int P = decltype(pc)::value, SET = decltype(setc)::value;
+    if constexpr (P == 0) {
+      issue_b(NP - 1, kt + 1);
+      issue_a(0, kt + 2);
+    } else {
+      issue_b(P - 1, kt + 2);
+      if constexpr (P == 1) issue_a(1, kt + 2);
+    }
+    const uint32_t cur = uint32_t(kt & 1) * STAGE, nxt = uint32_t(STAGE) - cur;
+    if constexpr (P >= NP - 2) {
+      constexpr int I = P - (NP - 2);
+      lds_frag8<ASZ + P * 8192, I * (ASZ / 2)>(bf, pb, cur, af[1 - SET][I], pa, nxt);
+    } else {
+      lds_frag4<ASZ + P * 8192>(bf, pb, cur);
+    }
+    wait_vm_lgkm0<pp_wait<NP>(P)>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i][P] = lin_mfma<uint16_t>(bf[s], af[SET][i][s], acc[i][P]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+  };
+  auto kstep = [&](auto setc, int kt) {
+    phase(std::integral_constant<int, 0>{}, setc, kt);
+    phase(std::integral_constant<int, 1>{}, setc, kt);
+    phase(std::integral_constant<int, 2>{}, setc, kt);
+    if constexpr (NP == 4) phase(std::integral_constant<int, 3>{}, setc, kt);
+  };
+  int kt = 0;
+  for (; kt + 1 < KT; kt += 2) {
+    kstep(std::integral_constant<int, 0>{}, kt);
+    kstep(std::integral_constant<int, 1>{}, kt + 1);
+  }
+  if (kt < KT) kstep(std::integral_constant<int, 0>{}, kt);
+  if (wv < 4) __builtin_amdgcn_s_barrier();
+  wait_vm_lgkm0<0>();
+  __builtin_amdgcn_s_barrier();
+
+  float* const stg = reinterpret_cast<float*>(smem + wv * 32 * SPITCH);
+  constexpr int LPR = WN / 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(stg + lrow * (SPITCH / 4) + j * 32 + 8 * g + 4 * lhalf) =
+            make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                        acc[i][j][4 * g + 3]);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+    for (int q = 0; q < 32 * LPR / 64; ++q) {
+      const int r = (lane + 64 * q) / LPR, c = 8 * ((lane + 64 * q) % LPR);
+      const int64_t m = m0 + wm * 64 + 32 * i + r, n = n0 + wn * WN + c;
+      float v[8];
+      load8(stg + r * (SPITCH / 4) + c, v);
+      if (m < M && n < N) finish8(v, m, n, N, ep);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // Y from the splits' partial sums [splits, M, N], added in split order; one
 // lane per 8 columns. Bound by reading the partial sums (L2 / Infinity Cache).
 __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restrict__ part,
@@ -289,7 +493,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 
 namespace {
 
-enum LinKind { LIN_ROWS, LIN_T32, LIN_T64, LIN_T128 };
+enum LinKind { LIN_ROWS, LIN_T32, LIN_T64, LIN_T128, LIN_PP3, LIN_PP4 };
 
 // Kernel and split count of a product. Rows up to 8 take the vector kernel.
 // Otherwise the tile shrinks until the tiles cover the 256 CUs, and a product
@@ -307,6 +511,12 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   if (t < 256) {
     p.kind = M <= 32 ? LIN_T32 : LIN_T64;
     t = M <= 32 ? tiles(32, 128) : tiles(64, 64);
+  }
+  if (esize == 2 && tiles(256, 192) >= 128) {
+    // the wide tiles whose rounds of one per CU cost less
+    const int64_t r3 = (tiles(256, 192) + 255) / 256 * 3, r4 = (tiles(256, 256) + 255) / 256 * 4;
+    p.kind = r3 < r4 ? LIN_PP3 : LIN_PP4;
+    return p;
   }
   const int ksteps = p.kper;
   if (t < 256) {
@@ -353,6 +563,17 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       else if (M == 2) launch_rows_nc<TE, 2>(X, int(M), W, N, K, ep, s);
       else if (M <= 4) launch_rows_nc<TE, 4>(X, int(M), W, N, K, ep, s);
       else launch_rows_nc<TE, 8>(X, int(M), W, N, K, ep, s);
+      break;
+    case LIN_PP3:
+    case LIN_PP4:
+      if constexpr (sizeof(TE) == 2) {
+        const int bn = p.kind == LIN_PP3 ? 192 : 256;
+        const dim3 grid(unsigned(((M + 255) / 256) * ((N + bn - 1) / bn)));
+        if (p.kind == LIN_PP3)
+          hipLaunchKernelGGL(linear_pp_kernel<3>, grid, dim3(512), 0, s, X, M, W, N, K, ep);
+        else
+          hipLaunchKernelGGL(linear_pp_kernel<4>, grid, dim3(512), 0, s, X, M, W, N, K, ep);
+      }
       break;
     case LIN_T32: launch_tile<TE, 32, 128, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
     case LIN_T64: launch_tile<TE, 64, 64, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;

@@ -77,6 +77,13 @@ def test_many_tiles(T, K, N, dt):
     run(T, K, N, dt, act="gelu", residual=True, gate_rows=-(-T // 3))
 
 
+@pytest.mark.parametrize("K", [8, 64, 72, 128, 136, 192, 256, 320, 456, 1152])
+@pytest.mark.parametrize("T,N", [(2500, 2312), (4000, 4040)])
+def test_wide_tiles(T, N, K):
+    # tiles of 256 x 192 and 256 x 256, from one k-step to many, odd and even counts, ragged on every side
+    run(T, K, N, hq.BF16, act="gelu", residual=True, gate_rows=1000)
+
+
 @pytest.mark.parametrize("dt,ydt", list(itertools.product([hq.BF16, hq.F32], repeat=2)))
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("T", [1, 7, 70, 700])
@@ -97,7 +104,7 @@ def test_empty_and_reused_output():
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
-@pytest.mark.parametrize("T,K,N", [(3, 72, 40), (33, 72, 40), (300, 1032, 136), (2100, 520, 2312)])
+@pytest.mark.parametrize("T,K,N", [(3, 72, 40), (33, 72, 40), (300, 1032, 136), (2100, 520, 2312), (2500, 1032, 2312), (4000, 584, 4040)])
 def test_neighbours_are_left_alone(T, K, N, dt):
     # the buffers around X, W and Y hold NaN and marks: no row, column or chunk
     # past the operands is read as data, nothing past Y is written
@@ -173,7 +180,7 @@ def test_side_stream_and_repeats():
     assert all(torch.equal(ref, y) for y in got)
 
 
-@pytest.mark.parametrize("T,K,N", [(2, 1152, 6912), (300, 4096, 1152), (2100, 1160, 2312)])
+@pytest.mark.parametrize("T,K,N", [(2, 1152, 6912), (300, 4096, 1152), (2100, 1160, 2312), (4000, 584, 4040)])
 def test_graph_replays_match_eager(T, K, N):
     desc = hq.LinearDesc(K, N, hq.BF16, hq.BF16, hq.BF16)
     Xa, W, b, g = make(T, K, N, hq.BF16)
