@@ -134,39 +134,4 @@ __device__ __forceinline__ void finish1(float v, int64_t m, int64_t n, int64_t N
   else finish1_as<float>(v, m, n, N, ep);
 }
 
-// The same for the quantised GEMMs' epilogues, whose lanes hold runs of four
-// columns of one row: element offsets of row m (clamped into the output: rows
-// past M are computed and never stored) in the residual and the gate.
-struct ExtRow {
-  int64_t r, g;
-};
-__device__ __forceinline__ ExtRow ext_row(const GemmEpi& ep, int64_t m, int64_t M) {
-  const LinEpi& l = ep.lin;
-  const int64_t mc = m < M ? m : M - 1;
-  return ExtRow{mc * ep.ldy, l.gate ? int64_t(uint32_t(mc) / uint32_t(l.gate_rows)) * l.gate_ld : 0};
-}
-__device__ __forceinline__ void load4(const uint16_t* __restrict__ p, float v[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
-// Columns n .. n+3 (clamped into the output like the row), bf16 Y.
-__device__ __forceinline__ void ext4(float (&y)[4], const LinEpi& ep, const ExtRow& row, int64_t n,
-                                     int64_t N) {
-  apply_act<4, false>(y, ep.act);
-  const int64_t nc = n < N ? n : N - 4;
-  if (ep.gate) {
-    float g[4];
-    load4(static_cast<const uint16_t*>(ep.gate) + row.g + nc, g);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] *= g[k];
-  }
-  if (ep.residual) {
-    float r[4];
-    load4(static_cast<const uint16_t*>(ep.residual) + row.r + nc, r);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] += r[k];
-  }
-}
-
 }  // namespace hq

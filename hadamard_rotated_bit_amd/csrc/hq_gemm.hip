@@ -23,44 +23,6 @@
 
 namespace hq {
 
-template <int BM, int BN, int BK, int WM, int WN, int S, int GM, int OCC>
-static hipError_t launch_cfg(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
-                             int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s) {
-  if (K % BK) return hipErrorInvalidValue;
-  constexpr int NT = (BM / WM) * (BN / WN) * 64;
-  const int64_t ntiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-  dim3 grid{unsigned(ntiles)}, block{NT};
-  GemmEpi ep = {};
-  if (epi) {
-    ep = *epi;
-    if (ep.ext)
-      hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC, true>), grid, block,
-                         0, s, A, M, B, N, K, nullptr, 0, ep);
-    else
-      hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC>), grid, block, 0, s,
-                         A, M, B, N, K, nullptr, 0, ep);
-  } else {
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, false, OCC>), grid, block, 0, s,
-                       A, M, B, N, K, acc_out, ldc, ep);
-  }
-  return hipGetLastError();
-}
-
-template <int LR>
-static hipError_t launch_i8_persist(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
-                                    const GemmEpi& ep, int cus, hipStream_t s) {
-  const int64_t ntiles = ((M + 255) / 256) * ((N + 191) / 192);
-  const unsigned grid = unsigned(ntiles < cus ? ntiles : cus);
-  const uint8_t *a = reinterpret_cast<const uint8_t*>(A), *b = reinterpret_cast<const uint8_t*>(B);
-  if (ep.ext)
-    hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR, true>), dim3(grid), dim3(256), 0,
-                       s, a, M, b, N, K, ep);
-  else
-    hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR, false>), dim3(grid), dim3(256),
-                       0, s, a, M, b, N, K, ep);
-  return hipGetLastError();
-}
-
 static int cu_count() {
   // CU count per device, queried once (racing writers store the same value).
   static int cu_cache[64] = {};
@@ -74,9 +36,59 @@ static int cu_count() {
   return cu_cache[dev] > 0 ? cu_cache[dev] : 256;
 }
 
+template <int BM, int BN, int BK, int WM, int WN, int S, int GM, int OCC>
+static hipError_t launch_cfg(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
+                             int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s) {
+  if (K % BK) return hipErrorInvalidValue;
+  constexpr int NT = (BM / WM) * (BN / WN) * 64;
+  const int64_t ntiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  dim3 grid{unsigned(ntiles)}, block{NT};
+  GemmEpi ep = {};
+  if (epi) {
+    ep = *epi;
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, true, OCC>), grid, block, 0, s,
+                       A, M, B, N, K, nullptr, 0, ep);
+  } else {
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, S, GM, false, OCC>), grid, block, 0, s,
+                       A, M, B, N, K, acc_out, ldc, ep);
+  }
+  return hipGetLastError();
+}
+
+// The product with the extended epilogue (activation, gate, residual): tiles
+// small enough that two blocks share a CU and one's epilogue runs beside the
+// other's products (as launch_f6_ext).
+template <int BN, int WN, int S, int OCC>
+static hipError_t launch_i8_ext(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
+                                const GemmEpi& ep, hipStream_t s) {
+  if (K % 128) return hipErrorInvalidValue;
+  const int64_t ntiles = ((M + 127) / 128) * ((N + BN - 1) / BN);
+  hipLaunchKernelGGL((gemm_i8_kernel<128, BN, 128, 64, WN, S, 8, true, OCC, true>),
+                     dim3(unsigned(ntiles)), dim3(256), 0, s, A, M, B, N, K, nullptr, 0, ep);
+  return hipGetLastError();
+}
+
+template <int LR>
+static hipError_t launch_i8_persist(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
+                                    const GemmEpi& ep, int cus, hipStream_t s) {
+  const int64_t ntiles = ((M + 255) / 256) * ((N + 191) / 192);
+  const unsigned grid = unsigned(ntiles < cus ? ntiles : cus);
+  hipLaunchKernelGGL((gemm_i8_persist<256, 192, 128, 96, 4, LR>), dim3(grid), dim3(256), 0, s,
+                     reinterpret_cast<const uint8_t*>(A), M, reinterpret_cast<const uint8_t*>(B),
+                     N, K, ep);
+  return hipGetLastError();
+}
+
 hipError_t launch_gemm(const int8_t* A, int64_t M, const int8_t* B, int64_t N, int K,
                        int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s) {
   if (M <= 0 || N <= 0) return hipSuccess;
+  if (epi && epi->ext) {
+    // where 128 x 128 tiles leave CUs idle, 128 x 64 (2000 x 1152 -> 1152: 16.9
+    // us a call against 20.5; 8192 x 4096 -> 4096 the other way, 230 against 192)
+    if (((M + 127) / 128) * ((N + 127) / 128) < cu_count())
+      return launch_i8_ext<64, 32, 3, 2>(A, M, B, N, K, *epi, s);
+    return launch_i8_ext<128, 64, 2, 2>(A, M, B, N, K, *epi, s);
+  }
   if (epi && epi->y_bf16 && K % 64 == 0 && K >= 256 && M > 512 && N > 512) {
     const int cus = cu_count();
     return !epi->rank         ? launch_i8_persist<0>(A, M, B, N, K, *epi, cus, s)

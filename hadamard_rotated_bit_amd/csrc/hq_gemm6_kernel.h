@@ -374,7 +374,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_f6_kernel(
 struct Frag8 {
   v4i c[2];
 };
-template <bool I8, int BM, int BN, int WM, int WN, int GM, int RG, int LR, bool EXT>
+template <bool I8, int BM, int BN, int WM, int WN, int GM, int RG, int LR>
 __device__ __forceinline__ void persist_body(const uint8_t* __restrict__ A, int64_t M,
                                              const uint8_t* __restrict__ B, int64_t N, int K,
                                              GemmEpi ep) {
@@ -654,7 +654,6 @@ __device__ __forceinline__ void persist_body(const uint8_t* __restrict__ A, int6
       for (int i = 0; i < TM; ++i) {
         const float sx = Pf[3 * BN + wm0 + 32 * i + erow];
         const float mu = Pf[3 * BN + BM + wm0 + 32 * i + erow];
-        const ExtRow er = EXT ? ext_row(ep, mw + 32 * i + erow, M) : ExtRow{};
         // Low-rank term of slice i (all strips): one 32-rank chunk of U and
         // L2 operands loaded before any product (see the tiled epilogue).
         v16f lr[LR ? TN : 1];
@@ -736,11 +735,6 @@ __device__ __forceinline__ void persist_body(const uint8_t* __restrict__ A, int6
               y2 += lr[j][4 * g + 2];
               y3 += lr[j][4 * g + 3];
             }
-            if constexpr (EXT) {
-              float e[4] = {y0, y1, y2, y3};
-              ext4(e, ep.lin, er, cur.n0 + nl, N);
-              y0 = e[0]; y1 = e[1]; y2 = e[2]; y3 = e[3];
-            }
             {
               const uint32_t la = uint32_t(reinterpret_cast<uintptr_t>(stg + erow * SP + (j * 32 + 8 * g + 4 * ehalf) * 2));
               const uint2 dv = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
@@ -800,20 +794,20 @@ __device__ __forceinline__ void persist_body(const uint8_t* __restrict__ A, int6
 #undef HP_ISSUE
 }
 
-template <int BM, int BN, int WM, int WN, int GM, int RG, int LR, bool EXT>
+template <int BM, int BN, int WM, int WN, int GM, int RG, int LR>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 __attribute__((amdgpu_waves_per_eu(1))) void gemm_f6_persist(
     const uint8_t* __restrict__ A, int64_t M, const uint8_t* __restrict__ B, int64_t N, int K,
     GemmEpi ep) {
-  persist_body<false, BM, BN, WM, WN, GM, RG, LR, EXT>(A, M, B, N, K, ep);
+  persist_body<false, BM, BN, WM, WN, GM, RG, LR>(A, M, B, N, K, ep);
 }
 
-template <int BM, int BN, int WM, int WN, int GM, int LR, bool EXT>
+template <int BM, int BN, int WM, int WN, int GM, int LR>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 __attribute__((amdgpu_waves_per_eu(1))) void gemm_i8_persist(
     const uint8_t* __restrict__ A, int64_t M, const uint8_t* __restrict__ B, int64_t N, int K,
     GemmEpi ep) {
-  persist_body<true, BM, BN, WM, WN, GM, 1, LR, EXT>(A, M, B, N, K, ep);
+  persist_body<true, BM, BN, WM, WN, GM, 1, LR>(A, M, B, N, K, ep);
 }
 
 }  // namespace hq

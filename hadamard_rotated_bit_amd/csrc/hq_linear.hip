@@ -271,31 +271,48 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 // the block runs one barrier interval behind the first, so on every SIMD one
 // wave reads LDS and issues stage loads while the other's MFMAs run (and has
 // priority for them). A k-step is NP phases, one 32-column strip of B each:
-//   L_p  issue this phase's stage loads, read strip p of B (and in the last
-//        two phases one half of the next k-step's A, which replaces the set
-//        the MFMAs use by a second one), wait, barrier
+//   L_p  issue this phase's stage loads, read strip p of B and a share of the
+//        next k-step's A (into the register set that the MFMAs do not use),
+//        wait, barrier
 //   M_p  8 MFMAs (64 rows x 32 columns x 64 k), barrier
-// A piece of a buffer is refilled as soon as its last reader has passed a
-// barrier: strip p of stage kt + 2 in phase p + 1 (the last strip in the first
-// phase of the next k-step), the two 32-row halves of A in phases 0 and 1. Every load thus
-// has 2 NP - 1 (B) or NP + 2 (A) phases to land; the waits count the newer
-// loads (they retire in order), the same sequence in every k-step (stages past
-// the end are issued against an empty descriptor and move nothing).
+// The L parts are kept even (2 or 3 loads, 6 or 8 fragment reads), since an
+// interval lasts as long as the longer of the two halves' parts.
+// A piece of a buffer is refilled once its last reader has passed a barrier:
+// strip p of stage kt + 2 in phase p + 1 (the last strip in the next k-step's
+// first phase); A of stage kt + 1 is read during k-step kt, its first 32-row half
+// in phases 0 and 1 (then refilled with stage kt + 3), its second half after
+// that (refilled in the next k-step's phases 0 and 1). The waits count the
+// newer loads (they retire in order), the same sequence in every k-step;
+// stages past the end are issued against an empty descriptor and move nothing.
 // LDS rows and their swizzle are those of linear_tile_kernel; the rows of A
 // are stored half by half (rows 64 r + 32 i + .. of half i together), those of
 // B strip by strip, so that each piece is one contiguous range.
+
+// Fragments from the given addresses (a strip of B, then a share of A) and the
+// wait for all of them.
 template <int OFF>
-__device__ __forceinline__ void lds_frag4(v4i (&f)[4], const uint32_t (&p)[4], uint32_t base) {
+__device__ __forceinline__ void lds_frag4(v4i (&f)[4], const uint32_t (&p)[4]) {
   asm volatile(
       "ds_read_b128 %0, %4 offset:%8\n ds_read_b128 %1, %5 offset:%8\n"
       "ds_read_b128 %2, %6 offset:%8\n ds_read_b128 %3, %7 offset:%8\n s_waitcnt lgkmcnt(0)"
       : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
-      : "v"(p[0] + base), "v"(p[1] + base), "v"(p[2] + base), "v"(p[3] + base), "n"(OFF)
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "n"(OFF)
       : "memory");
 }
 template <int OFFA, int OFFB>
-__device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[4], uint32_t base_a,
-                                          v4i (&g)[4], const uint32_t (&q)[4], uint32_t base_b) {
+__device__ __forceinline__ void lds_frag6(v4i (&f)[4], const uint32_t (&p)[4], v4i& g0, v4i& g1,
+                                          uint32_t q0, uint32_t q1) {
+  asm volatile(
+      "ds_read_b128 %0, %6 offset:%12\n ds_read_b128 %1, %7 offset:%12\n"
+      "ds_read_b128 %2, %8 offset:%12\n ds_read_b128 %3, %9 offset:%12\n"
+      "ds_read_b128 %4, %10 offset:%13\n ds_read_b128 %5, %11 offset:%13\n s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(g0), "=&v"(g1)
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q0), "v"(q1), "n"(OFFA), "n"(OFFB)
+      : "memory");
+}
+template <int OFFA, int OFFB>
+__device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[4], v4i (&g)[4],
+                                          const uint32_t (&q)[4]) {
   asm volatile(
       "ds_read_b128 %0, %8 offset:%16\n ds_read_b128 %1, %9 offset:%16\n"
       "ds_read_b128 %2, %10 offset:%16\n ds_read_b128 %3, %11 offset:%16\n"
@@ -303,20 +320,21 @@ __device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[4], u
       "ds_read_b128 %6, %14 offset:%17\n ds_read_b128 %7, %15 offset:%17\n s_waitcnt lgkmcnt(0)"
       : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(g[0]), "=&v"(g[1]), "=&v"(g[2]),
         "=&v"(g[3])
-      : "v"(p[0] + base_a), "v"(p[1] + base_a), "v"(p[2] + base_a), "v"(p[3] + base_a),
-        "v"(q[0] + base_b), "v"(q[1] + base_b), "v"(q[2] + base_b), "v"(q[3] + base_b),
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]),
         "n"(OFFA), "n"(OFFB)
       : "memory");
 }
 
 // Loads that may still be in flight when phase p ends, for what phase p + 1
-// reads to have landed (1 per B strip, 2 per half of A; see the order above).
+// reads to have landed. Issue order of a k-step (u: unit of a half of A):
+//   NP = 4: B3 A1u0 | B0 A1u1 | B1 A0u0 | B2 A0u1     (8 loads)
+//   NP = 3: B2 A1u0 | B0 A1u1 | B1 A0u0 A0u1          (7 loads)
+// Next phase 0 reads A half 0, last issued two k-steps back (one k-step newer);
+// phase 1 reads B1, phase 2 (NP = 3: the last) A half 1, phase 3 B3.
 template <int NP>
 constexpr int pp_wait(int p) {
-  if (p == NP - 1) return 2 * NP + 4;      // strip 0 of the next k-step
-  if (p == NP - 2) return NP == 4 ? 9 : 7;   // half 1 of the next A
-  if (p == NP - 3) return NP == 4 ? 11 : 7;  // half 0 of the next A
-  return 12;                               // NP = 4, p = 0: strip 1
+  if (NP == 4) return p == 0 || p == 2 ? 13 : 8;
+  return p == 0 ? 11 : 7;
 }
 
 template <int NP>
@@ -325,9 +343,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     LinEpi ep) {
   static_assert(NP == 3 || NP == 4, "waits are counted for 3 and 4 strips");
   constexpr int BM = 256, WN = 32 * NP, BN = 2 * WN;
-  constexpr int ASZ = 128 * BM, STAGE = ASZ + 128 * BN;
+  constexpr int ASZ = 128 * BM, STAGE = 65536;   // a power of two: buffers toggle by one xor
   constexpr int SPITCH = 4 * WN + 16;
-  constexpr int LDSB = 2 * STAGE > 8 * 32 * SPITCH ? 2 * STAGE : 8 * 32 * SPITCH;
+  constexpr int LDSN = STAGE + ASZ + 128 * BN, LDSE = 8 * 32 * SPITCH;
+  constexpr int LDSB = LDSN > LDSE ? LDSN : LDSE;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[LDSB];
 
   const int lane = threadIdx.x & 63;
@@ -347,22 +366,29 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const uint32_t sub = uint32_t((wv & 3) * 8 + (lane >> 3));
   const uint32_t va = (uint32_t(wv >> 2) * 64 + sub) * uint32_t(ldb) + 16 * chunk;
   const uint32_t vb = (uint32_t(wv >> 2) * WN + sub) * uint32_t(ldb) + 16 * chunk;
-  auto issue_a = [&](int i, int kt) {
+  // One unit of a half of A / the wave's unit of a strip of B. FAST: a whole
+  // stage inside K (the row in the vector offset, so that rows past the end
+  // stay out of range, the stage in the scalar one); otherwise stages past K
+  // take an empty descriptor and chunks past K an offset out of range.
+  auto issue = [&](auto fastc, const uint8_t* base, int nrec, uint32_t v, int row, int kt, int lds) {
     const int kb = kt * 128;
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(abase, kt < KT ? nrec_a : 0);
-    const bool in = kb + 16 * chunk < ldb;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      lds_dma16_buf(r, in ? va + uint32_t((q * 128 + i * 32) * ldb + kb) : 0x80000000u, 0u,
-                    smem + (kt & 1) * STAGE + i * (ASZ / 2) + (q * 8 + wv) * 1024);
+    uint8_t* const dst = smem + (kt & 1) * STAGE + lds + wv * 1024;
+    if constexpr (decltype(fastc)::value) {
+      lds_dma16_buf(make_rsrc(base, nrec), v + uint32_t(row * ldb), uint32_t(kb), dst);
+    } else {
+      const bool in = kb + 16 * chunk < ldb;
+      lds_dma16_buf(make_rsrc(base, kt < KT ? nrec : 0), in ? v + uint32_t(row * ldb + kb) : 0x80000000u,
+                    0u, dst);
+    }
   };
-  auto issue_b = [&](int j, int kt) {
-    const int kb = kt * 128;
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(bbase, kt < KT ? nrec_b : 0);
-    const bool in = kb + 16 * chunk < ldb;
-    lds_dma16_buf(r, in ? vb + uint32_t(32 * j * ldb + kb) : 0x80000000u, 0u,
-                  smem + (kt & 1) * STAGE + ASZ + j * 8192 + wv * 1024);
+  auto issue_a = [&](auto fastc, int i, int q, int kt) {
+    issue(fastc, abase, nrec_a, va, q * 128 + i * 32, kt, i * (ASZ / 2) + q * 8192);
   };
+  auto issue_b = [&](auto fastc, int j, int kt) {
+    issue(fastc, bbase, nrec_b, vb, 32 * j, kt, ASZ + j * 8192);
+  };
+  constexpr std::false_type slow{};
+  constexpr std::true_type fast{};
 
   const int lrow = lane & 31, lhalf = lane >> 5;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(smem));
@@ -382,39 +408,55 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
   v4i af[2][2][4], bf[4];
 
-  // the order of a steady k-step, from stage 0 on
-  issue_a(0, 0);
-  issue_b(0, 0);
-  issue_a(1, 0);
-#pragma unroll
-  for (int j = 1; j < NP; ++j) issue_b(j, 0);
-  issue_a(0, 1);
-  issue_b(0, 1);
-  issue_a(1, 1);
-#pragma unroll
-  for (int j = 1; j < NP - 1; ++j) issue_b(j, 1);
-  wait_vm_lgkm0<2 * NP + 2>();   // both halves of A and strip 0 of stage 0
+  // the order of steady k-steps -3, -2 and -1
+  issue_a(slow, 0, 0, 0);
+  issue_a(slow, 0, 1, 0);
+  issue_a(slow, 1, 0, 0);
+  issue_b(slow, 0, 0);
+  issue_a(slow, 1, 1, 0);
+  issue_b(slow, 1, 0);
+  issue_a(slow, 0, 0, 1);
+  if constexpr (NP == 4) issue_b(slow, 2, 0);
+  issue_a(slow, 0, 1, 1);
+  issue_b(slow, NP - 1, 0);
+  issue_a(slow, 1, 0, 1);
+  issue_b(slow, 0, 1);
+  issue_a(slow, 1, 1, 1);
+  wait_vm_lgkm0<NP + 4>();   // all of A of stage 0
   __builtin_amdgcn_s_barrier();
-  lds_frag4<0>(af[0][0], pa, 0u);
-  lds_frag4<ASZ / 2>(af[0][1], pa, 0u);
+  lds_frag4<0>(af[0][0], pa);
+  lds_frag4<ASZ / 2>(af[0][1], pa);
+  __builtin_amdgcn_s_barrier();
+  issue_b(slow, 1, 1);
+  issue_a(slow, 0, 0, 2);
+  if constexpr (NP == 4) issue_b(slow, 2, 1);
+  issue_a(slow, 0, 1, 2);
+  wait_vm_lgkm0<pp_wait<NP>(NP - 1)>();
   __builtin_amdgcn_s_barrier();
   if (wv >= 4) __builtin_amdgcn_s_barrier();
 
-  auto phase = [&](auto pc, auto setc, int kt) {
+  auto phase = [&](auto pc, auto setc, auto fc, int kt) {
     constexpr int P = decltype(pc)::value, SET = decltype(setc)::value;
-    if constexpr (P == 0) {
-      issue_b(NP - 1, kt + 1);
-      issue_a(0, kt + 2);
+    if constexpr (P == 0) issue_b(fc, NP - 1, kt + 1);
+    else issue_b(fc, P - 1, kt + 2);
+    if constexpr (P < 2) issue_a(fc, 1, P, kt + 2);
+    if constexpr (P == 2) issue_a(fc, 0, 0, kt + 3);
+    if constexpr (P == NP - 1) issue_a(fc, 0, 1, kt + 3);
+    // pa, pb: this stage's buffer
+    if constexpr (NP == 3 && P == 2) {
+      const uint32_t pn[4] = {pa[0] ^ STAGE, pa[1] ^ STAGE, pa[2] ^ STAGE, pa[3] ^ STAGE};
+      lds_frag8<ASZ + P * 8192, ASZ / 2>(bf, pb, af[1 - SET][1], pn);
     } else {
-      issue_b(P - 1, kt + 2);
-      if constexpr (P == 1) issue_a(1, kt + 2);
+      constexpr int I = P / 2, F = 2 * (P % 2);
+      lds_frag6<ASZ + P * 8192, I * (ASZ / 2)>(bf, pb, af[1 - SET][I][F], af[1 - SET][I][F + 1],
+                                               pa[F] ^ STAGE, pa[F + 1] ^ STAGE);
     }
-    const uint32_t cur = uint32_t(kt & 1) * STAGE, nxt = uint32_t(STAGE) - cur;
-    if constexpr (P >= NP - 2) {
-      constexpr int I = P - (NP - 2);
-      lds_frag8<ASZ + P * 8192, I * (ASZ / 2)>(bf, pb, cur, af[1 - SET][I], pa, nxt);
-    } else {
-      lds_frag4<ASZ + P * 8192>(bf, pb, cur);
+    if constexpr (P == NP - 1) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        pa[s] ^= STAGE;
+        pb[s] ^= STAGE;
+      }
     }
     wait_vm_lgkm0<pp_wait<NP>(P)>();
     __builtin_amdgcn_s_barrier();
@@ -428,18 +470,25 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
   };
-  auto kstep = [&](auto setc, int kt) {
-    phase(std::integral_constant<int, 0>{}, setc, kt);
-    phase(std::integral_constant<int, 1>{}, setc, kt);
-    phase(std::integral_constant<int, 2>{}, setc, kt);
-    if constexpr (NP == 4) phase(std::integral_constant<int, 3>{}, setc, kt);
+  auto kstep = [&](auto setc, auto fc, int kt) {
+    phase(std::integral_constant<int, 0>{}, setc, fc, kt);
+    phase(std::integral_constant<int, 1>{}, setc, fc, kt);
+    phase(std::integral_constant<int, 2>{}, setc, fc, kt);
+    if constexpr (NP == 4) phase(std::integral_constant<int, 3>{}, setc, fc, kt);
   };
+  constexpr std::integral_constant<int, 0> set0{};
+  constexpr std::integral_constant<int, 1> set1{};
+  const int KF = ldb / 128;      // stages of whole chunks
   int kt = 0;
-  for (; kt + 1 < KT; kt += 2) {
-    kstep(std::integral_constant<int, 0>{}, kt);
-    kstep(std::integral_constant<int, 1>{}, kt + 1);
+  for (; kt + 4 < KF; kt += 2) {
+    kstep(set0, fast, kt);
+    kstep(set1, fast, kt + 1);
   }
-  if (kt < KT) kstep(std::integral_constant<int, 0>{}, kt);
+  for (; kt + 1 < KT; kt += 2) {
+    kstep(set0, slow, kt);
+    kstep(set1, slow, kt + 1);
+  }
+  if (kt < KT) kstep(set0, slow, kt);
   if (wv < 4) __builtin_amdgcn_s_barrier();
   wait_vm_lgkm0<0>();
   __builtin_amdgcn_s_barrier();
