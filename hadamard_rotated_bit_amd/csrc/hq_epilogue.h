@@ -15,18 +15,23 @@ namespace hq {
 
 __device__ __forceinline__ float relu_f32(float x) { return x < 0.0f ? 0.0f : x; }  // keeps NaN
 
-// SiLU, GELU and its tanh form are all x / (1 + 2^(-x P(x^2))): P is the
-// constant log2(e) for SiLU and linear for the tanh form (fp32 accuracy), and
-// for GELU with a bf16 result the degree-6 fit of log2(Phi(x) / Phi(-x)) / x on |x| <= 5 (relative error
-// of phi at most 1.1e-4 there: 1/37 of a bf16 half step; beyond, x^2 is held
-// at 25 and phi differs from x or 0 by less than 1.5e-5 in absolute value).
-// One exp2 and one reciprocal per value, no branch between the three.
-__device__ __forceinline__ float act_fast(float x, const ActCoef& a) {
-  const float t = fminf(x * x, a.tmax);
-  float p = a.c[6];
+// SiLU, GELU and its tanh form are all x / (1 + 2^(x P(x^2))): P is the
+// constant -log2(e) for SiLU (DEG 0) and linear for the tanh form (DEG 1, fp32
+// accuracy), and for GELU with a bf16 result (DEG 6) the fit of -log2(Phi(x) /
+// Phi(-x)) / x on |x| <= 5 (relative error of phi at most 1.1e-4 there: 1/37
+// of a bf16 half step; beyond, x^2 is held at 25 and phi differs from x or 0
+// by less than 1.5e-5 in absolute value). One exp2 and one reciprocal per value;
+// the degree is fixed per loop, as the exponent's terms are what the vector
+// ALU spends on it.
+template <int DEG>
+__device__ __forceinline__ float act_sigmoid(float x, const ActCoef& a) {
+  float p = a.c[DEG];
+  if constexpr (DEG > 0) {
+    const float t = fminf(x * x, a.tmax);
 #pragma unroll
-  for (int k = 5; k >= 0; --k) p = fmaf(p, t, a.c[k]);
-  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-(x * p)));
+    for (int k = DEG - 1; k >= 0; --k) p = fmaf(p, t, a.c[k]);
+  }
+  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * p));
 }
 
 // GELU for an fp32 result: max(x, 0) - |x| h(|x|), h(a) = Phi(-a) =
@@ -61,13 +66,16 @@ __device__ __forceinline__ void apply_act(float (&v)[N], const ActCoef& a) {
     for (int k = 0; k < N; ++k) v[k] = relu_f32(v[k]);
     return;
   }
-  if (FULL && a.act == ACT_GELU) {
+  if (a.act == ACT_SILU) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = gelu_full(v[k]);
-    return;
+    for (int k = 0; k < N; ++k) v[k] = act_sigmoid<0>(v[k], a);
+  } else if (a.act == ACT_GELU_TANH) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = act_sigmoid<1>(v[k], a);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = FULL ? gelu_full(v[k]) : act_sigmoid<6>(v[k], a);
   }
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = act_fast(v[k], a);
 }
 
 __device__ __forceinline__ void store8(float* __restrict__ p, const float v[8]) {

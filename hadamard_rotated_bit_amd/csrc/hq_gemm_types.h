@@ -15,8 +15,8 @@ constexpr int F6_GROUP = 4;
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
 // An activation as its kernels take it: the kind and, for SiLU and the two
-// GELU forms, the polynomial P(t) = sum c_k t^k of phi(x) = x / (1 + 2^(-x P(x^2))),
-// t held at tmax (act_fast, hq_epilogue.h).
+// GELU forms, the polynomial P(t) = sum c_k t^k of phi(x) = x / (1 + 2^(x P(x^2))),
+// t held at tmax (act_sigmoid, hq_epilogue.h).
 struct ActCoef {
   int act;
   float tmax;

@@ -655,24 +655,23 @@ hipError_t launch_linear(const void* X, int bf16, int64_t M, const void* W, int6
                       static_cast<float*>(part), ep, s);
 }
 
-// GELU (bf16 results): degree-6 weighted least-maximum fit of log2(Phi(x) / Phi(-x)) / x in
+// GELU (bf16 results): degree-6 weighted least-maximum fit of -log2(Phi(x) / Phi(-x)) / x in
 // x^2 on |x| <= 5; the other two are exact forms.
 ActCoef act_coef(int act) {
   ActCoef a = {};
   a.act = act;
   constexpr float log2e = 1.4426950408889634f;
   if (act == ACT_SILU) {
-    a.tmax = 0.0f;
-    a.c[0] = log2e;
+    a.c[0] = -log2e;
   } else if (act == ACT_GELU_TANH) {
-    a.tmax = 1e6f;   // 2^(-x P) is 0 or infinite long before; keeps x^2 finite
-    a.c[0] = 1.5957691216057308f * log2e;
-    a.c[1] = 1.5957691216057308f * 0.044715f * log2e;
+    a.tmax = 1e6f;   // 2^(x P) is 0 or infinite long before; keeps x^2 finite
+    a.c[0] = -1.5957691216057308f * log2e;
+    a.c[1] = -1.5957691216057308f * 0.044715f * log2e;
   } else if (act == ACT_GELU) {
     a.tmax = 25.0f;
-    const float c[7] = {2.3017581959277815f,     0.10552445421016707f,   -0.0003938443860880515f,
-                        -0.0001041246928390452f, 6.513520962607899e-06f, -1.7551338906125295e-07f,
-                        1.842194984814521e-09f};
+    const float c[7] = {-2.3017581959277815f,   -0.10552445421016707f,   0.0003938443860880515f,
+                        0.0001041246928390452f, -6.513520962607899e-06f, 1.7551338906125295e-07f,
+                        -1.842194984814521e-09f};
     for (int k = 0; k < 7; ++k) a.c[k] = c[k];
   }
   return a;

@@ -8,21 +8,20 @@
 // once; the statistics need all of a group before its first output.
 //
 // Statistics never subtract large sums. A lane owns 8 consecutive channels
-// (one 16- or 32-byte load per row) and takes, per channel, the mean of the
-// rows in its registers and then the squares about that mean; batches, lanes
-// and chunks are joined in a fixed tree by
+// (one 16- or 32-byte load per row) and takes, per unit of channels that share
+// a group, the mean of the rows in its registers and then the squares about
+// that mean; batches, lanes and chunks are joined in a fixed tree by
 //   mean = m_a + d n_b / n,   M2 = M2_a + M2_b + d^2 n_a n_b / n,   d = m_b - m_a,
-// and the channels of a group by mean_g = avg m_c, M2_g = sum M2_c + n (m_c -
-// mean_g)^2. Everything is fp32; groups need not be multiples of 8 channels
-// wide, since channels meet only in the last step.
+// and the units of a group by mean_g = avg m_u, M2_g = sum M2_u + n (m_u -
+// mean_g)^2. Everything is fp32; groups may have any width.
 //
 // Two forms (norm_plan):
 //  norm_block_kernel   a block holds all positions of one sample's slab of
 //                      whole groups in registers: one launch, x read once.
-//  norm_stats_kernel + norm_apply_kernel
+//  norm_stats_kernel (+ norm_join_kernel) + norm_apply_kernel
 //                      chunks of positions; partial statistics in the
-//                      workspace; the second pass finds x in the Infinity
-//                      Cache where it fits.
+//                      workspace; the second pass finds x in the caches
+//                      where it fits.
 #include "hq_epilogue.h"
 #include "hq_internal.h"
 
@@ -38,7 +37,7 @@ struct NormKArgs {
   float eps;
   int y_bf16;
   ActCoef act;
-  float2* part;         // [S, G, chunks] (mean, M2)
+  float2* part;         // [S, G, chunks] (mean, M2), then [S, G] joined
   int chunks;
   int64_t rpc;          // rows per chunk
   int slab;             // channels per block (norm_block_kernel)
@@ -63,15 +62,21 @@ __device__ __forceinline__ void raw_get(const Raw8<float>& r, float v[8]) {
   load8(reinterpret_cast<const float*>(&r.q[0]), v);
 }
 
-// Running statistics of 8 channels over n rows.
-struct Stat8 {
-  float n, mean[8], m2[8];
+// A lane's 8 channels are taken in units of U = gcd(C / G, 8) channels: a unit
+// lies within one group, so its channels share one mean and one M2 (NS = 8 / U
+// of them per lane: 1 where the group width is a multiple of 8, 4 at 10).
+// Running statistics of a lane's units over n values each.
+template <int NS>
+struct Stat {
+  float n, mean[NS], m2[NS];
 };
-__device__ __forceinline__ void stat_merge(Stat8& a, float nb, const float mb[8], const float m2b[8]) {
+template <int NS>
+__device__ __forceinline__ void stat_merge(Stat<NS>& a, float nb, const float (&mb)[NS],
+                                           const float (&m2b)[NS]) {
   if (nb == 0.0f) return;
   const float nt = a.n + nb, r = nb / nt, w = a.n * r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < NS; ++e) {
     const float d = mb[e] - a.mean[e];
     a.mean[e] = fmaf(d, r, a.mean[e]);
     a.m2[e] += fmaf(d * d, w, m2b[e]);
@@ -79,24 +84,32 @@ __device__ __forceinline__ void stat_merge(Stat8& a, float nb, const float mb[8]
   a.n = nt;
 }
 
-// The statistics of the first `n` of the R rows in `x` (n uniform in nothing:
-// each lane its own), merged into `a`.
-template <typename TE, int R>
-__device__ __forceinline__ void stat_rows(Stat8& a, const Raw8<TE> (&x)[R], int n) {
+// The statistics of the first `n` of the R rows in `x` (each lane its own n),
+// merged into `a`.
+template <typename TE, int U, int R>
+__device__ __forceinline__ void stat_rows(Stat<8 / U>& a, Raw8<TE> (&x)[R], int n) {
+  constexpr int NS = 8 / U;
   if (n <= 0) return;
-  float m[8] = {0, 0, 0, 0, 0, 0, 0, 0}, q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  float m[NS] = {}, q[NS] = {};
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (i < n) {
       float v[8];
       raw_get(x[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[e] += v[e];
+      for (int e = 0; e < 8; ++e) m[e / U] += v[e];
     }
   }
-  const float inv = 1.0f / float(n);
+  const float nv = float(n * U), inv = 1.0f / nv;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m[e] *= inv;
+  for (int e = 0; e < NS; ++e) m[e] *= inv;
+  // the rows stay packed between the two passes (their floats, kept, would
+  // take twice the registers of a batch)
+  if constexpr (sizeof(TE) == 2) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      asm volatile("" : "+v"(x[i].q[0].x), "+v"(x[i].q[0].y), "+v"(x[i].q[0].z), "+v"(x[i].q[0].w));
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (i < n) {
@@ -104,61 +117,71 @@ __device__ __forceinline__ void stat_rows(Stat8& a, const Raw8<TE> (&x)[R], int 
       raw_get(x[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = v[e] - m[e];
-        q[e] = fmaf(d, d, q[e]);
+        const float d = v[e] - m[e / U];
+        q[e / U] = fmaf(d, d, q[e / U]);
       }
     }
   }
-  stat_merge(a, float(n), m, q);
+  stat_merge<NS>(a, nv, m, q);
 }
 
 // Joins the statistics of the block's RY row lanes (ty) for each of the VR
 // channel vectors (tx): halves the lanes until lane 0 has all, the upper part
-// of each step through LDS. sm: NT 17-float slots. Leaves the per-channel
-// means in sm[0 .. 8 VR) and M2 in sm[8 VR .. 16 VR) (after a barrier).
-template <int NT>
-__device__ __forceinline__ void stat_tree(Stat8& a, float* sm, int tx, int ty, int VR, int RY,
+// of each step through LDS (slots of an odd number of floats: lanes hit
+// distinct banks). Leaves the units' means in sm[0 .. NS VR) and their M2
+// behind them, after a barrier. sm: NT (2 NS + 1) floats.
+template <int NS>
+__device__ __forceinline__ void stat_tree(Stat<NS>& a, float* sm, int tx, int ty, int VR, int RY,
                                           bool live) {
-  float* const slot = sm + (ty * VR + tx) * 17;   // odd pitch: lanes hit distinct banks
+  constexpr int PITCH = 2 * NS + 1;
+  float* const slot = sm + (ty * VR + tx) * PITCH;
   int n = RY;
   while (n > 1) {
     const int h = (n + 1) >> 1;
     if (live && ty >= h && ty < n) {
-      slot[16] = a.n;
+      slot[2 * NS] = a.n;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < NS; ++e) {
         slot[e] = a.mean[e];
-        slot[8 + e] = a.m2[e];
+        slot[NS + e] = a.m2[e];
       }
     }
     __syncthreads();
     if (live && ty < n - h) {
-      const float* o = slot + h * VR * 17;
-      float mb[8], qb[8];
+      const float* o = slot + h * VR * PITCH;
+      float mb[NS], qb[NS];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < NS; ++e) {
         mb[e] = o[e];
-        qb[e] = o[8 + e];
+        qb[e] = o[NS + e];
       }
-      stat_merge(a, o[16], mb, qb);
+      stat_merge<NS>(a, o[2 * NS], mb, qb);
     }
     n = h;
   }
   __syncthreads();
   if (live && ty == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      sm[8 * tx + e] = a.mean[e];
-      sm[8 * VR + 8 * tx + e] = a.m2[e];
+    for (int e = 0; e < NS; ++e) {
+      sm[NS * tx + e] = a.mean[e];
+      sm[NS * VR + NS * tx + e] = a.m2[e];
     }
   }
   __syncthreads();
 }
 
-// Sum over aligned runs of `lanes` (a power of two up to 64) lanes.
+// Sum over aligned runs of `lanes` (a power of two up to 64) lanes, on the
+// VALU; `lanes` is uniform.
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  switch (lanes) {
+    case 2: return group_sum<2>(v);
+    case 4: return group_sum<4>(v);
+    case 8: return group_sum<8>(v);
+    case 16: return group_sum<16>(v);
+    case 32: return group_sum<32>(v);
+    case 64: return group_sum<64>(v);
+    default: return v;
+  }
 }
 __device__ __forceinline__ int pow2_at_least(int n, int most) {
   int l = 1;
@@ -166,34 +189,73 @@ __device__ __forceinline__ int pow2_at_least(int n, int most) {
   return l;
 }
 
-// Group statistics from per-channel ones (cm, cq: channel means and M2 over n
-// rows each): calls out(g, mean, M2) once per group.
+// Group statistics from the units' (cm, cq: means and M2 over n values each;
+// cu units per group): calls out(g, mean, M2) once per group.
 template <int NT, typename F>
-__device__ __forceinline__ void group_stats(const float* cm, const float* cq, int groups, int cg,
+__device__ __forceinline__ void group_stats(const float* cm, const float* cq, int groups, int cu,
                                             float n, F out) {
-  const int lg = pow2_at_least(cg, 64);
+  const int lg = pow2_at_least(cu, 64), sh = __builtin_ctz(lg);
   const int l = threadIdx.x & (lg - 1);
-  const float inv = 1.0f / float(cg);
-  for (int g = threadIdx.x / lg; g < groups; g += NT / lg) {
+  const float inv = 1.0f / float(cu);
+  for (int g = threadIdx.x >> sh; g < groups; g += NT >> sh) {
     float s = 0.0f;
-    for (int c = l; c < cg; c += lg) s += cm[g * cg + c];
+    for (int c = l; c < cu; c += lg) s += cm[g * cu + c];
     const float mean = lanes_sum(s, lg) * inv;
     float q = 0.0f;
-    for (int c = l; c < cg; c += lg) {
-      const float d = cm[g * cg + c] - mean;
-      q += fmaf(n * d, d, cq[g * cg + c]);
+    for (int c = l; c < cu; c += lg) {
+      const float d = cm[g * cu + c] - mean;
+      q += fmaf(n * d, d, cq[g * cu + c]);
     }
     q = lanes_sum(q, lg);
     if (l == 0) out(g, mean, q);
   }
 }
 
-// y of one row's 8 channels: (x - mean) a + b, phi, one rounding.
-__device__ __forceinline__ void norm_store(const float v[8], const float mean[8], const float a[8],
-                                           const float b[8], const NormKArgs& k, int64_t off) {
-  float y[8];
+__device__ __forceinline__ float rstd_of(float m2, const NormKArgs& k) {
+  return 1.0f / sqrtf(m2 / (float(k.P) * float(k.C / k.G)) + k.eps);
+}
+
+// gamma and beta of channels c .. c+7.
+__device__ __forceinline__ void load_affine(const NormKArgs& k, int c, float a[8], float b[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = fmaf(v[e] - mean[e], a[e], b[e]);
+  for (int e = 0; e < 8; ++e) {
+    a[e] = 1.0f;
+    b[e] = 0.0f;
+  }
+  if (k.gamma) load8(k.gamma + c, a);
+  if (k.beta) load8(k.beta + c, b);
+}
+
+// A lane's coefficients, y = (x - mean) a + b with a = gamma rstd. The mean is
+// not folded into b: a constant group (rstd = 1 / sqrt(eps)) then gives b
+// exactly instead of a rounding of mean a.
+struct Coef {
+  float mean[8], a[8], b[8];
+};
+// c0: the lane's first channel counted from the first of gm / gr (the groups'
+// means and reciprocal deviations); c.a, c.b hold gamma and beta.
+__device__ __forceinline__ void coef_finish(Coef& c, int c0, int cg, const float* gm,
+                                            const float* gr) {
+  int g = c0 / cg, r = c0 - g * cg;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    c.mean[e] = gm[g];
+    c.a[e] *= gr[g];
+    if (++r == cg) {
+      r = 0;
+      ++g;
+    }
+  }
+}
+
+// y of one row's 8 channels: phi, one rounding.
+template <typename TE>
+__device__ __forceinline__ void norm_store(const Raw8<TE>& x, const Coef& c, const NormKArgs& k,
+                                           int64_t off) {
+  float y[8];
+  raw_get(x, y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e] - c.mean[e], c.a[e], c.b[e]);
   if (k.y_bf16) {
     apply_act<8, false>(y, k.act);
     store8(static_cast<uint16_t*>(k.y) + off, y);
@@ -203,154 +265,213 @@ __device__ __forceinline__ void norm_store(const float v[8], const float mean[8]
   }
 }
 
-// Per-lane coefficients of channels c0 .. c0+7 (c0 counted from the block's
-// first channel cb): mean, gamma rstd, beta. gm / gr: the groups' means and
-// 1 / sqrt(var + eps), from the block's first group.
-__device__ __forceinline__ void norm_coef(const NormKArgs& k, int cb, int c0, int cg,
-                                          const float* gm, const float* gr, float mean[8],
-                                          float a[8], float b[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int g = (c0 + e) / cg;
-    mean[e] = gm[g];
-    a[e] = gr[g] * (k.gamma ? k.gamma[cb + c0 + e] : 1.0f);
-    b[e] = k.beta ? k.beta[cb + c0 + e] : 0.0f;
-  }
-}
-
 // ---- one launch -------------------------------------------------------------------
 
 constexpr int NORM_BLOCK_GROUPS = 512;   // groups per slab at most
 
 // Block (slab, sample): R rows per lane in registers.
-template <typename TE, int NT, int R>
+template <typename TE, int U, int NT, int R>
 __global__ __launch_bounds__(NT) void norm_block_kernel(NormKArgs k) {
-  __shared__ float sm[NT * 17];
+  constexpr int NS = 8 / U;
+  __shared__ float sm[NT * (2 * NS + 1)];
   __shared__ float gm[NORM_BLOCK_GROUPS], gr[NORM_BLOCK_GROUPS];
-  const int nslab = (k.C + k.slab - 1) / k.slab;
-  const int64_t s = blockIdx.x / nslab;
-  const int cb = int(blockIdx.x - s * nslab) * k.slab;
+  // slabs of a sample share its lines: on one XCD (block b runs on XCD b mod 8)
+  // where the samples are a multiple of 8
+  const uint32_t nslab = uint32_t(k.C + k.slab - 1) / uint32_t(k.slab);
+  const uint32_t samples = gridDim.x / nslab;
+  const bool by_xcd = samples % 8 == 0;
+  const uint32_t major = blockIdx.x / (by_xcd ? samples : nslab);
+  const uint32_t minor = blockIdx.x - major * (by_xcd ? samples : nslab);
+  const uint32_t smp = by_xcd ? minor : major;
+  const int cb = int(by_xcd ? major : minor) * k.slab;
   const int nc = (k.C - cb) < k.slab ? (k.C - cb) : k.slab;
   const int VR = nc / 8, RY = NT / VR, cg = k.C / k.G;
   const int ty = int(threadIdx.x) / VR, tx = int(threadIdx.x) - ty * VR;
   const bool live = ty < RY;
-  const int64_t base = s * k.P * k.C + cb + 8 * tx;
-  const TE* const x = static_cast<const TE*>(k.x);
+  const int P = int(k.P);
+  const int64_t base = int64_t(smp) * k.P * k.C + cb + 8 * tx;
+  const TE* const x = static_cast<const TE*>(k.x) + base;
   Raw8<TE> v[R];
   int n = 0;   // rows ty, ty + RY, ... of this lane
-  if (live && ty < k.P) n = int((k.P - ty + RY - 1) / RY);
+  if (live && ty < P) n = (P - ty + RY - 1) / RY;
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    if (i < n) v[i] = raw_load(x + base + int64_t(ty + i * RY) * k.C);
-  Stat8 a = {};
-  stat_rows<TE, R>(a, v, n);
-  stat_tree<NT>(a, sm, tx, ty, VR, RY, live);
-  const float inv = 1.0f / (float(k.P) * float(cg));
-  group_stats<NT>(sm, sm + 8 * VR, nc / cg, cg, float(k.P), [&](int g, float mean, float m2) {
-    gm[g] = mean;
-    gr[g] = 1.0f / sqrtf(fmaf(m2, inv, k.eps));
-  });
+    if (i < n) v[i] = raw_load(x + int64_t(ty + i * RY) * k.C);
+  Coef c = {};
+  if (live) load_affine(k, cb + 8 * tx, c.a, c.b);
+  Stat<NS> a = {};
+  stat_rows<TE, U, R>(a, v, n);
+  stat_tree<NS>(a, sm, tx, ty, VR, RY, live);
+  group_stats<NT>(sm, sm + NS * VR, nc / cg, cg / U, float(P) * float(U),
+                  [&](int g, float mean, float m2) {
+                    gm[g] = mean;
+                    gr[g] = rstd_of(m2, k);
+                  });
   __syncthreads();
   if (!live) return;
-  float mean[8], ca[8], cbeta[8];
-  norm_coef(k, cb, 8 * tx, cg, gm, gr, mean, ca, cbeta);
+  coef_finish(c, 8 * tx, cg, gm, gr);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (i < n) {
-      float f[8];
-      raw_get(v[i], f);
-      norm_store(f, mean, ca, cbeta, k, base + int64_t(ty + i * RY) * k.C);
-    }
-  }
+  for (int i = 0; i < R; ++i)
+    if (i < n) norm_store<TE>(v[i], c, k, base + int64_t(ty + i * RY) * k.C);
 }
 
-// ---- two launches -----------------------------------------------------------------
+// ---- two or three launches ----------------------------------------------------------
 
-// Partial statistics of chunk c of sample s (block s chunks + c).
-template <typename TE, int NT>
+// Partial statistics of chunk c of sample s (block s chunks + c). A batch of
+// rows is loaded before the one in registers is summed.
+template <typename TE, int U, int NT>
 __global__ __launch_bounds__(NT) void norm_stats_kernel(NormKArgs k) {
-  constexpr int R = 8;
-  __shared__ float sm[NT * 17];
-  const int64_t s = blockIdx.x / k.chunks;
-  const int c = int(blockIdx.x - s * k.chunks);
+  constexpr int NS = 8 / U;
+  constexpr int R = 16 / sizeof(TE);   // 8 or 4 rows: 32 registers
+  __shared__ float sm[NT * (2 * NS + 1)];
+  const uint32_t s = blockIdx.x / uint32_t(k.chunks);
+  const int c = int(blockIdx.x - s * uint32_t(k.chunks));
   const int64_t r0 = int64_t(c) * k.rpc;
   const int rows = int((k.P - r0) < k.rpc ? (k.P - r0) : k.rpc);
   const int VR = k.C / 8, RY = NT / VR, cg = k.C / k.G;
   const int ty = int(threadIdx.x) / VR, tx = int(threadIdx.x) - ty * VR;
   const bool live = ty < RY;
-  const TE* const x = static_cast<const TE*>(k.x) + (s * k.P + r0) * k.C + 8 * tx;
-  Stat8 a = {};
+  const TE* const x = static_cast<const TE*>(k.x) + (int64_t(s) * k.P + r0) * k.C + 8 * tx;
+  Stat<NS> a = {};
   if (live) {
-    for (int r = ty; r < rows; r += R * RY) {
-      Raw8<TE> v[R];
-      const int n = (rows - r + RY - 1) / RY;
+    Raw8<TE> v[2][R];
+    auto fetch = [&](Raw8<TE> (&d)[R], int r) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (i < n) v[i] = raw_load(x + int64_t(r + i * RY) * k.C);
-      stat_rows<TE, R>(a, v, n < R ? n : R);
+        if (r + i * RY < rows) d[i] = raw_load(x + int64_t(r + i * RY) * k.C);
+    };
+    auto sum = [&](Raw8<TE> (&d)[R], int r) {
+      const int n = (rows - r + RY - 1) / RY;
+      stat_rows<TE, U, R>(a, d, n < R ? n : R);
+    };
+    fetch(v[0], ty);
+    for (int r = ty; r < rows; r += 2 * R * RY) {
+      fetch(v[1], r + R * RY);
+      sum(v[0], r);
+      if (r + R * RY < rows) {
+        fetch(v[0], r + 2 * R * RY);
+        sum(v[1], r + R * RY);
+      }
     }
   }
-  stat_tree<NT>(a, sm, tx, ty, VR, RY, live);
-  group_stats<NT>(sm, sm + 8 * VR, k.G, cg, float(rows), [&](int g, float mean, float m2) {
-    k.part[(s * k.G + g) * k.chunks + c] = make_float2(mean, m2);
-  });
+  stat_tree<NS>(a, sm, tx, ty, VR, RY, live);
+  group_stats<NT>(sm, sm + NS * VR, k.G, cg / U, float(rows) * float(U),
+                  [&](int g, float mean, float m2) {
+                    k.part[(int64_t(s) * k.G + g) * k.chunks + c] = make_float2(mean, m2);
+                  });
 }
 
-// Joins the chunks' statistics (every block for its sample), then normalises
-// rows [rpb b, rpb (b + 1)) of the sample.
+__device__ __forceinline__ float chunk_rows(const NormKArgs& k, int c) {
+  const int64_t left = k.P - int64_t(c) * k.rpc;
+  return float(left < k.rpc ? left : k.rpc);
+}
+
+// The chunks (up to 1024) of each (sample, group) joined into one: a block
+// each, the partial results in registers, mean first, then the squares about it.
+__global__ __launch_bounds__(256) void norm_join_kernel(NormKArgs k, float2* __restrict__ out) {
+  __shared__ float red[2][4];
+  const float2* p = k.part + int64_t(blockIdx.x) * k.chunks;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float2 v[4];
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = int(threadIdx.x) + 256 * i;
+    v[i] = c < k.chunks ? p[c] : make_float2(0.0f, 0.0f);
+    w[i] = c < k.chunks ? chunk_rows(k, c) : 0.0f;
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = fmaf(v[i].x, w[i], s);
+  s = group_sum<64>(s);
+  if (lane == 0) red[0][wave] = s;
+  __syncthreads();
+  const float mean = ((red[0][0] + red[0][1]) + (red[0][2] + red[0][3])) / float(k.P);
+  const float cg = float(k.C / k.G);
+  float q = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float d = v[i].x - mean;
+    q += w[i] > 0.0f ? fmaf(d * d, w[i] * cg, v[i].y) : 0.0f;
+  }
+  q = group_sum<64>(q);
+  if (lane == 0) red[1][wave] = q;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    out[blockIdx.x] = make_float2(mean, (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]));
+}
+
+// Normalises rows of sample s. Chunk c of the first pass is cut into `subs`
+// parts, and block s subs chunks + sub chunks + c takes part sub (from the
+// chunk's end): blocks b and b mod chunks share an XCD where chunks is a
+// multiple of 8, and the rows that its L2 still holds from the first pass, the
+// last ones of each chunk, come first. Statistics: join_n partial results per
+// group (1 after norm_join_kernel), joined by every block.
 template <typename TE, int NT>
-__global__ __launch_bounds__(NT) void norm_apply_kernel(NormKArgs k, int bps, int64_t rpb) {
-  constexpr int R = 4;
+__global__ __launch_bounds__(NT) void norm_apply_kernel(NormKArgs k, const float2* __restrict__ stats,
+                                                        int join_n, int subs, int64_t rps) {
+  constexpr int R = 8 / sizeof(TE);    // 4 or 2 rows
   constexpr int MAXG = NT == 256 ? 2048 : NORM_MAX_C;   // G <= C, C <= 2048 with 256 threads
   __shared__ float gm[MAXG], gr[MAXG];
-  const int64_t s = blockIdx.x / bps;
-  const int64_t r0 = int64_t(int(blockIdx.x - s * bps)) * rpb;
-  const int rows = int((k.P - r0) < rpb ? (k.P - r0) : rpb);
-  const int cg = k.C / k.G;
-  const int lq = pow2_at_least(k.chunks, 64);
-  const int l = threadIdx.x & (lq - 1);
-  const float inv = 1.0f / (float(k.P) * float(cg));
-  for (int g = threadIdx.x / lq; g < k.G; g += NT / lq) {
-    const float2* p = k.part + (s * k.G + g) * k.chunks;
-    float sum = 0.0f;
-    for (int c = l; c < k.chunks; c += lq) {
-      const int64_t left = k.P - int64_t(c) * k.rpc;
-      sum = fmaf(p[c].x, float(left < k.rpc ? left : k.rpc), sum);
+  const uint32_t per = uint32_t(subs) * uint32_t(k.chunks);
+  const uint32_t s = blockIdx.x / per, rest = blockIdx.x - s * per;
+  const int sub = int(rest / uint32_t(k.chunks)), c = int(rest - uint32_t(sub) * uint32_t(k.chunks));
+  const int64_t c0 = int64_t(c) * k.rpc, c1 = c0 + k.rpc < k.P ? c0 + k.rpc : k.P;
+  const int64_t r1 = c1 - sub * rps;
+  const int64_t r0 = r1 - rps > c0 ? r1 - rps : c0;
+  const int rows = int(r1 - r0);       // <= 0 for parts past a short last chunk
+  const int VR = k.C / 8, RY = NT / VR, cg = k.C / k.G;
+  const int ty = int(threadIdx.x) / VR, tx = int(threadIdx.x) - ty * VR;
+  const bool live = ty < RY;
+  const int64_t base = (int64_t(s) * k.P + r0) * k.C + 8 * tx;
+  const TE* const x = static_cast<const TE*>(k.x) + base;   // rows <= 0: no row is touched
+  Raw8<TE> v[2][R];
+  auto fetch = [&](Raw8<TE> (&d)[R], int r) {   // rows r, r - RY, ...
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (r - i * RY >= 0) d[i] = raw_load(x + int64_t(r - i * RY) * k.C);
+  };
+  const int last = live ? rows - 1 - ty : -1;
+  fetch(v[0], last);
+  Coef cf = {};
+  if (live) load_affine(k, 8 * tx, cf.a, cf.b);
+
+  const float2* const ps = stats + int64_t(s) * k.G * join_n;
+  if (join_n == 1) {
+    for (int g = threadIdx.x; g < k.G; g += NT) {
+      const float2 r = ps[g];
+      gm[g] = r.x;
+      gr[g] = rstd_of(r.y, k);
     }
-    const float mean = lanes_sum(sum, lq) / float(k.P);
-    float q = 0.0f;
-    for (int c = l; c < k.chunks; c += lq) {
-      const int64_t left = k.P - int64_t(c) * k.rpc;
-      const float2 v = p[c];
-      const float d = v.x - mean;
-      q += fmaf(d * d, float(left < k.rpc ? left : k.rpc) * float(cg), v.y);
-    }
-    q = lanes_sum(q, lq);
-    if (l == 0) {
-      gm[g] = mean;
-      gr[g] = 1.0f / sqrtf(fmaf(q, inv, k.eps));
+  } else {
+    const int lq = pow2_at_least(join_n, 32), sh = __builtin_ctz(lq);
+    const int l = threadIdx.x & (lq - 1);
+    for (int g = threadIdx.x >> sh; g < k.G; g += NT >> sh) {
+      const float2 r = l < join_n ? ps[int64_t(g) * join_n + l] : make_float2(0.0f, 0.0f);
+      const float w = l < join_n ? chunk_rows(k, l) : 0.0f;
+      const float mean = lanes_sum(r.x * w, lq) / float(k.P);
+      const float d = r.x - mean;
+      const float q = lanes_sum(w > 0.0f ? fmaf(d * d, w * float(cg), r.y) : 0.0f, lq);
+      if (l == 0) {
+        gm[g] = mean;
+        gr[g] = rstd_of(q, k);
+      }
     }
   }
   __syncthreads();
-  const int VR = k.C / 8, RY = NT / VR;
-  const int ty = int(threadIdx.x) / VR, tx = int(threadIdx.x) - ty * VR;
-  if (ty >= RY) return;
-  float mean[8], ca[8], cbeta[8];
-  norm_coef(k, 0, 8 * tx, cg, gm, gr, mean, ca, cbeta);
-  const int64_t base = (s * k.P + r0) * k.C + 8 * tx;
-  const TE* const x = static_cast<const TE*>(k.x) + base;
-  for (int r = ty; r < rows; r += R * RY) {
-    Raw8<TE> v[R];
+  if (!live) return;
+  coef_finish(cf, 8 * tx, cg, gm, gr);
+  auto emit = [&](const Raw8<TE> (&d)[R], int r) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (r + i * RY < rows) v[i] = raw_load(x + int64_t(r + i * RY) * k.C);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (r + i * RY < rows) {
-        float f[8];
-        raw_get(v[i], f);
-        norm_store(f, mean, ca, cbeta, k, base + int64_t(r + i * RY) * k.C);
-      }
+      if (r - i * RY >= 0) norm_store<TE>(d[i], cf, k, base + int64_t(r - i * RY) * k.C);
+  };
+  for (int r = last; r >= 0; r -= 2 * R * RY) {
+    fetch(v[1], r - R * RY);
+    emit(v[0], r);
+    if (r - R * RY >= 0) {
+      fetch(v[0], r - 2 * R * RY);
+      emit(v[1], r - R * RY);
     }
   }
 }
@@ -361,79 +482,102 @@ namespace {
 
 struct NormPlan {
   int block;         // 1: norm_block_kernel
-  int nt, r, slab;   // its threads, rows per lane and channels per block
-  int chunks;        // two launches: chunks per sample and their rows
+  int nt, r, slab;   // threads; its rows per lane and channels per block
+  int chunks;        // otherwise: chunks per sample and their rows,
   int64_t rpc;
-  int bps;           // apply blocks per sample and their rows
-  int64_t rpb;
+  int subs;          // parts of a chunk in the second pass and their rows,
+  int64_t rps;
+  int join;          // 1: norm_join_kernel between the passes
 };
 
 int gcd_i(int a, int b) { return b ? gcd_i(b, a % b) : a; }
 
 // Slabs are whole groups and whole 8-channel vectors: multiples of `unit` =
-// lcm(C / G, 8) channels, taken until a row's piece is a 128-byte line, then
-// doubled while all positions still are one pass of 256 lanes.
+// lcm(C / G, 8) channels, taken until a row's piece is 64 bytes (8 x 1536 x
+// 256 fp32: 13.3 us against 14.0 with 32 bytes and 14.3 with 128), or 32 bytes
+// where a sample's slabs share an XCD's L2 and wider ones would leave CUs idle
+// (the same in bf16: 9.7 us against 11.8); where all positions are less than
+// one pass of 256 lanes, they are doubled. Up to 8 rows per lane a block keeps
+// its slab in registers (1 x 1024 x 512 fp32: 8.4 us against 12.9 for two
+// launches); longer ones take the chunked form, which spreads a sample over
+// every CU (1 x 4096 x 512 bf16: 14.7 us against 21).
 NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   NormPlan p = {};
   const int cg = C / G, unit = cg / gcd_i(cg, 8) * 8;
+  const int piece = esize == 2 && S % 8 == 0 && S * (C / 16) <= 256 ? 32 : 64;
   int slab = unit;
-  while (slab * esize < 128 && slab < C) slab += unit;
+  while (slab * esize < piece && slab < C) slab += unit;
   while (slab < C && P * slab / 4 <= 256 && 2 * slab / cg <= NORM_BLOCK_GROUPS) slab *= 2;
   if (slab > C) slab = C;
   for (int nt : {256, 1024}) {
     const int VR = slab / 8;
     if (VR > nt || slab / cg > NORM_BLOCK_GROUPS) continue;
-    const int RY = nt / VR;
-    const int64_t need = (P + RY - 1) / RY;
+    const int64_t need = (P + nt / VR - 1) / (nt / VR);   // rows per lane
     if (need <= 8) {
       p.block = 1;
       p.nt = nt;
       p.slab = slab;
-      p.r = need <= 2 ? 2 : 8;
+      p.r = need <= 2 && nt == 256 ? 2 : 8;
       return p;
     }
   }
   p.nt = C <= 2048 ? 256 : 1024;
-  if (S * P * C >= int64_t(1) << 22) p.nt = 1024;
   const int RY = p.nt / (C / 8);
-  int64_t want = (512 + S - 1) / S;                       // about two blocks per CU
+  int64_t want = (1024 + S - 1) / S;                      // about four blocks per CU
   const int64_t most = (P + RY * 8 - 1) / (RY * 8);       // at least 8 rows per lane
   if (want > most) want = most;
-  if (want > 256) want = 256;
-  if (want < 1) want = 1;
   p.rpc = (P + want - 1) / want;
   p.chunks = int((P + p.rpc - 1) / p.rpc);
-  p.rpb = p.rpc;
-  p.bps = p.chunks;
+  // parts of at most 16 rows per lane
+  p.subs = int((p.rpc + RY * 16 - 1) / (RY * 16));
+  p.rps = (p.rpc + p.subs - 1) / p.subs;
+  // many chunks: every block of the second pass would read them all
+  p.join = p.chunks > 32;
   return p;
+}
+
+template <typename TE, int U>
+void launch_norm_first(const NormPlan& p, const NormKArgs& k, dim3 grid, hipStream_t s) {
+  if (!p.block && p.nt == 256)
+    hipLaunchKernelGGL((norm_stats_kernel<TE, U, 256>), grid, dim3(256), 0, s, k);
+  else if (!p.block)
+    hipLaunchKernelGGL((norm_stats_kernel<TE, U, 1024>), grid, dim3(1024), 0, s, k);
+  else if (p.nt == 256 && p.r == 2)
+    hipLaunchKernelGGL((norm_block_kernel<TE, U, 256, 2>), grid, dim3(256), 0, s, k);
+  else if (p.nt == 256)
+    hipLaunchKernelGGL((norm_block_kernel<TE, U, 256, 8>), grid, dim3(256), 0, s, k);
+  else
+    hipLaunchKernelGGL((norm_block_kernel<TE, U, 1024, 8>), grid, dim3(1024), 0, s, k);
 }
 
 template <typename TE>
 hipError_t launch_norm_typed(const NormPlan& p, const NormKArgs& k, int64_t S, hipStream_t s) {
-  if (p.block) {
-    const dim3 grid(unsigned(S * ((k.C + p.slab - 1) / p.slab)));
-    if (p.nt == 256 && p.r == 2)
-      hipLaunchKernelGGL((norm_block_kernel<TE, 256, 2>), grid, dim3(256), 0, s, k);
-    else if (p.nt == 256)
-      hipLaunchKernelGGL((norm_block_kernel<TE, 256, 8>), grid, dim3(256), 0, s, k);
-    else if (p.r == 2)
-      hipLaunchKernelGGL((norm_block_kernel<TE, 1024, 2>), grid, dim3(1024), 0, s, k);
-    else
-      hipLaunchKernelGGL((norm_block_kernel<TE, 1024, 8>), grid, dim3(1024), 0, s, k);
-    return hipGetLastError();
+  const dim3 g1(unsigned(S * (p.block ? (k.C + p.slab - 1) / p.slab : p.chunks)));
+  switch (gcd_i(k.C / k.G, 8)) {
+    case 8: launch_norm_first<TE, 8>(p, k, g1, s); break;
+    case 4: launch_norm_first<TE, 4>(p, k, g1, s); break;
+    case 2: launch_norm_first<TE, 2>(p, k, g1, s); break;
+    default: launch_norm_first<TE, 1>(p, k, g1, s); break;
   }
-  const dim3 g1(unsigned(S * p.chunks)), g2(unsigned(S * p.bps));
-  if (p.nt == 256) {
-    hipLaunchKernelGGL((norm_stats_kernel<TE, 256>), g1, dim3(256), 0, s, k);
-    const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.block) return e;
+  const dim3 g2(unsigned(S * p.chunks * p.subs));
+  const float2* stats = k.part;
+  int join_n = p.chunks;
+  if (p.join) {
+    float2* joined = k.part + S * k.G * p.chunks;
+    hipLaunchKernelGGL(norm_join_kernel, dim3(unsigned(S * k.G)), dim3(256), 0, s, k, joined);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((norm_apply_kernel<TE, 256>), g2, dim3(256), 0, s, k, p.bps, p.rpb);
-  } else {
-    hipLaunchKernelGGL((norm_stats_kernel<TE, 1024>), g1, dim3(1024), 0, s, k);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((norm_apply_kernel<TE, 1024>), g2, dim3(1024), 0, s, k, p.bps, p.rpb);
+    stats = joined;
+    join_n = 1;
   }
+  if (p.nt == 256)
+    hipLaunchKernelGGL((norm_apply_kernel<TE, 256>), g2, dim3(256), 0, s, k, stats, join_n, p.subs,
+                       p.rps);
+  else
+    hipLaunchKernelGGL((norm_apply_kernel<TE, 1024>), g2, dim3(1024), 0, s, k, stats, join_n,
+                       p.subs, p.rps);
   return hipGetLastError();
 }
 
@@ -442,7 +586,7 @@ hipError_t launch_norm_typed(const NormPlan& p, const NormKArgs& k, int64_t S, h
 size_t norm_part_bytes(int64_t S, int64_t P, int C, int G, int esize) {
   if (S <= 0 || P <= 0) return 0;
   const NormPlan p = norm_plan(S, P, C, G, esize);
-  return p.block ? 0 : sizeof(float2) * size_t(S) * size_t(G) * size_t(p.chunks);
+  return p.block ? 0 : sizeof(float2) * size_t(S) * size_t(G) * size_t(p.chunks + p.join);
 }
 
 hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
