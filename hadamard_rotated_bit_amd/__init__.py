@@ -191,6 +191,9 @@ def quant_linear(desc: Desc, prepared: torch.Tensor, X: torch.Tensor,
     T = X.shape[0]
     _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
     if epilogue is not None:
+        if _elsewhere(X):
+            with torch.cuda.device(X.device):
+                return _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue)
         return _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue)
     if out is None:
         out = torch.empty(T, desc.d_out, dtype=_TORCH[desc.y_dtype], device=X.device)
@@ -375,22 +378,18 @@ def prepared_views(desc: Desc, prepared: torch.Tensor) -> dict:
 
 # ---- epilogues and dense layers ---------------------------------------------
 
-class _on:
-    """Makes ``device`` current for the launch of a call on its tensors."""
-    __slots__ = ("index", "prev")
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether the tensor's device is not the current one (a call then runs
+    again under it: kernels launch on the current device)."""
+    return t.device.index != torch.cuda.current_device()
 
-    def __init__(self, device: torch.device):
-        self.index = device.index
 
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.index != self.prev:
-            torch.cuda.set_device(self.index)
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
-    def __exit__(self, *exc):
-        if self.index != self.prev:
-            torch.cuda.set_device(self.prev)
+
+def _stream_of(t: torch.Tensor) -> int:
+    return torch.cuda.current_stream(t.device.index).cuda_stream
 
 
 def _same_device(ref: torch.Tensor, **tensors) -> None:
@@ -441,9 +440,8 @@ def _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue):
     if workspace is None:
         workspace = torch.empty(max(lib.hq_workspace_bytes(desc._ref, T), 1), dtype=torch.uint8,
                                 device=X.device)
-    with _on(X.device) as stream:
-        check(lib.hq_quant_linear_epi(desc._ref, _ptr(prepared), _ptr(X), T, ep, _ptr(out),
-                                      _ptr(workspace), workspace.nbytes, stream))
+    check(lib.hq_quant_linear_epi(desc._ref, _addr(prepared), _addr(X), T, ep, _addr(out),
+                                  _addr(workspace), workspace.nbytes, _stream_of(X)))
     return out
 
 
@@ -482,6 +480,9 @@ def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
     allocated when it is needed and not given."""
     T = X.shape[0]
     _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
+    if _elsewhere(X):
+        with torch.cuda.device(X.device):
+            return linear(desc, X, weight, bias, epilogue, out, workspace)
     _need(weight, "weight", _TORCH[desc.w_dtype], (desc.d_out, desc.d_in))
     if bias is not None:
         _need(bias, "bias", torch.float32, (desc.d_out,))
@@ -497,10 +498,9 @@ def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
         n = lib.hq_linear_workspace_bytes(desc._ref, T)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
-    with _on(X.device) as stream:
-        check(lib.hq_linear(desc._ref, _ptr(X), _ptr(weight), _ptr(bias), T, ep, _ptr(out),
-                            _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                            stream))
+    check(lib.hq_linear(desc._ref, _addr(X), _addr(weight), _addr(bias), T, ep, _addr(out),
+                        _addr(workspace), 0 if workspace is None else workspace.nbytes,
+                        _stream_of(X)))
     return out
 
 
@@ -542,6 +542,9 @@ def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = 
         raise ValueError(f"X must be [samples, positions, channels], got {tuple(X.shape)}")
     S, P = X.shape[0], X.shape[1]
     _need(X, "X", _TORCH[desc.x_dtype], (S, P, desc.channels))
+    if _elsewhere(X):
+        with torch.cuda.device(X.device):
+            return group_norm(desc, X, gamma, beta, out, workspace)
     if gamma is not None:
         _need(gamma, "gamma", torch.float32, (desc.channels,))
     if beta is not None:
@@ -557,10 +560,9 @@ def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = 
         n = lib.hq_group_norm_workspace_bytes(desc._ref, S, P)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
-    with _on(X.device) as stream:
-        check(lib.hq_group_norm(desc._ref, _ptr(X), _ptr(gamma), _ptr(beta), S, P, _ptr(out),
-                                _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                                stream))
+    check(lib.hq_group_norm(desc._ref, _addr(X), _addr(gamma), _addr(beta), S, P, _addr(out),
+                            _addr(workspace), 0 if workspace is None else workspace.nbytes,
+                            _stream_of(X)))
     return out
 
 

@@ -102,25 +102,56 @@ __device__ __forceinline__ v16f lin_mfma(const v4i& w, const v4i& x, v16f c) {
   }
 }
 
-// LDS fragment reads as inline asm that waits for its own results: written as
+// LDS fragment reads are inline asm that waits for its own results: written as
 // ordinary loads, the compiler would wait for every stage load in flight (it
-// cannot tell that they fill other buffers).
-__device__ __forceinline__ void lds_read2(v4i& a, v4i& b, uint32_t pa, uint32_t pb) {
-  asm volatile("ds_read_b128 %0, %2\n ds_read_b128 %1, %3\n s_waitcnt lgkmcnt(0)"
-               : "=&v"(a), "=&v"(b)
-               : "v"(pa), "v"(pb)
-               : "memory");
-}
-__device__ __forceinline__ void lds_read4(v4i& a, v4i& b, v4i& c, v4i& d, uint32_t pa, uint32_t pb) {
+// cannot tell that they fill other buffers). All fragments of a k-step are read
+// at once (one LDS latency per k-step): p[s], q[s] are the addresses of substep
+// s of the wave's rows of A and of B; a second 32-row block is 4096 bytes on.
+__device__ __forceinline__ void lds_kstep(v4i (&a)[1][4], v4i (&b)[1][4], const uint32_t (&p)[4],
+                                          const uint32_t (&q)[4]) {
   asm volatile(
-      "ds_read_b128 %0, %4\n ds_read_b128 %1, %4 offset:4096\n"
-      "ds_read_b128 %2, %5\n ds_read_b128 %3, %5 offset:4096\n s_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
-      : "v"(pa), "v"(pb)
+      "ds_read_b128 %0, %8\n ds_read_b128 %4, %12\n ds_read_b128 %1, %9\n ds_read_b128 %5, %13\n"
+      "ds_read_b128 %2, %10\n ds_read_b128 %6, %14\n ds_read_b128 %3, %11\n ds_read_b128 %7, %15\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[0][2]), "=&v"(a[0][3]), "=&v"(b[0][0]),
+        "=&v"(b[0][1]), "=&v"(b[0][2]), "=&v"(b[0][3])
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3])
+      : "memory");
+}
+__device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[1][4], const uint32_t (&p)[4],
+                                          const uint32_t (&q)[4]) {
+  asm volatile(
+      "ds_read_b128 %0, %12\n ds_read_b128 %4, %12 offset:4096\n ds_read_b128 %8, %16\n"
+      "ds_read_b128 %1, %13\n ds_read_b128 %5, %13 offset:4096\n ds_read_b128 %9, %17\n"
+      "ds_read_b128 %2, %14\n ds_read_b128 %6, %14 offset:4096\n ds_read_b128 %10, %18\n"
+      "ds_read_b128 %3, %15\n ds_read_b128 %7, %15 offset:4096\n ds_read_b128 %11, %19\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[0][2]), "=&v"(a[0][3]), "=&v"(a[1][0]),
+        "=&v"(a[1][1]), "=&v"(a[1][2]), "=&v"(a[1][3]), "=&v"(b[0][0]), "=&v"(b[0][1]),
+        "=&v"(b[0][2]), "=&v"(b[0][3])
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3])
+      : "memory");
+}
+__device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[2][4], const uint32_t (&p)[4],
+                                          const uint32_t (&q)[4]) {
+  asm volatile(
+      "ds_read_b128 %0, %16\n ds_read_b128 %4, %16 offset:4096\n"
+      "ds_read_b128 %8, %20\n ds_read_b128 %12, %20 offset:4096\n"
+      "ds_read_b128 %1, %17\n ds_read_b128 %5, %17 offset:4096\n"
+      "ds_read_b128 %9, %21\n ds_read_b128 %13, %21 offset:4096\n"
+      "ds_read_b128 %2, %18\n ds_read_b128 %6, %18 offset:4096\n"
+      "ds_read_b128 %10, %22\n ds_read_b128 %14, %22 offset:4096\n"
+      "ds_read_b128 %3, %19\n ds_read_b128 %7, %19 offset:4096\n"
+      "ds_read_b128 %11, %23\n ds_read_b128 %15, %23 offset:4096\n s_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[0][2]), "=&v"(a[0][3]), "=&v"(a[1][0]),
+        "=&v"(a[1][1]), "=&v"(a[1][2]), "=&v"(a[1][3]), "=&v"(b[0][0]), "=&v"(b[0][1]),
+        "=&v"(b[0][2]), "=&v"(b[0][3]), "=&v"(b[1][0]), "=&v"(b[1][1]), "=&v"(b[1][2]),
+        "=&v"(b[1][3])
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3])
       : "memory");
 }
 
-// BM x BN tile, waves of WM x WN (32 x 32 or 64 x 64), S stage buffers of 128
+// BM x BN tile, waves of WM x WN (32 or 64 rows and columns), S stage buffers of 128
 // bytes per row (64 bf16 or 32 fp32 values of K), filled by buffer loads
 // straight into LDS, S - 1 stages ahead. Rows past M or N and chunks past K
 // lie outside the tile's buffer descriptor: they arrive as zeros and move no
@@ -140,7 +171,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   constexpr int STAGE = 128 * (BM + BN);
   constexpr int SPITCH = 4 * WN + 16;            // staging row: WN floats and one 16-byte pad
   static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && NW % 2 == 0, "whole 1-KB units per wave");
-  static_assert(TM == TN && (TM == 1 || TM == 2), "32 x 32 or 64 x 64 waves");
+  static_assert(TM <= 2 && TN <= TM, "32 x 32, 64 x 32 or 64 x 64 waves");
   static_assert(NW * 32 * SPITCH <= S * STAGE, "epilogue staging fits in the stage buffers");
   static_assert((S - 1) * L <= 63, "outstanding loads fit vmcnt");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
@@ -184,11 +215,13 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 
   const int lrow = lane & 31, lhalf = lane >> 5;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(smem));
-  uint32_t co[4];
+  uint32_t pa[4], pb[4];   // substep s of the wave's first rows of A and B in buffer 0
 #pragma unroll
-  for (int s = 0; s < 4; ++s) co[s] = uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
-  const uint32_t arow = lds0 + uint32_t((wm0 + lrow) * 128);
-  const uint32_t brow = lds0 + uint32_t((BM + wn0 + lrow) * 128);
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t co = lds0 + uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
+    pa[s] = co + uint32_t((wm0 + lrow) * 128);
+    pb[s] = co + uint32_t((BM + wn0 + lrow) * 128);
+  }
 
   v16f acc[TM][TN];
 #pragma unroll
@@ -196,38 +229,30 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 #pragma unroll
     for (int j = 0; j < TN; ++j)
       acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-  v4i af[2][TM], bf[2][TN];
-#define HL_READ(SET_, BUF_, S_)                                                              \
-  do {                                                                                       \
-    const uint32_t o_ = uint32_t((BUF_) * STAGE) + co[S_];                                   \
-    if constexpr (TM == 2)                                                                   \
-      lds_read4(af[SET_][0], af[SET_][TM - 1], bf[SET_][0], bf[SET_][TN - 1], arow + o_, brow + o_); \
-    else                                                                                     \
-      lds_read2(af[SET_][0], bf[SET_][0], arow + o_, brow + o_);                             \
-  } while (0)
 
 #pragma unroll
   for (int p = 0; p < S - 1; ++p) HL_ISSUE(p);
+  int buf = 0;
   for (int kt = 0; kt < KT; ++kt) {
     // stage kt has landed in every wave; every wave is done with stage kt - 1
     wait_vm_lgkm0<(S - 2) * L>();
     __builtin_amdgcn_s_barrier();
     HL_ISSUE(kt + S - 1);
-    const int buf = kt % S;
-    HL_READ(0, buf, 0);
+    const uint32_t o = uint32_t(buf * STAGE);
+    buf = buf == S - 1 ? 0 : buf + 1;
+    v4i af[TM][4], bf[TN][4];
+    const uint32_t qa[4] = {pa[0] + o, pa[1] + o, pa[2] + o, pa[3] + o};
+    const uint32_t qb[4] = {pb[0] + o, pb[1] + o, pb[2] + o, pb[3] + o};
+    lds_kstep(af, bf, qa, qb);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s < 3) HL_READ((s + 1) & 1, buf, s + 1);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = lin_mfma<TE>(bf[s & 1][j], af[s & 1][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        for (int j = 0; j < TN; ++j) acc[i][j] = lin_mfma<TE>(bf[j][s], af[i][s], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
   }
-#undef HL_READ
 #undef HL_ISSUE
   wait_vm_lgkm0<0>();  // no LDS write may land in the staging area (or after the block ends)
   __builtin_amdgcn_s_barrier();
@@ -542,11 +567,23 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 
 namespace {
 
-enum LinKind { LIN_ROWS, LIN_T32, LIN_T64, LIN_T128, LIN_PP3, LIN_PP4 };
+enum LinKind { LIN_ROWS, LIN_T32, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
 
-// Kernel and split count of a product. Rows up to 8 take the vector kernel.
-// Otherwise the tile shrinks until the tiles cover the 256 CUs, and a product
-// that still leaves CUs idle is split over K, at least 4 k-steps per split.
+// Kernel and split count of a product.
+//  up to 8 rows: the vector kernel.
+//  bf16 with 128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns,
+//    whichever's rounds of one tile per CU cost less.
+//  otherwise the tile shrinks until there is one per CU: bf16 64 x 128 (1037 x
+//    1160 -> 2312: 19.6 us against 22.8 for 64 x 64), fp32 128 x 128 (1024 x 4096
+//    -> 4096: 274 us against 281), then 64 x 64 (12288 x 256 -> 256 fp32: 20.4 us
+//    against 23.9 for 64 x 128), up to 32 rows 32 x 128.
+//  A product that still leaves CUs idle is split over K. A split costs a second
+//    launch and the partial sums, about 4 us, and a k-step 0.24 us (bf16) or
+//    0.35 us (fp32): so bf16 aims at one block per CU with 12 k-steps or more
+//    each (4 where there are less than 64 tiles), fp32 at two with 4 or more (512
+//    x 1152 -> 1152 bf16: 8.0 us unsplit against 10.6 in two; 64 x 4096 -> 4096:
+//    12.0 us in four against 14.2 in eight; 128 x 4096 -> 1152 fp32: 21.6 us in
+//    14 against 26.2 in eight).
 struct LinPlan {
   LinKind kind;
   int splits, kper;
@@ -554,24 +591,25 @@ struct LinPlan {
 LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   LinPlan p = {LIN_ROWS, 1, (K * esize + 127) / 128};
   if (M <= 8) return p;
+  const bool bf16 = esize == 2;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  int64_t t = tiles(128, 128);
-  p.kind = LIN_T128;
-  if (t < 256) {
-    p.kind = M <= 32 ? LIN_T32 : LIN_T64;
-    t = M <= 32 ? tiles(32, 128) : tiles(64, 64);
-  }
-  if (esize == 2 && tiles(256, 192) >= 128) {
-    // the wide tiles whose rounds of one per CU cost less
+  if (bf16 && tiles(256, 192) >= 128) {
     const int64_t r3 = (tiles(256, 192) + 255) / 256 * 3, r4 = (tiles(256, 256) + 255) / 256 * 4;
     p.kind = r3 < r4 ? LIN_PP3 : LIN_PP4;
     return p;
   }
+  if (bf16 ? tiles(64, 128) >= 256 : tiles(128, 128) >= 256) {
+    p.kind = bf16 ? LIN_T64X128 : LIN_T128;
+    return p;
+  }
+  p.kind = M <= 32 ? LIN_T32 : LIN_T64;
+  const int64_t t = M <= 32 ? tiles(32, 128) : tiles(64, 64);
   const int ksteps = p.kper;
   if (t < 256) {
-    int64_t want = 512 / t;
-    if (want > ksteps / 4) want = ksteps / 4;
-    if (want > 16) want = 16;
+    int64_t want = bf16 ? (256 + t / 2) / t : 512 / t;
+    const int64_t most = ksteps / (bf16 && t >= 64 ? 12 : 4);
+    if (want > most) want = most;
+    if (want > (bf16 ? 8 : 16)) want = bf16 ? 8 : 16;
     if (want > 1) {
       p.kper = int((ksteps + want - 1) / want);
       p.splits = (ksteps + p.kper - 1) / p.kper;
@@ -626,7 +664,14 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       break;
     case LIN_T32: launch_tile<TE, 32, 128, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
     case LIN_T64: launch_tile<TE, 64, 64, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
-    case LIN_T128: launch_tile<TE, 128, 128, 64, 64, 2, 2>(X, M, W, N, K, p, part, ep, s); break;
+    case LIN_T64X128:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 64, 128, 64, 32, 3, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
+    case LIN_T128:
+      if constexpr (sizeof(TE) == 4)
+        launch_tile<TE, 128, 128, 64, 64, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
   }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.splits > 1) {
