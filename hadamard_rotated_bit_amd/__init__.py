@@ -188,13 +188,10 @@ def quant_linear(desc: Desc, prepared: torch.Tensor, X: torch.Tensor,
                  epilogue: Optional["Epilogue"] = None) -> torch.Tensor:
     """Y = the quantised layer applied to X [T, d_in]; with ``epilogue``
     (hq_quant_linear_epi) Y = residual + gate * phi(layer(X))."""
+    if epilogue is not None:
+        return _quant_linear_epi(desc, prepared, X, out, workspace, epilogue)
     T = X.shape[0]
     _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
-    if epilogue is not None:
-        if _elsewhere(X):
-            with torch.cuda.device(X.device):
-                return _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue)
-        return _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue)
     if out is None:
         out = torch.empty(T, desc.d_out, dtype=_TORCH[desc.y_dtype], device=X.device)
     else:
@@ -378,24 +375,50 @@ def prepared_views(desc: Desc, prepared: torch.Tensor) -> dict:
 
 # ---- epilogues and dense layers ---------------------------------------------
 
-def _elsewhere(t: torch.Tensor) -> bool:
-    """Whether the tensor's device is not the current one (a call then runs
-    again under it: kernels launch on the current device)."""
-    return t.device.index != torch.cuda.current_device()
+def _fits(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    """_need, and that ``t`` is on GPU ``device``; one expression when it is."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous()):
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, X on cuda:{device}")
+
+
+def _gpu_of(X: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Checks X like _need; returns its GPU."""
+    device = X.get_device() if isinstance(X, torch.Tensor) else -1
+    if device < 0 or X.dtype is not dtype or X.shape != shape or not X.is_contiguous():
+        _need(X, name, dtype, shape)
+    return device
+
+
+def _workspace_of(workspace: Optional[torch.Tensor], nbytes: int, X: torch.Tensor, device: int):
+    """(tensor that keeps it alive, address, bytes) of a call's workspace,
+    allocated when it is needed and not given (the library checks its size)."""
+    if workspace is None:
+        if not nbytes:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    elif workspace.get_device() != device:
+        raise ValueError(f"workspace is on {workspace.device}, X on cuda:{device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device.index).cuda_stream
+# The current stream's handle without building a Stream object (0.1 us instead
+# of 1 us, a tenth of a small call), where torch has the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _same_device(ref: torch.Tensor, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, X on {ref.device}")
+def _stream_of(device: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 @dataclasses.dataclass(frozen=True)
@@ -409,10 +432,10 @@ class Epilogue:
     gate: Optional[torch.Tensor] = None
     gate_rows: int = 0
 
-    def _c(self, X: torch.Tensor, T: int, d_out: int, dtype: torch.dtype):
+    def _c(self, T: int, d_out: int, dtype: torch.dtype, device: int):
         g, r, ld = self.gate, self.residual, 0
         if r is not None:
-            _need(r, "residual", dtype, (T, d_out))
+            _fits(r, "residual", dtype, (T, d_out), device)
         if g is not None:
             if not isinstance(g, torch.Tensor) or not g.is_cuda or g.dtype != dtype:
                 raise ValueError(f"gate must be a CUDA (HIP) tensor of {dtype}")
@@ -421,27 +444,30 @@ class Epilogue:
                 raise ValueError(f"gate must have shape (>= {rows}, {d_out}), got {tuple(g.shape)}")
             if g.stride(1) != 1:
                 raise ValueError("gate rows must be contiguous")
+            if g.get_device() != device:
+                raise ValueError(f"gate is on {g.device}, X on cuda:{device}")
             ld = g.stride(0) if g.shape[0] > 1 else d_out
-        _same_device(X, residual=r, gate=g)
-        return ctypes.byref(_lib.HqEpilogue(self.act, r.data_ptr() if r is not None else None,
-                                            g.data_ptr() if g is not None else None,
-                                            self.gate_rows, ld))
+        return ctypes.byref(_lib.HqEpilogue(self.act, _addr(r), _addr(g), self.gate_rows, ld))
 
 
-def _quant_linear_epi(desc, prepared, X, T, out, workspace, epilogue):
+def _quant_linear_epi(desc, prepared, X, out, workspace, epilogue):
+    T = X.shape[0]
+    device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
+    if device != torch.cuda.current_device():   # kernels launch on the current device
+        with torch.cuda.device(device):
+            return _quant_linear_epi(desc, prepared, X, out, workspace, epilogue)
     ydt = _TORCH[desc.y_dtype]
     if out is None:
         out = torch.empty(T, desc.d_out, dtype=ydt, device=X.device)
     else:
-        _need(out, "out", ydt, (T, desc.d_out))
-    _same_device(X, prepared=prepared, out=out, workspace=workspace)
-    ep = epilogue._c(X, T, desc.d_out, ydt)
+        _fits(out, "out", ydt, (T, desc.d_out), device)
+    if prepared.get_device() != device:
+        raise ValueError(f"prepared is on {prepared.device}, X on cuda:{device}")
+    ep = epilogue._c(T, desc.d_out, ydt, device)
     lib = load()
-    if workspace is None:
-        workspace = torch.empty(max(lib.hq_workspace_bytes(desc._ref, T), 1), dtype=torch.uint8,
-                                device=X.device)
-    check(lib.hq_quant_linear_epi(desc._ref, _addr(prepared), _addr(X), T, ep, _addr(out),
-                                  _addr(workspace), workspace.nbytes, _stream_of(X)))
+    ws, ws_addr, ws_bytes = _workspace_of(workspace, lib.hq_workspace_bytes(desc._ref, T), X, device)
+    check(lib.hq_quant_linear_epi(desc._ref, prepared.data_ptr(), X.data_ptr(), T, ep,
+                                  out.data_ptr(), ws_addr, ws_bytes, _stream_of(device)))
     return out
 
 
@@ -479,28 +505,25 @@ def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
     quantised. ``workspace`` (linear_workspace_bytes(desc, T) bytes) is
     allocated when it is needed and not given."""
     T = X.shape[0]
-    _need(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
-    if _elsewhere(X):
-        with torch.cuda.device(X.device):
+    xdt = _TORCH[desc.x_dtype]
+    device = _gpu_of(X, "X", xdt, (T, desc.d_in))
+    if device != torch.cuda.current_device():   # kernels launch on the current device
+        with torch.cuda.device(device):
             return linear(desc, X, weight, bias, epilogue, out, workspace)
-    _need(weight, "weight", _TORCH[desc.w_dtype], (desc.d_out, desc.d_in))
+    _fits(weight, "weight", _TORCH[desc.w_dtype], (desc.d_out, desc.d_in), device)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (desc.d_out,))
+        _fits(bias, "bias", torch.float32, (desc.d_out,), device)
     ydt = _TORCH[desc.y_dtype]
     if out is None:
         out = torch.empty(T, desc.d_out, dtype=ydt, device=X.device)
     else:
-        _need(out, "out", ydt, (T, desc.d_out))
-    _same_device(X, weight=weight, bias=bias, out=out, workspace=workspace)
-    ep = None if epilogue is None else epilogue._c(X, T, desc.d_out, ydt)
+        _fits(out, "out", ydt, (T, desc.d_out), device)
+    ep = None if epilogue is None else epilogue._c(T, desc.d_out, ydt, device)
     lib = load()
-    if workspace is None:
-        n = lib.hq_linear_workspace_bytes(desc._ref, T)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
-    check(lib.hq_linear(desc._ref, _addr(X), _addr(weight), _addr(bias), T, ep, _addr(out),
-                        _addr(workspace), 0 if workspace is None else workspace.nbytes,
-                        _stream_of(X)))
+    ws, ws_addr, ws_bytes = _workspace_of(
+        workspace, lib.hq_linear_workspace_bytes(desc._ref, T), X, device)
+    check(lib.hq_linear(desc._ref, X.data_ptr(), weight.data_ptr(), _addr(bias), T, ep,
+                        out.data_ptr(), ws_addr, ws_bytes, _stream_of(device)))
     return out
 
 
@@ -540,29 +563,25 @@ def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = 
     needed and not given."""
     if X.dim() != 3:
         raise ValueError(f"X must be [samples, positions, channels], got {tuple(X.shape)}")
-    S, P = X.shape[0], X.shape[1]
-    _need(X, "X", _TORCH[desc.x_dtype], (S, P, desc.channels))
-    if _elsewhere(X):
-        with torch.cuda.device(X.device):
+    S, P, C = X.shape[0], X.shape[1], desc.channels
+    device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (S, P, C))
+    if device != torch.cuda.current_device():   # kernels launch on the current device
+        with torch.cuda.device(device):
             return group_norm(desc, X, gamma, beta, out, workspace)
     if gamma is not None:
-        _need(gamma, "gamma", torch.float32, (desc.channels,))
+        _fits(gamma, "gamma", torch.float32, (C,), device)
     if beta is not None:
-        _need(beta, "beta", torch.float32, (desc.channels,))
+        _fits(beta, "beta", torch.float32, (C,), device)
     ydt = _TORCH[desc.y_dtype]
     if out is None:
-        out = torch.empty(S, P, desc.channels, dtype=ydt, device=X.device)
+        out = torch.empty(S, P, C, dtype=ydt, device=X.device)
     else:
-        _need(out, "out", ydt, (S, P, desc.channels))
-    _same_device(X, gamma=gamma, beta=beta, out=out, workspace=workspace)
+        _fits(out, "out", ydt, (S, P, C), device)
     lib = load()
-    if workspace is None:
-        n = lib.hq_group_norm_workspace_bytes(desc._ref, S, P)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
-    check(lib.hq_group_norm(desc._ref, _addr(X), _addr(gamma), _addr(beta), S, P, _addr(out),
-                            _addr(workspace), 0 if workspace is None else workspace.nbytes,
-                            _stream_of(X)))
+    ws, ws_addr, ws_bytes = _workspace_of(
+        workspace, lib.hq_group_norm_workspace_bytes(desc._ref, S, P), X, device)
+    check(lib.hq_group_norm(desc._ref, X.data_ptr(), _addr(gamma), _addr(beta), S, P,
+                            out.data_ptr(), ws_addr, ws_bytes, _stream_of(device)))
     return out
 
 

@@ -83,22 +83,99 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__
 // ---- MFMA tiles -----------------------------------------------------------------
 //
 // Fragments: for a 32 x 128-byte piece of an operand, lane l holds row l % 32,
-// 16-byte chunk 2 s + l / 32 of substep s. In bf16 a chunk is the 8
-// consecutive k of one v_mfma_f32_32x32x16_bf16; in fp32 its 4 values enter
-// four v_mfma_f32_32x32x2_f32, whose k pairs are (chunk 2s, chunk 2s + 1)
-// value by value (the same map for both operands, so any pairing is the same
-// sum). The weight fragment is the first operand: lane l's accumulator r
-// belongs to row l % 32 and column 8 (r / 4) + 4 (l / 32) + r % 4.
-template <typename TE>
-__device__ __forceinline__ v16f lin_mfma(const v4i& w, const v4i& x, v16f c) {
+// 16-byte chunk 2 s + l / 32 of substep s = 0 .. 3. In bf16 a chunk is the 8
+// consecutive k of one v_mfma_f32_32x32x16_bf16. The weight fragment is the
+// first operand: lane l's accumulator r belongs to row l % 32 and column
+// 8 (r / 4) + 4 (l / 32) + r % 4.
+//
+// fp32 operands run on the bf16 matrix units too: x = h + m + l with h the
+// upper 16 bits of x (a bf16 by truncation), m those of x - h and l = x - h - m,
+// which has 8 bits left, all three exact. The product keeps
+//   x w = h h + (h m + m h) + (h l + m m + l h)
+// and leaves m l, l m and l l, at most 2^-22 and on average 2^-24 of |x w|, the
+// size of the fp32 rounding of the product itself; sums stay in fp32. Six MFMAs
+// of 32 cycles per 16 k instead of eight v_mfma_f32_32x32x2_f32 of 64 cycles.
+// (The split of an infinity is inf, NaN, NaN: an infinite operand gives NaN.)
+// The 8 values per lane are two chunks, substeps 2 t and 2 t + 1: any pairing
+// of k is the same sum, as both operands use the same one.
+struct Split {
+  v8bf h, m, l;
+};
+__device__ __forceinline__ Split split8(const v4i& c0, const v4i& c1) {
+  uint32_t h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x0 = uint32_t(i < 2 ? c0[2 * i] : c1[2 * i - 4]);
+    const uint32_t x1 = uint32_t(i < 2 ? c0[2 * i + 1] : c1[2 * i - 3]);
+    const float r0 = __uint_as_float(x0) - __uint_as_float(x0 & 0xFFFF0000u);
+    const float r1 = __uint_as_float(x1) - __uint_as_float(x1 & 0xFFFF0000u);
+    const uint32_t b0 = __float_as_uint(r0), b1 = __float_as_uint(r1);
+    const float l0 = r0 - __uint_as_float(b0 & 0xFFFF0000u);
+    const float l1 = r1 - __uint_as_float(b1 & 0xFFFF0000u);
+    h[i] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);   // the upper halves of a pair
+    m[i] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+    l[i] = __builtin_amdgcn_perm(__float_as_uint(l1), __float_as_uint(l0), 0x07060302u);
+  }
+  Split s;
+  s.h = __builtin_bit_cast(v8bf, make_uint4(h[0], h[1], h[2], h[3]));
+  s.m = __builtin_bit_cast(v8bf, make_uint4(m[0], m[1], m[2], m[3]));
+  s.l = __builtin_bit_cast(v8bf, make_uint4(l[0], l[1], l[2], l[3]));
+  return s;
+}
+
+__device__ __forceinline__ v16f mfma_bf16(const v8bf& w, const v8bf& x, const v16f& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, c, 0, 0, 0);
+}
+
+// Instruction order: NM MFMAs with NV vector instructions spread between them.
+template <int I, int NM, int NV>
+__device__ __forceinline__ void mfma_valu_interleave() {
+  if constexpr (I < NM) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int v = (I + 1) * NV / NM - I * NV / NM;
+    __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    mfma_valu_interleave<I + 1, NM, NV>();
+  }
+}
+
+// The products of one k-step.
+template <typename TE, int TM, int TN>
+__device__ __forceinline__ void lin_kstep(v16f (&acc)[TM][TN], const v4i (&a)[TM][4],
+                                          const v4i (&b)[TN][4]) {
   if constexpr (sizeof(TE) == 2) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w),
-                                                   __builtin_bit_cast(v8bf, x), c, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = mfma_bf16(__builtin_bit_cast(v8bf, b[j][s]), __builtin_bit_cast(v8bf, a[i][s]),
+                                acc[i][j]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(w[e]), __int_as_float(x[e]), c, 0, 0, 0);
-    return c;
+    for (int t = 0; t < 2; ++t) {
+      Split x[TM], w[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) x[i] = split8(a[i][2 * t], a[i][2 * t + 1]);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) w[j] = split8(b[j][2 * t], b[j][2 * t + 1]);
+      // the small terms first, each over all tiles before the next
+#define HL_TERM(W_, X_)                                                     \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i)                            \
+      _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] = mfma_bf16(w[j].W_, x[i].X_, acc[i][j])
+      HL_TERM(l, h);
+      HL_TERM(m, m);
+      HL_TERM(h, l);
+      HL_TERM(m, h);
+      HL_TERM(h, m);
+      HL_TERM(h, h);
+#undef HL_TERM
+    }
+    // the second half's split runs between the first half's MFMAs
+    constexpr int NM = 6 * TM * TN, NV = 44 * (TM + TN);
+    __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
+    mfma_valu_interleave<0, NM, NV>();
+    __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
   }
 }
 
@@ -245,12 +322,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
     const uint32_t qb[4] = {pb[0] + o, pb[1] + o, pb[2] + o, pb[3] + o};
     lds_kstep(af, bf, qa, qb);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = lin_mfma<TE>(bf[j][s], af[i][s], acc[i][j]);
+    lin_kstep<TE, TM, TN>(acc, af, bf);
     __builtin_amdgcn_sched_barrier(0);
   }
 #undef HL_ISSUE
@@ -490,7 +562,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[i][P] = lin_mfma<uint16_t>(bf[s], af[SET][i][s], acc[i][P]);
+      for (int i = 0; i < 2; ++i)
+        acc[i][P] = mfma_bf16(__builtin_bit_cast(v8bf, bf[s]),
+                              __builtin_bit_cast(v8bf, af[SET][i][s]), acc[i][P]);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();

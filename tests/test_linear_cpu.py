@@ -102,6 +102,6 @@ def test_python_refusals():
     with pytest.raises(ValueError, match="CUDA"):
         hq.linear(d, X, torch.zeros(32, 64))
     with pytest.raises(ValueError, match="residual"):
-        hq.Epilogue(residual=torch.zeros(4, 32))._c(X, 4, 32, torch.float32)
+        hq.Epilogue(residual=torch.zeros(4, 32))._c(4, 32, torch.float32, 0)
     with pytest.raises(ValueError, match="gate"):
-        hq.Epilogue(gate=torch.zeros(1, 32), gate_rows=4)._c(X, 4, 32, torch.float32)
+        hq.Epilogue(gate=torch.zeros(1, 32), gate_rows=4)._c(4, 32, torch.float32, 0)
