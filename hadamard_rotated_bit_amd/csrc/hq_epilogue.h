@@ -78,6 +78,25 @@ __device__ __forceinline__ void apply_act(float (&v)[N], const ActCoef& a) {
   }
 }
 
+// Eight consecutive elements as loaded.
+template <typename TE>
+struct Raw8 {
+  uint4 q[sizeof(TE) / 2];
+};
+template <typename TE>
+__device__ __forceinline__ Raw8<TE> raw_load(const TE* p) {
+  Raw8<TE> r;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void raw_get(const Raw8<uint16_t>& r, float v[8]) {
+  load8(reinterpret_cast<const uint16_t*>(&r.q[0]), v);
+}
+__device__ __forceinline__ void raw_get(const Raw8<float>& r, float v[8]) {
+  load8(reinterpret_cast<const float*>(&r.q[0]), v);
+}
+
 __device__ __forceinline__ void store8(float* __restrict__ p, const float v[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -87,39 +106,82 @@ __device__ __forceinline__ void store8(uint16_t* __restrict__ p, const float v[8
                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Eight consecutive outputs n .. n+7 (n a multiple of 8) of row m, from the
-// product v: bias, phi, gate, residual, one rounding, one 16- or 32-byte
-// store. The residual is read right before the store by the lane that writes
-// the same elements, so Y may be the residual's own buffer.
-template <typename TY>
-__device__ __forceinline__ void finish8_as(float (&v)[8], int64_t m, int64_t n, int64_t N,
-                                           const LinEpi& ep) {
-  if (ep.bias) {
-    float b[8];
-    load8(ep.bias + n, b);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += b[k];
-  }
-  apply_act<8, sizeof(TY) == 4>(v, ep.act);
-  if (ep.gate) {
-    float g[8];
-    load8(static_cast<const TY*>(ep.gate) + int64_t(uint32_t(m) / uint32_t(ep.gate_rows)) * ep.gate_ld + n, g);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= g[k];
-  }
+// Q pieces of eight consecutive outputs each (columns n[q] .. n[q] + 7, n a
+// multiple of 8, of row m[q]; ok[q]: inside the output) from v, the product with
+// its bias: phi, gate, residual, one rounding, one 16- or 32-byte store. All
+// loads come before the first store: Y may be the residual's own buffer, so the
+// compiler cannot move a later piece's loads above an earlier one's store, and
+// each piece would wait for its own residual. Every element is read by the lane
+// that writes it.
+template <typename TY, int Q>
+__device__ __forceinline__ void finish8(float (&v)[Q][8], const int64_t (&m)[Q],
+                                        const int64_t (&n)[Q], const bool (&ok)[Q], int64_t N,
+                                        const LinEpi& ep) {
+  Raw8<TY> r[Q], g[Q];
   if (ep.residual) {
-    float r[8];
-    load8(static_cast<const TY*>(ep.residual) + m * N + n, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += r[k];
+    for (int q = 0; q < Q; ++q)
+      if (ok[q]) r[q] = raw_load(static_cast<const TY*>(ep.residual) + m[q] * N + n[q]);
   }
-  store8(static_cast<TY*>(ep.Y) + m * N + n, v);
+  if (ep.gate) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (ok[q])
+        g[q] = raw_load(static_cast<const TY*>(ep.gate) +
+                        int64_t(uint32_t(m[q]) / uint32_t(ep.gate_rows)) * ep.gate_ld + n[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (!ok[q]) continue;
+    float t[8];
+    apply_act<8, sizeof(TY) == 4>(v[q], ep.act);
+    if (ep.gate) {
+      raw_get(g[q], t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[q][k] *= t[k];
+    }
+    if (ep.residual) {
+      raw_get(r[q], t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[q][k] += t[k];
+    }
+    store8(static_cast<TY*>(ep.Y) + m[q] * N + n[q], v[q]);
+  }
 }
 
-__device__ __forceinline__ void finish8(float (&v)[8], int64_t m, int64_t n, int64_t N,
-                                        const LinEpi& ep) {
-  if (ep.y_bf16) finish8_as<uint16_t>(v, m, n, N, ep);
-  else finish8_as<float>(v, m, n, N, ep);
+// A wave's 32 rows x (8 LPR) columns, staged as fp32 rows of `pitch` floats, as
+// rows again: eight consecutive columns per lane, whole row segments per store,
+// Q pieces at a time. Rows from m0, columns from n0.
+template <typename TY, int LPR, int Q>
+__device__ __forceinline__ void finish_rows_as(const float* stg, int pitch, int lane, int64_t m0,
+                                               int64_t n0, int64_t M, int64_t N, const LinEpi& ep) {
+  constexpr int NQ = 32 * LPR / 64;             // pieces per lane
+  static_assert(NQ % Q == 0, "whole groups");
+#pragma unroll 1
+  for (int q0 = 0; q0 < NQ; q0 += Q) {
+    float v[Q][8];
+    int64_t m[Q], n[Q];
+    bool ok[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = lane + 64 * (q0 + q), r = i / LPR, c = 8 * (i - r * LPR);
+      m[q] = m0 + r;
+      n[q] = n0 + c;
+      ok[q] = m[q] < M && n[q] < N;
+      load8(stg + r * pitch + c, v[q]);
+    }
+    finish8<TY, Q>(v, m, n, ok, N, ep);
+  }
+}
+// Q: pieces at a time for bf16 results, what the kernel's registers leave room
+// for; fp32 ones take half as many.
+template <int LPR, int Q>
+__device__ __forceinline__ void finish_rows(const float* stg, int pitch, int lane, int64_t m0,
+                                            int64_t n0, int64_t M, int64_t N, const LinEpi& ep) {
+  if (ep.y_bf16)
+    finish_rows_as<uint16_t, LPR, Q>(stg, pitch, lane, m0, n0, M, N, ep);
+  else
+    finish_rows_as<float, LPR, Q % 2 ? 1 : Q / 2>(stg, pitch, lane, m0, n0, M, N, ep);
 }
 
 // One output, the same steps.

@@ -276,7 +276,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_f6g_kernel(
 #undef HG_ISSUE
 
   if constexpr (EXT) {
-    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
+    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE, 2>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
     return;
   }
   if (ep.y_bf16) {

@@ -170,8 +170,8 @@ __device__ __forceinline__ void gemm_epilogue(AccT (&acc)[TM][TN], uint8_t* smem
 // idle LDS that belongs to the wave and taken back as rows of eight columns
 // per lane, so that residual, gate and Y move in whole row segments and phi is
 // written once, in a rolled loop (unrolled over the accumulators its code
-// overflowed the registers). LDSB: bytes of LDS there are.
-template <int BM, int BN, int TM, int TN, int NW, int LDSB, typename AccT>
+// overflowed the registers). LDSB: bytes of LDS there are; Q: see finish_rows.
+template <int BM, int BN, int TM, int TN, int NW, int LDSB, int Q, typename AccT>
 __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* smem, int tid,
                                                   int lane, int64_t m0, int64_t n0, int wm0,
                                                   int wn0, int64_t M, int64_t N,
@@ -235,17 +235,7 @@ __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* 
       }
     }
     __builtin_amdgcn_wave_barrier();
-    constexpr int LPR = 4 * TN;               // lanes per row
-#pragma unroll 1
-    for (int q = lane; q < 32 * LPR; q += 64) {
-      const int r = q / LPR, c = 8 * (q - r * LPR);
-      const int64_t m = m0 + wm0 + 32 * i + r, n = n0 + wn0 + c;
-      if (m < M && n < N) {
-        float v[8];
-        load8(stg + r * PITCH + c, v);
-        finish8(v, m, n, N, ep.lin);
-      }
-    }
+    finish_rows<4 * TN, Q>(stg, PITCH, lane, m0 + wm0 + 32 * i, n0 + wn0, M, N, ep.lin);
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -521,7 +511,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void gemm_i8_kernel(
 #undef HQ_ISSUE_STAGE
 
   if constexpr (EXT)
-    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
+    gemm_epilogue_ext<BM, BN, TM, TN, NW, S * STAGE, 2>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, ep);
   else
     gemm_epilogue<BM, BN, TM, TN, NW, DEQ>(acc, smem, tid, lane, m0, n0, wm0, wn0, M, N, Cout, ldc, ep);
 }

@@ -17,14 +17,15 @@ namespace hq {
 // ---- few rows ------------------------------------------------------------------
 //
 // One wave owns NC output columns and all TT rows; its lanes split K in
-// 16-byte (bf16) or 32-byte (fp32) pieces, U pieces of 512 elements loaded
-// before the first is used. The wave's sums meet in a fixed lane tree. Bound
-// by reading W once (N K elements); X is read by every wave from L2.
+// pieces of 8 elements, U pieces of 512 per wave and pass, all of W's and X's
+// loads of a pass in flight before the first is used. The wave's sums meet in a
+// fixed lane tree. Bound by reading W once (N K elements); X is read by every
+// wave from L2.
 template <typename TE, int TT, int NC>
 __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__ X, int M,
                                                           const TE* __restrict__ W, int64_t N,
                                                           int K, LinEpi ep) {
-  constexpr int U = 4;
+  constexpr int U = TT <= 2 ? 4 : TT == 4 ? 3 : 2;   // bounded by the registers of the X pieces
   const int lane = threadIdx.x & 63;
   const int64_t n0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * NC;
   if (n0 >= N) return;
@@ -40,29 +41,31 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[t][c] = 0.0f;
   for (int kb = lane * 8; kb < K; kb += 512 * U) {
-    float w[U][NC][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (kb + 512 * u < K) {
-          load8(wp[c] + kb + 512 * u, w[u][c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[u][c][e] = 0.0f;
-        }
-      }
+    Raw8<TE> w[U][NC], x[U][TT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kb + 512 * u >= K) break;
+      if (kb + 512 * u < K) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        float x[8];
-        load8(xp[t] + kb + 512 * u, x);
+        for (int c = 0; c < NC; ++c) w[u][c] = raw_load(wp[c] + kb + 512 * u);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int t = 0; t < TT; ++t) x[u][t] = raw_load(xp[t] + kb + 512 * u);
+      }
+    }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[t][c] = fmaf(x[e], w[u][c][e], acc[t][c]);
+    for (int u = 0; u < U; ++u) {
+      if (kb + 512 * u < K) {
+        float wf[NC][8];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) raw_get(w[u][c], wf[c]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          float xf[8];
+          raw_get(x[u][t], xf);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[t][c] = fmaf(xf[e], wf[c][e], acc[t][c]);
+        }
       }
     }
   }
@@ -125,6 +128,41 @@ __device__ __forceinline__ Split split8(const v4i& c0, const v4i& c1) {
 
 __device__ __forceinline__ v16f mfma_bf16(const v8bf& w, const v8bf& x, const v16f& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, c, 0, 0, 0);
+}
+
+// Accumulators started at the bias: register r of strip j belongs to column
+// n + 32 j + 8 (r / 4) + r % 4 (the same for every row), zero without a bias.
+template <int TM, int TN>
+__device__ __forceinline__ void bias_acc(v16f (&acc)[TM][TN], const float* __restrict__ bias,
+                                         int64_t n, int64_t N) {
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int64_t c = n + 32 * j + 8 * g;
+      const float4 b = bias && c < N ? *reinterpret_cast<const float4*>(bias + c)
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      acc[0][j][4 * g] = b.x;
+      acc[0][j][4 * g + 1] = b.y;
+      acc[0][j][4 * g + 2] = b.z;
+      acc[0][j][4 * g + 3] = b.w;
+    }
+#pragma unroll
+    for (int i = 1; i < TM; ++i) acc[i][j] = acc[0][j];
+  }
+}
+
+// A wave's staged 32 rows as raw sums into part [M, N].
+template <int LPR>
+__device__ __forceinline__ void store_part(const float* stg, int pitch, int lane, int64_t m0,
+                                           int64_t n0, int64_t M, int64_t N, float* part) {
+#pragma unroll
+  for (int q = 0; q < 32 * LPR / 64; ++q) {
+    const int i = lane + 64 * q, r = i / LPR, c = 8 * (i - r * LPR);
+    float v[8];
+    load8(stg + r * pitch + c, v);
+    if (m0 + r < M && n0 + c < N) store8(part + (m0 + r) * N + n0 + c, v);
+  }
 }
 
 // Instruction order: NM MFMAs with NV vector instructions spread between them.
@@ -300,15 +338,10 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
     pb[s] = co + uint32_t((BM + wn0 + lrow) * 128);
   }
 
-  v16f acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-
 #pragma unroll
   for (int p = 0; p < S - 1; ++p) HL_ISSUE(p);
+  v16f acc[TM][TN];
+  bias_acc<TM, TN>(acc, part ? nullptr : ep.bias, n0 + wn0 + 4 * lhalf, N);
   int buf = 0;
   for (int kt = 0; kt < KT; ++kt) {
     // stage kt has landed in every wave; every wave is done with stage kt - 1
@@ -333,7 +366,6 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   // them back as rows, eight consecutive columns per lane: whole row segments
   // per store, and one epilogue for every kernel.
   float* const stg = reinterpret_cast<float*>(smem + wv * 32 * SPITCH);
-  constexpr int LPR = WN / 8;                    // lanes per row
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -344,19 +376,11 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
             make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                         acc[i][j][4 * g + 3]);
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < 32 * LPR / 64; ++q) {
-      const int r = (lane + 64 * q) / LPR, c = 8 * ((lane + 64 * q) % LPR);
-      const int64_t m = m0 + wm0 + 32 * i + r, n = n0 + wn0 + c;
-      float v[8];
-      load8(stg + r * (SPITCH / 4) + c, v);
-      if (m < M && n < N) {
-        if (part)
-          store8(part + (int64_t(blockIdx.y) * M + m) * N + n, v);
-        else
-          finish8(v, m, n, N, ep);
-      }
-    }
+    const int64_t mr = m0 + wm0 + 32 * i, nc = n0 + wn0;
+    if (part)
+      store_part<WN / 8>(stg, SPITCH / 4, lane, mr, nc, M, N, part + int64_t(blockIdx.y) * M * N);
+    else
+      finish_rows<WN / 8, WN == 32 ? 2 : 4>(stg, SPITCH / 4, lane, mr, nc, M, N, ep);
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -498,11 +522,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 
   v16f acc[2][NP];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-      acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  bias_acc<2, NP>(acc, ep.bias, n0 + wn * WN + 4 * lhalf, N);
   v4i af[2][2][4], bf[4];
 
   // the order of steady k-steps -3, -2 and -1
@@ -593,7 +613,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   __builtin_amdgcn_s_barrier();
 
   float* const stg = reinterpret_cast<float*>(smem + wv * 32 * SPITCH);
-  constexpr int LPR = WN / 8;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -604,14 +623,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                         acc[i][j][4 * g + 3]);
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 4
-    for (int q = 0; q < 32 * LPR / 64; ++q) {
-      const int r = (lane + 64 * q) / LPR, c = 8 * ((lane + 64 * q) % LPR);
-      const int64_t m = m0 + wm * 64 + 32 * i + r, n = n0 + wn * WN + c;
-      float v[8];
-      load8(stg + r * (SPITCH / 4) + c, v);
-      if (m < M && n < N) finish8(v, m, n, N, ep);
-    }
+    finish_rows<WN / 8, NP == 4 ? 4 : 3>(stg, SPITCH / 4, lane, m0 + wm * 64 + 32 * i, n0 + wn * WN, M,
+                                         N, ep);
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -624,17 +637,19 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t npr = N / 8;
   if (i >= M * npr) return;
-  const int64_t m = i / npr, n = (i - m * npr) * 8;
-  const float* p = part + m * N + n;
-  float v[8];
-  load8(p, v);
-  for (int s = 1; s < splits; ++s) {
+  const int64_t m[1] = {i / npr}, n[1] = {(i - m[0] * npr) * 8};
+  const bool ok[1] = {true};
+  const float* p = part + m[0] * N + n[0];
+  float v[1][8] = {};
+  if (ep.bias) load8(ep.bias + n[0], v[0]);
+  for (int s = 0; s < splits; ++s) {
     float a[8];
     load8(p + int64_t(s) * M * N, a);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += a[e];
+    for (int e = 0; e < 8; ++e) v[0][e] += a[e];
   }
-  finish8(v, m, n, N, ep);
+  if (ep.y_bf16) finish8<uint16_t, 1>(v, m, n, ok, N, ep);
+  else finish8<float, 1>(v, m, n, ok, N, ep);
 }
 
 // ---- host side --------------------------------------------------------------------

@@ -43,25 +43,6 @@ struct NormKArgs {
   int slab;             // channels per block (norm_block_kernel)
 };
 
-// Eight channels as loaded.
-template <typename TE>
-struct Raw8 {
-  uint4 q[sizeof(TE) / 2];
-};
-template <typename TE>
-__device__ __forceinline__ Raw8<TE> raw_load(const TE* p) {
-  Raw8<TE> r;
-#pragma unroll
-  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
-  return r;
-}
-__device__ __forceinline__ void raw_get(const Raw8<uint16_t>& r, float v[8]) {
-  load8(reinterpret_cast<const uint16_t*>(&r.q[0]), v);
-}
-__device__ __forceinline__ void raw_get(const Raw8<float>& r, float v[8]) {
-  load8(reinterpret_cast<const float*>(&r.q[0]), v);
-}
-
 // A lane's 8 channels are taken in units of U = gcd(C / G, 8) channels: a unit
 // lies within one group, so its channels share one mean and one M2 (NS = 8 / U
 // of them per lane: 1 where the group width is a multiple of 8, 4 at 10).
