@@ -26,7 +26,8 @@ __device__ __forceinline__ float relu_f32(float x) { return x < 0.0f ? 0.0f : x;
 template <int DEG>
 __device__ __forceinline__ float act_sigmoid(float x, const ActCoef& a) {
   float p = a.c[DEG];
-  if constexpr (DEG > 0) {
+  if constexpr (DEG == 1) p = fmaf(p, x * x, a.c[0]);   // an infinite square saturates as it should
+  if constexpr (DEG > 1) {
     const float t = fminf(x * x, a.tmax);
 #pragma unroll
     for (int k = DEG - 1; k >= 0; --k) p = fmaf(p, t, a.c[k]);

@@ -395,7 +395,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 //   L_p  issue this phase's stage loads, read strip p of B and a share of the
 //        next k-step's A (into the register set that the MFMAs do not use),
 //        wait, barrier
-//   M_p  8 MFMAs (64 rows x 32 columns x 64 k), barrier
+//   M_p  16 MFMAs (64 rows x 32 columns x 64 k), barrier
 // The L parts are kept even (2 or 3 loads, 6 or 8 fragment reads), since an
 // interval lasts as long as the longer of the two halves' parts.
 // A piece of a buffer is refilled once its last reader has passed a barrier:
@@ -409,40 +409,49 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 // are stored half by half (rows 64 r + 32 i + .. of half i together), those of
 // B strip by strip, so that each piece is one contiguous range.
 
-// Fragments from the given addresses (a strip of B, then a share of A) and the
-// wait for all of them.
+// The MFMA is v_mfma_f32_16x16x32_bf16: under the chip's power limit, with every
+// CU busy, it sustains 1.87 PFLOP/s on random operands against 1.61 for 32x32x16
+// (registers only), and square4k-sized products run into that limit. A
+// fragment is 16 rows of 32 k: lane l holds chunk l / 16 + 4 s of row l % 16;
+// fragment 2 rb + s of a 32-row piece is row block rb, k half s. The weight
+// fragment is the first operand: lane l's accumulator r belongs to row l % 16
+// and column 4 (l / 16) + r of its 16 x 16 block.
+
+// Fragments of a piece from the addresses p of its k halves (OFF: the piece; the
+// second row block is 2048 bytes on), all four or a strip of B's four and one
+// row block of A's or all of them, and the wait for all of them.
 template <int OFF>
-__device__ __forceinline__ void lds_frag4(v4i (&f)[4], const uint32_t (&p)[4]) {
+__device__ __forceinline__ void lds_frag4(v4i (&f)[4], const uint32_t (&p)[2]) {
   asm volatile(
-      "ds_read_b128 %0, %4 offset:%8\n ds_read_b128 %1, %5 offset:%8\n"
-      "ds_read_b128 %2, %6 offset:%8\n ds_read_b128 %3, %7 offset:%8\n s_waitcnt lgkmcnt(0)"
+      "ds_read_b128 %0, %4 offset:%6\n ds_read_b128 %1, %5 offset:%6\n"
+      "ds_read_b128 %2, %4 offset:%7\n ds_read_b128 %3, %5 offset:%7\n s_waitcnt lgkmcnt(0)"
       : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
-      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "n"(OFF)
+      : "v"(p[0]), "v"(p[1]), "n"(OFF), "n"(OFF + 2048)
       : "memory");
 }
-template <int OFFA, int OFFB>
-__device__ __forceinline__ void lds_frag6(v4i (&f)[4], const uint32_t (&p)[4], v4i& g0, v4i& g1,
-                                          uint32_t q0, uint32_t q1) {
+template <int OFFB, int OFFA>
+__device__ __forceinline__ void lds_frag6(v4i (&f)[4], const uint32_t (&p)[2], v4i& g0, v4i& g1,
+                                          const uint32_t (&q)[2]) {
   asm volatile(
-      "ds_read_b128 %0, %6 offset:%12\n ds_read_b128 %1, %7 offset:%12\n"
-      "ds_read_b128 %2, %8 offset:%12\n ds_read_b128 %3, %9 offset:%12\n"
-      "ds_read_b128 %4, %10 offset:%13\n ds_read_b128 %5, %11 offset:%13\n s_waitcnt lgkmcnt(0)"
+      "ds_read_b128 %0, %6 offset:%10\n ds_read_b128 %1, %7 offset:%10\n"
+      "ds_read_b128 %2, %6 offset:%11\n ds_read_b128 %3, %7 offset:%11\n"
+      "ds_read_b128 %4, %8 offset:%12\n ds_read_b128 %5, %9 offset:%12\n s_waitcnt lgkmcnt(0)"
       : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(g0), "=&v"(g1)
-      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q0), "v"(q1), "n"(OFFA), "n"(OFFB)
+      : "v"(p[0]), "v"(p[1]), "v"(q[0]), "v"(q[1]), "n"(OFFB), "n"(OFFB + 2048), "n"(OFFA)
       : "memory");
 }
-template <int OFFA, int OFFB>
-__device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[4], v4i (&g)[4],
-                                          const uint32_t (&q)[4]) {
+template <int OFFB, int OFFA>
+__device__ __forceinline__ void lds_frag8(v4i (&f)[4], const uint32_t (&p)[2], v4i (&g)[4],
+                                          const uint32_t (&q)[2]) {
   asm volatile(
-      "ds_read_b128 %0, %8 offset:%16\n ds_read_b128 %1, %9 offset:%16\n"
-      "ds_read_b128 %2, %10 offset:%16\n ds_read_b128 %3, %11 offset:%16\n"
-      "ds_read_b128 %4, %12 offset:%17\n ds_read_b128 %5, %13 offset:%17\n"
-      "ds_read_b128 %6, %14 offset:%17\n ds_read_b128 %7, %15 offset:%17\n s_waitcnt lgkmcnt(0)"
+      "ds_read_b128 %0, %8 offset:%12\n ds_read_b128 %1, %9 offset:%12\n"
+      "ds_read_b128 %2, %8 offset:%13\n ds_read_b128 %3, %9 offset:%13\n"
+      "ds_read_b128 %4, %10 offset:%14\n ds_read_b128 %5, %11 offset:%14\n"
+      "ds_read_b128 %6, %10 offset:%15\n ds_read_b128 %7, %11 offset:%15\n s_waitcnt lgkmcnt(0)"
       : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(g[0]), "=&v"(g[1]), "=&v"(g[2]),
         "=&v"(g[3])
-      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]),
-        "n"(OFFA), "n"(OFFB)
+      : "v"(p[0]), "v"(p[1]), "v"(q[0]), "v"(q[1]), "n"(OFFB), "n"(OFFB + 2048), "n"(OFFA),
+        "n"(OFFA + 2048)
       : "memory");
 }
 
@@ -511,18 +520,25 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   constexpr std::false_type slow{};
   constexpr std::true_type fast{};
 
-  const int lrow = lane & 31, lhalf = lane >> 5;
+  const int lrow = lane & 15, lquad = lane >> 4;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(smem));
-  uint32_t pa[4], pb[4];
+  uint32_t pa[2], pb[2];   // k half s of the wave's first rows in this stage's buffer
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint32_t co = lds0 + uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
+  for (int s = 0; s < 2; ++s) {
+    const uint32_t co = lds0 + uint32_t(((lquad + 4 * s) ^ (lrow >> 1)) * 16);
     pa[s] = co + uint32_t((wm * 32 + lrow) * 128);
     pb[s] = co + uint32_t((wn * 32 + lrow) * 128);
   }
 
-  v16f acc[2][NP];
-  bias_acc<2, NP>(acc, ep.bias, n0 + wn * WN + 4 * lhalf, N);
+  // accumulators of 16 x 16 block (row block i, column block j), from the bias
+  v4f acc[4][2 * NP];
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j) {
+    const int64_t n = n0 + wn * WN + 16 * j + 4 * lquad;
+    const v4f b = ep.bias && n < N ? *reinterpret_cast<const v4f*>(ep.bias + n) : v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][j] = b;
+  }
   v4i af[2][2][4], bf[4];
 
   // the order of steady k-steps -3, -2 and -1
@@ -560,17 +576,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if constexpr (P == 2) issue_a(fc, 0, 0, kt + 3);
     if constexpr (P == NP - 1) issue_a(fc, 0, 1, kt + 3);
     // pa, pb: this stage's buffer
+    const uint32_t pn[2] = {pa[0] ^ STAGE, pa[1] ^ STAGE};
     if constexpr (NP == 3 && P == 2) {
-      const uint32_t pn[4] = {pa[0] ^ STAGE, pa[1] ^ STAGE, pa[2] ^ STAGE, pa[3] ^ STAGE};
       lds_frag8<ASZ + P * 8192, ASZ / 2>(bf, pb, af[1 - SET][1], pn);
     } else {
-      constexpr int I = P / 2, F = 2 * (P % 2);
-      lds_frag6<ASZ + P * 8192, I * (ASZ / 2)>(bf, pb, af[1 - SET][I][F], af[1 - SET][I][F + 1],
-                                               pa[F] ^ STAGE, pa[F + 1] ^ STAGE);
+      constexpr int I = P / 2, RB = P % 2;
+      lds_frag6<ASZ + P * 8192, I * (ASZ / 2) + RB * 2048>(bf, pb, af[1 - SET][I][2 * RB],
+                                                           af[1 - SET][I][2 * RB + 1], pn);
     }
     if constexpr (P == NP - 1) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < 2; ++s) {
         pa[s] ^= STAGE;
         pb[s] ^= STAGE;
       }
@@ -580,11 +596,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        acc[i][P] = mfma_bf16(__builtin_bit_cast(v8bf, bf[s]),
-                              __builtin_bit_cast(v8bf, af[SET][i][s]), acc[i][P]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][2 * P + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(v8bf, bf[2 * j + s]),
+              __builtin_bit_cast(v8bf, af[SET][i / 2][2 * (i % 2) + s]), acc[i][2 * P + j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
@@ -616,12 +635,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
+    for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4*>(stg + lrow * (SPITCH / 4) + j * 32 + 8 * g + 4 * lhalf) =
-            make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                        acc[i][j][4 * g + 3]);
+      for (int j = 0; j < 2 * NP; ++j)
+        *reinterpret_cast<v4f*>(stg + (16 * rb + lrow) * (SPITCH / 4) + 16 * j + 4 * lquad) =
+            acc[2 * i + rb][j];
     __builtin_amdgcn_wave_barrier();
     finish_rows<WN / 8, NP == 4 ? 4 : 3>(stg, SPITCH / 4, lane, m0 + wm * 64 + 32 * i, n0 + wn * WN, M,
                                          N, ep);
@@ -798,7 +816,6 @@ ActCoef act_coef(int act) {
   if (act == ACT_SILU) {
     a.c[0] = -log2e;
   } else if (act == ACT_GELU_TANH) {
-    a.tmax = 1e6f;   // 2^(x P) is 0 or infinite long before; keeps x^2 finite
     a.c[0] = -1.5957691216057308f * log2e;
     a.c[1] = -1.5957691216057308f * 0.044715f * log2e;
   } else if (act == ACT_GELU) {
