@@ -954,6 +954,11 @@ int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, con
   if (need && (!workspace || workspace_bytes < need))
     return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
                 workspace ? workspace_bytes : size_t(0), need);
+  if (need && (overlap(workspace, need, Y, ny) || overlap(workspace, need, X, size_t(T) * din * es) ||
+               overlap(workspace, need, weight, din * dout * es) ||
+               overlap(workspace, need, bias, 4 * dout) ||
+               overlap(workspace, need, ep.residual, ny)))
+    return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
   const hipError_t e =
       hq::launch_linear(X, desc->x_dtype == HQ_BF16, T, weight, desc->d_out, desc->d_in,
                         need ? workspace : nullptr, ep, static_cast<hipStream_t>(stream));
@@ -998,6 +1003,10 @@ int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, c
   if (need && (!workspace || workspace_bytes < need))
     return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
                 workspace ? workspace_bytes : size_t(0), need);
+  if (need && (overlap(workspace, need, X, nx) || overlap(workspace, need, Y, ny) ||
+               overlap(workspace, need, gamma, 4 * size_t(desc->channels)) ||
+               overlap(workspace, need, beta, 4 * size_t(desc->channels))))
+    return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
   hq::NormArgs a = {};
   a.x = X;
   a.y = Y;

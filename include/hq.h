@@ -273,9 +273,10 @@ int hq_quant_linear_noalloc(const hq_desc* desc, const void* prepared, const voi
  * with V the layer's output (with its bias), phi an hq_act, R the residual
  * (absent: 0) and g the gate (absent: 1). V, phi, the gate and the sum are
  * fp32; Y is rounded once. phi is computed to a few fp32 ulp for fp32 Y; for
- * bf16 Y to a relative 1.1e-4 (GELU) or better, a small part of the rounding
- * to bf16. NaN goes through every activation, +inf stays +inf; -inf gives 0
- * with ReLU and, where the formula reads -inf * 0, NaN or 0. */
+ * bf16 Y to a relative 1.1e-4 (GELU, |V| up to 5; beyond it to 1.5e-5
+ * absolute) or better, a small part of the rounding to bf16. NaN goes through
+ * every activation, +inf stays +inf; -inf gives 0 with ReLU and, where the
+ * formula reads -inf * 0, NaN or 0. */
 typedef enum {
   HQ_ACT_NONE = 0,
   HQ_ACT_RELU = 1,      /* max(x, 0)                                           */
@@ -331,8 +332,13 @@ size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T);
  *  row-major; bias f32 [d_out] or NULL (none); epilogue NULL or as above;
  *  workspace at least hq_linear_workspace_bytes(desc, T) bytes (NULL when that
  *  is 0), not shared with a concurrent call. T up to 2^26; T = 0 is a no-op.
- *  Y must not overlap X, weight, bias or the gate. The same inputs always give
- *  the same bits (sums have a fixed order for a given shape). */
+ *  Neither Y nor the workspace may overlap X, weight, bias, the gate or each
+ *  other. The same inputs always give the same bits (sums have a fixed order
+ *  for a given shape). fp32 operands enter the matrix units as exact sums of
+ *  three bf16 parts; the parts' products below 2^-22 of the whole are left out,
+ *  which is the size of an fp32 product's own rounding. An infinite or NaN
+ *  value of X or weight makes the outputs it enters infinite or NaN, and no
+ *  others. */
 int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,
               int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
               size_t workspace_bytes, void* stream);

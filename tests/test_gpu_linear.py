@@ -156,6 +156,44 @@ def test_activation_range(act, ydt):
     assert_within(Y, torch.nan_to_num(y, 0.0), tol.nan_to_num(1e-30), act)
 
 
+@pytest.mark.parametrize("T", [4, 40, 2100])
+def test_fp32_operands_of_every_size(T):
+    # magnitudes from 1e-25 to near the largest float in one row of operands:
+    # the parts of a split value are exact and no part overflows. Rows and
+    # columns are scaled by powers of two, so the sums are those of plain data.
+    K, N = 264, 136
+    X, W, b, g = make(T, K, N, hq.F32, bias=False)
+    ex = torch.randint(-40, 41, (T, 1), generator=g, device="cuda").double()
+    ew = torch.randint(-40, 41, (N, 1), generator=g, device="cuda").double()
+    X2, W2 = (X.double() * 2.0 ** ex).float(), (W.double() * 2.0 ** ew).float()
+    Y = hq.linear(hq.LinearDesc(K, N, hq.F32, hq.F32, hq.F32), X2, W2)
+    v, err = product64(X2, W2, None)
+    assert_within(Y, *epilogue64(v, err, "none", hq.F32), "scaled rows")
+    big = torch.finfo(torch.float32).max
+    X3, W3 = torch.zeros(T, K, device="cuda"), torch.zeros(N, K, device="cuda")
+    X3[:, 7], W3[:, 7] = big, 0.9990234375
+    assert_within(hq.linear(hq.LinearDesc(K, N, hq.F32, hq.F32, hq.F32), X3, W3),
+                  *epilogue64(*product64(X3, W3, None), "none", hq.F32), "largest")
+
+
+@pytest.mark.parametrize("T,K,N", [(2, 1152, 6912), (300, 4096, 1152), (2500, 1160, 2312)])
+def test_two_calls_at_once(T, K, N):
+    # two streams, each with its own buffers, queued together
+    desc = hq.LinearDesc(K, N, hq.BF16, hq.BF16, hq.BF16)
+    Xa, W, b, g = make(T, K, N, hq.BF16)
+    Xb = make(T, K, N, hq.BF16, seed=1)[0]
+    ref = [hq.linear(desc, x, W, b) for x in (Xa, Xb)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for rep in range(6):
+        for k, x in enumerate((Xa, Xb)):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(hq.linear(desc, x, W, b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref[k]) for k in range(2) for y in got[k])
+
+
 def test_offsets_past_32_bits():
     T, K, N = 270_001, 8192, 8   # X holds 2.2e9 values
     desc = hq.LinearDesc(K, N, hq.BF16, hq.BF16, hq.BF16)

@@ -180,3 +180,26 @@ def test_streams_and_graph_replays(S, P, C, G):
         assert torch.equal(out, Ya if rep % 2 == 0 else Yb), f"replay {rep}"
         assert torch.equal(other, Yb)
     del graph
+
+
+@pytest.mark.parametrize("S,P,C,G", [(3, 77, 320, 32), (1, 20000, 128, 32), (8, 300, 256, 32)])
+def test_two_calls_at_once(S, P, C, G):
+    # two streams, each with its own buffers, queued together
+    desc = hq.NormDesc(C, G, act=hq.HQ_ACT_SILU, x_dtype=hq.BF16, y_dtype=hq.BF16)
+    Xa, ga, be = make(S, P, C, hq.BF16)
+    Xb = make(S, P, C, hq.BF16, seed=5)[0]
+    ref = [hq.group_norm(desc, x, ga, be) for x in (Xa, Xb)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for rep in range(6):
+        for k, x in enumerate((Xa, Xb)):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(hq.group_norm(desc, x, ga, be))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref[k]) for k in range(2) for y in got[k])
+
+
+@pytest.mark.parametrize("S,P,C,G,dt", [(1, 1 << 22, 8, 2, hq.BF16), (2, 1 << 20, 40, 4, hq.F32)])
+def test_long_sums(S, P, C, G, dt):
+    run(S, P, C, G, dt, act="none", mean=3.0)

@@ -90,6 +90,10 @@ def test_workspace_refused_when_missing_or_small():
     assert call(d=d, T=300) == -3
     assert call(d=d, T=300, ws=0x5000, n=n - 1) == -3
     assert b"workspace" in lib.hq_last_error()
+    # X, weight and Y of this call are at 0x10000, 0x20000000 and 0x40000000
+    for at in (0x10000, 0x20000000 + 4096, 0x40000000 - 16):
+        assert call(d=d, T=300, ws=at, n=n) == -1
+        assert b"workspace overlaps" in lib.hq_last_error()
 
 
 def test_empty_call_is_a_no_op():

@@ -64,6 +64,9 @@ def test_workspace():
     assert call(**big) == -3
     assert call(**big, ws=0x5000, n=n - 1) == -3
     assert b"workspace" in lib.hq_last_error()
+    for at in (0x100000, 0x40000000 - 16):
+        assert call(**big, ws=at, n=n) == -1
+        assert b"workspace overlaps" in lib.hq_last_error()
 
 
 def test_empty_calls_are_no_ops():
