@@ -150,6 +150,18 @@ __device__ __forceinline__ void finish8(float (&v)[Q][8], const int64_t (&m)[Q],
   }
 }
 
+// One piece: eight consecutive outputs n .. n+7 of row m.
+__device__ __forceinline__ void finish_piece(const float (&v)[8], int64_t m, int64_t n, int64_t N,
+                                             const LinEpi& ep) {
+  float a[1][8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[0][k] = v[k];
+  const int64_t am[1] = {m}, an[1] = {n};
+  const bool ok[1] = {true};
+  if (ep.y_bf16) finish8<uint16_t, 1>(a, am, an, ok, N, ep);
+  else finish8<float, 1>(a, am, an, ok, N, ep);
+}
+
 // A wave's 32 rows x (8 LPR) columns, staged as fp32 rows of `pitch` floats, as
 // rows again: eight consecutive columns per lane, whole row segments per store,
 // Q pieces at a time. Rows from m0, columns from n0.

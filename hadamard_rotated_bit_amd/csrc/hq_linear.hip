@@ -3,11 +3,13 @@
 // nn.Linear layout: both operands K-contiguous, no transposition anywhere) in
 // bf16 or fp32, fp32 accumulation, and the epilogue of hq_epilogue.h.
 //
-// Three kernels, chosen by shape (linear_plan):
-//  linear_rows_kernel  M <= 8: one pass over W on the vector ALU.
-//  linear_tile_kernel  MFMA tiles; few tiles are split over K (partial sums
-//                      in the workspace, added in split order by
-//                      linear_reduce_kernel, which then runs the epilogue).
+// Kernels, chosen by shape (linear_plan):
+//  linear_rows_kernel   M <= 8: one pass over W on the vector ALU.
+//  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 128; few tiles share
+//                       their k-steps among groups of waves and are split over K
+//                       (partial sums in the workspace, added in split order by
+//                       linear_reduce_kernel, which then runs the epilogue).
+//  linear_pp_kernel     bf16 tiles of 256 x 192 and 256 x 256.
 #include "hq_epilogue.h"
 #include "hq_gemm6_kernel.h"
 #include "hq_internal.h"
@@ -274,9 +276,12 @@ __device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[2][4], const 
 // of row r sits in slot c ^ ((r / 2) mod 8): the 16 lanes of one read phase
 // hit 16 distinct 16-byte positions of the 64 banks.
 // blockIdx.y is the split: k-steps [kper y, kper (y + 1)); with more than one
-// split the raw sums go to part [splits, M, N].
-template <typename TE, int BM, int BN, int WM, int WN, int S, int OCC>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
+// split the raw sums go to part [splits, M, N]. G groups of waves hold the whole
+// tile each and share the k-steps of a block among them (group g takes steps g,
+// g + G, ...; one barrier per G steps), for products with too few tiles to fill
+// the CUs: their sums meet in LDS, in group order.
+template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64 * G)
 __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
     const TE* __restrict__ X, int64_t M, const TE* __restrict__ W, int64_t N, int K, int kper,
     float* __restrict__ part, LinEpi ep) {
@@ -287,12 +292,13 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   constexpr int SPITCH = 4 * WN + 16;            // staging row: WN floats and one 16-byte pad
   static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && NW % 2 == 0, "whole 1-KB units per wave");
   static_assert(TM <= 2 && TN <= TM, "32 x 32, 64 x 32 or 64 x 64 waves");
-  static_assert(NW * 32 * SPITCH <= S * STAGE, "epilogue staging fits in the stage buffers");
+  static_assert(G * NW * 32 * SPITCH <= S * G * STAGE, "epilogue staging fits in the stage buffers");
   static_assert((S - 1) * L <= 63, "outstanding loads fit vmcnt");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * G * STAGE];
 
   const int lane = threadIdx.x & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int grp = wave / NW, wv = wave % NW;     // k group, wave of the tile
   int64_t m0, n0;
   f6_tile_origin<BM, BN, 8>(int(blockIdx.x), M, N, &m0, &n0);
   const int wm0 = (wv / WAVES_N) * WM, wn0 = (wv % WAVES_N) * WN;
@@ -314,9 +320,9 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 #define HL_ISSUE(KT_)                                                                        \
   do {                                                                                       \
     const int kt_ = (KT_);                                                                   \
-    uint8_t* base_ = smem + (kt_ % S) * STAGE;                                               \
-    const bool ok_ = kt_ < KT;                                                               \
-    const int kb_ = (kt0 + kt_) * 128;                                                       \
+    uint8_t* base_ = smem + ((kt_ % S) * G + grp) * STAGE;                                   \
+    const bool ok_ = kt_ * G + grp < KT;                                                     \
+    const int kb_ = (kt0 + kt_ * G + grp) * 128;                                             \
     const __amdgpu_buffer_rsrc_t ra_ = make_rsrc(abase, ok_ ? nrec_a : 0);                   \
     const __amdgpu_buffer_rsrc_t rb_ = make_rsrc(bbase, ok_ ? nrec_b : 0);                   \
     const bool in_ = kb_ + 16 * chunk < ldb;                                                 \
@@ -333,22 +339,22 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   uint32_t pa[4], pb[4];   // substep s of the wave's first rows of A and B in buffer 0
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const uint32_t co = lds0 + uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
+    const uint32_t co = lds0 + uint32_t(grp * STAGE) + uint32_t(((2 * s + lhalf) ^ ((lrow >> 1) & 7)) * 16);
     pa[s] = co + uint32_t((wm0 + lrow) * 128);
     pb[s] = co + uint32_t((BM + wn0 + lrow) * 128);
   }
 
+  v16f acc[TM][TN];
+  bias_acc<TM, TN>(acc, part || grp ? nullptr : ep.bias, n0 + wn0 + 4 * lhalf, N);
 #pragma unroll
   for (int p = 0; p < S - 1; ++p) HL_ISSUE(p);
-  v16f acc[TM][TN];
-  bias_acc<TM, TN>(acc, part ? nullptr : ep.bias, n0 + wn0 + 4 * lhalf, N);
   int buf = 0;
-  for (int kt = 0; kt < KT; ++kt) {
+  for (int kt = 0; kt * G < KT; ++kt) {
     // stage kt has landed in every wave; every wave is done with stage kt - 1
     wait_vm_lgkm0<(S - 2) * L>();
     __builtin_amdgcn_s_barrier();
     HL_ISSUE(kt + S - 1);
-    const uint32_t o = uint32_t(buf * STAGE);
+    const uint32_t o = uint32_t(buf * (G * STAGE));
     buf = buf == S - 1 ? 0 : buf + 1;
     v4i af[TM][4], bf[TN][4];
     const uint32_t qa[4] = {pa[0] + o, pa[1] + o, pa[2] + o, pa[3] + o};
@@ -364,8 +370,10 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 
   // Each wave stages its 32-row slices in its own part of the LDS and takes
   // them back as rows, eight consecutive columns per lane: whole row segments
-  // per store, and one epilogue for every kernel.
-  float* const stg = reinterpret_cast<float*>(smem + wv * 32 * SPITCH);
+  // per store, and one epilogue for every kernel. With groups, the G copies of a
+  // slice are added on the way and their waves share its rows.
+  constexpr int SLOT = 32 * SPITCH;
+  float* const stg = reinterpret_cast<float*>(smem + wave * SLOT);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -375,13 +383,36 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
         *reinterpret_cast<float4*>(stg + lrow * (SPITCH / 4) + j * 32 + 8 * g + 4 * lhalf) =
             make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                         acc[i][j][4 * g + 3]);
-    __builtin_amdgcn_wave_barrier();
     const int64_t mr = m0 + wm0 + 32 * i, nc = n0 + wn0;
-    if (part)
-      store_part<WN / 8>(stg, SPITCH / 4, lane, mr, nc, M, N, part + int64_t(blockIdx.y) * M * N);
-    else
-      finish_rows<WN / 8, WN == 32 ? 2 : 4>(stg, SPITCH / 4, lane, mr, nc, M, N, ep);
-    __builtin_amdgcn_wave_barrier();
+    float* const mine = part ? part + int64_t(blockIdx.y) * M * N : nullptr;
+    if constexpr (G == 1) {
+      __builtin_amdgcn_wave_barrier();
+      if (part)
+        store_part<WN / 8>(stg, SPITCH / 4, lane, mr, nc, M, N, mine);
+      else
+        finish_rows<WN / 8, WN == 32 ? 2 : 4>(stg, SPITCH / 4, lane, mr, nc, M, N, ep);
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      __syncthreads();
+      const float* const all = reinterpret_cast<const float*>(smem + wv * SLOT);
+      constexpr int LPR = WN / 8;
+      for (int q = lane + 64 * grp; q < 32 * LPR; q += 64 * G) {
+        const int r = q / LPR, c = 8 * (q - r * LPR);
+        float v[8] = {};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float a[8];
+          load8(all + g * (NW * SLOT / 4) + r * (SPITCH / 4) + c, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += a[e];
+        }
+        const int64_t m = mr + r, n = nc + c;
+        if (m >= M || n >= N) continue;
+        if (mine) store8(mine + m * N + n, v);
+        else finish_piece(v, m, n, N, ep);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -655,42 +686,48 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t npr = N / 8;
   if (i >= M * npr) return;
-  const int64_t m[1] = {i / npr}, n[1] = {(i - m[0] * npr) * 8};
-  const bool ok[1] = {true};
-  const float* p = part + m[0] * N + n[0];
-  float v[1][8] = {};
-  if (ep.bias) load8(ep.bias + n[0], v[0]);
+  const int64_t m = i / npr, n = (i - m * npr) * 8;
+  const float* p = part + m * N + n;
+  float v[8] = {};
+  if (ep.bias) load8(ep.bias + n, v);
   for (int s = 0; s < splits; ++s) {
     float a[8];
     load8(p + int64_t(s) * M * N, a);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[0][e] += a[e];
+    for (int e = 0; e < 8; ++e) v[e] += a[e];
   }
-  if (ep.y_bf16) finish8<uint16_t, 1>(v, m, n, ok, N, ep);
-  else finish8<float, 1>(v, m, n, ok, N, ep);
+  finish_piece(v, m, n, N, ep);
 }
 
 // ---- host side --------------------------------------------------------------------
 
 namespace {
 
-enum LinKind { LIN_ROWS, LIN_T32, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
+enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
 
 // Kernel and split count of a product.
 //  up to 8 rows: the vector kernel.
 //  bf16 with 128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns,
 //    whichever's rounds of one tile per CU cost less.
 //  otherwise the tile shrinks until there is one per CU: bf16 64 x 128 (1037 x
-//    1160 -> 2312: 19.6 us against 22.8 for 64 x 64), fp32 128 x 128 (1024 x 4096
-//    -> 4096: 274 us against 281), then 64 x 64 (12288 x 256 -> 256 fp32: 20.4 us
-//    against 23.9 for 64 x 128), up to 32 rows 32 x 128.
-//  A product that still leaves CUs idle is split over K. A split costs a second
-//    launch and the partial sums, about 4 us, and a k-step 0.24 us (bf16) or
-//    0.35 us (fp32): so bf16 aims at one block per CU with 12 k-steps or more
-//    each (4 where there are less than 64 tiles), fp32 at two with 4 or more (512
-//    x 1152 -> 1152 bf16: 8.0 us unsplit against 10.6 in two; 64 x 4096 -> 4096:
-//    12.0 us in four against 14.2 in eight; 128 x 4096 -> 1152 fp32: 21.6 us in
-//    14 against 26.2 in eight).
+//    1160 -> 2312: 19.6 us against 22.5 for 64 x 64) or 64 x 64 (2048 x 1152 ->
+//    1152: 13.9 us against 16.8 with two groups of waves), fp32 128 x 128 (1024 x
+//    4096 -> 4096: 206 us against 236 for 64 x 64).
+//  Fewer tiles than CUs: two groups of waves share a tile's k-steps, 64 x 64
+//    tiles (512 x 4096 -> 1152 bf16: 15.3 us against 15.7 for one group split in
+//    three over blocks; 512 x 1152 -> 1152: 7.2 us against 8.2), and 32 x 64 tiles
+//    where those are no more than the CUs (300 x 4096 -> 1152: 14.9 us against
+//    17.0 for 64 x 64 of one group split in four). fp32 computes six times as
+//    much per byte, and two groups suit it at any count; it takes 32 x 64 tiles
+//    up to 128 of them (9 x 4096 -> 4096: 18.4 us against 22.1) or where K is too
+//    short to split (2048 x 256 -> 256: 6.2 us against 7.2).
+//  What still leaves CUs idle is split over K, at 16 k-steps a block or more in
+//    bf16 (64 x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four;
+//    32 x 1152 -> 4608: 5.6 us whole against 7.3), in fp32 at 12 for 32 x 64 tiles
+//    (16 x 1152 -> 4608: 10.0 us in three against 11.2 in four) and at 24 for 64 x
+//    64 (300 x 4096 -> 1152: 33 us in five against 36 in six; 512 x 1152 -> 1152:
+//    19.7 us whole against 20.1 in three): a split costs a second launch and the
+//    partial sums.
 struct LinPlan {
   LinKind kind;
   int splits, kper;
@@ -709,18 +746,23 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
     p.kind = bf16 ? LIN_T64X128 : LIN_T128;
     return p;
   }
-  p.kind = M <= 32 ? LIN_T32 : LIN_T64;
-  const int64_t t = M <= 32 ? tiles(32, 128) : tiles(64, 64);
+  const int64_t t = tiles(64, 64), t32 = tiles(32, 64);
   const int ksteps = p.kper;
-  if (t < 256) {
-    int64_t want = bf16 ? (256 + t / 2) / t : 512 / t;
-    const int64_t most = ksteps / (bf16 && t >= 64 ? 12 : 4);
-    if (want > most) want = most;
-    if (want > (bf16 ? 8 : 16)) want = bf16 ? 8 : 16;
-    if (want > 1) {
-      p.kper = int((ksteps + want - 1) / want);
-      p.splits = (ksteps + p.kper - 1) / p.kper;
-    }
+  int64_t want = 1;
+  if (bf16) {
+    p.kind = t32 <= 256 ? LIN_T32 : t <= 256 ? LIN_T64X2 : LIN_T64;
+    if (p.kind == LIN_T32) want = std::min<int64_t>(256 / t32, ksteps / 16);
+  } else if (t32 <= 128 || (t32 <= 256 && ksteps < 24)) {
+    p.kind = LIN_T32;
+    want = std::min<int64_t>(512 / t32, ksteps / 12);
+  } else {
+    p.kind = LIN_T64X2;
+    want = std::min<int64_t>(512 / t, ksteps / 24);
+  }
+  want = std::min<int64_t>(want, bf16 ? 4 : 8);
+  if (want > 1) {
+    p.kper = int((ksteps + want - 1) / want);
+    p.splits = (ksteps + p.kper - 1) / p.kper;
   }
   return p;
 }
@@ -737,13 +779,13 @@ void launch_rows_nc(const TE* X, int M, const TE* W, int64_t N, int K, const Lin
                        X, M, W, N, K, ep);
 }
 
-template <typename TE, int BM, int BN, int WM, int WN, int S, int OCC>
+template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
 void launch_tile(const TE* X, int64_t M, const TE* W, int64_t N, int K, const LinPlan& p,
                  float* part, const LinEpi& ep, hipStream_t s) {
   const int64_t ntiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-  hipLaunchKernelGGL((linear_tile_kernel<TE, BM, BN, WM, WN, S, OCC>),
+  hipLaunchKernelGGL((linear_tile_kernel<TE, BM, BN, WM, WN, G, S, OCC>),
                      dim3(unsigned(ntiles), unsigned(p.splits)),
-                     dim3((BM / WM) * (BN / WN) * 64), 0, s, X, M, W, N, K, p.kper,
+                     dim3((BM / WM) * (BN / WN) * 64 * G), 0, s, X, M, W, N, K, p.kper,
                      p.splits > 1 ? part : nullptr, ep);
 }
 
@@ -769,15 +811,24 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
           hipLaunchKernelGGL(linear_pp_kernel<4>, grid, dim3(512), 0, s, X, M, W, N, K, ep);
       }
       break;
-    case LIN_T32: launch_tile<TE, 32, 128, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
-    case LIN_T64: launch_tile<TE, 64, 64, 32, 32, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
+    case LIN_T32: launch_tile<TE, 32, 64, 32, 32, 2, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
+    case LIN_T64X2:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 64, 64, 32, 32, 2, 3, 1>(X, M, W, N, K, p, part, ep, s);
+      else
+        launch_tile<TE, 64, 64, 32, 32, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
+    case LIN_T64:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 64, 64, 32, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
     case LIN_T64X128:
       if constexpr (sizeof(TE) == 2)
-        launch_tile<TE, 64, 128, 64, 32, 3, 2>(X, M, W, N, K, p, part, ep, s);
+        launch_tile<TE, 64, 128, 64, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
       break;
     case LIN_T128:
       if constexpr (sizeof(TE) == 4)
-        launch_tile<TE, 128, 128, 64, 64, 2, 2>(X, M, W, N, K, p, part, ep, s);
+        launch_tile<TE, 128, 128, 64, 64, 1, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
   }
   hipError_t e = hipGetLastError();

@@ -84,6 +84,14 @@ def test_wide_tiles(T, N, K):
     run(T, K, N, hq.BF16, act="gelu", residual=True, gate_rows=1000)
 
 
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("K", [8, 64, 72, 136, 192, 328, 1096, 2056])
+@pytest.mark.parametrize("T,N", [(9, 72), (100, 1160), (590, 1160)])
+def test_shared_k_steps(T, N, K, dt):
+    # two groups of waves on a tile's k-steps: fewer steps than groups, odd and even counts, with and without a split
+    run(T, K, N, dt, act="silu", residual=True, gate_rows=7)
+
+
 @pytest.mark.parametrize("dt,ydt", list(itertools.product([hq.BF16, hq.F32], repeat=2)))
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("T", [1, 7, 70, 700])
