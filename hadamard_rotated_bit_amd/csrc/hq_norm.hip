@@ -15,7 +15,12 @@
 // and the units of a group by mean_g = avg m_u, M2_g = sum M2_u + n (m_u -
 // mean_g)^2. Everything is fp32; groups may have any width.
 //
-// Two forms (norm_plan):
+// Forms (norm_plan):
+//  norm_rows_kernel    one position, groups of whole 8-channel pieces: a wave or
+//                      a part of one holds a group (8192 rows of 1152 bf16: 10.0
+//                      us, 3.8 TB/s, fp32 15.1 us, 5.0 TB/s, against 21.9 and 21.8
+//                      with a block per row; 8192 x 18 groups of 64: 9.9 us
+//                      against 21.1).
 //  norm_block_kernel   a block holds all positions of one sample's slab of
 //                      whole groups in registers: one launch, x read once.
 //  norm_stats_kernel (+ norm_join_kernel) + norm_apply_kernel
@@ -246,6 +251,85 @@ __device__ __forceinline__ void norm_store(const Raw8<TE>& x, const Coef& c, con
   }
 }
 
+// ---- one position -----------------------------------------------------------------
+
+// One position per sample and groups of whole 8-channel pieces (G = 1 is layer
+// norm, G heads a norm of each head): `rows` = S G rows of w = C / G channels, L
+// lanes per row (64, or fewer for short rows: several rows per wave), R pieces of
+// 8 channels per lane in registers, no LDS. The first sum gives a mean m', the
+// second pass sums x - m' and its square and corrects both: mean = m' + s1 / w,
+// M2 = s2 - s1^2 / w, so a rounded m' (or a constant row) leaves no trace. HOLD
+// (G = 1): gamma and beta stay in registers over a wave's rows.
+template <typename TE, int R, bool HOLD>
+__global__ __launch_bounds__(256) void norm_rows_kernel(NormKArgs k, int64_t rows, int L) {
+  const int w = k.C / k.G, VR = w / 8;
+  const int sub = int(threadIdx.x) & (L - 1), rpb = 256 / L;
+  const float inv = 1.0f / float(w);
+  auto sum = [&](float v) {   // rows of more than one piece per lane take whole waves
+    if constexpr (R > 1) return group_sum<64>(v);
+    else return lanes_sum(v, L);
+  };
+  Coef c[HOLD ? R : 1];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (sub + 64 * i < VR) load_affine(k, 8 * (sub + 64 * i), c[i].a, c[i].b);
+  }
+  // the same number of turns for every lane of a wave: sums run over all lanes
+  for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < rows; r0 += int64_t(gridDim.x) * rpb) {
+    const int64_t row = r0 + int(threadIdx.x) / L;
+    const int nv = row < rows ? VR : 0;   // pieces of the lane's row
+    const int64_t base = row * w + 8 * sub;
+    const TE* const x = static_cast<const TE*>(k.x) + base;
+    Raw8<TE> v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (sub + 64 * i < nv) v[i] = raw_load(x + 512 * i);
+    float s0 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (sub + 64 * i < nv) {
+        float f[8];
+        raw_get(v[i], f);
+        s0 += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      }
+    }
+    const float m0 = sum(s0) * inv;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (sub + 64 * i < nv) {
+        float f[8];
+        raw_get(v[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = f[e] - m0;
+          s1 += d;
+          s2 = fmaf(d, d, s2);
+        }
+      }
+    }
+    s1 = sum(s1);
+    s2 = sum(s2);
+    const float mean = fmaf(s1, inv, m0);
+    const float rstd = rstd_of(fmaxf(fmaf(-s1 * inv, s1, s2), 0.0f), k);
+    const int c0 = HOLD ? 0 : int(row % k.G) * w;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (sub + 64 * i >= nv) continue;
+      Coef d;
+      if constexpr (HOLD) d = c[i];
+      else load_affine(k, c0 + 8 * (sub + 64 * i), d.a, d.b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d.mean[e] = mean;
+        d.a[e] *= rstd;
+      }
+      norm_store<TE>(v[i], d, k, base + 512 * i);
+    }
+  }
+}
+
 // ---- one launch -------------------------------------------------------------------
 
 constexpr int NORM_BLOCK_GROUPS = 512;   // groups per slab at most
@@ -462,7 +546,8 @@ __global__ __launch_bounds__(NT) void norm_apply_kernel(NormKArgs k, const float
 namespace {
 
 struct NormPlan {
-  int block;         // 1: norm_block_kernel
+  int block;         // 1: one launch without a workspace,
+  int rows;          // 1: norm_rows_kernel, otherwise norm_block_kernel:
   int nt, r, slab;   // threads; its rows per lane and channels per block
   int chunks;        // otherwise: chunks per sample and their rows,
   int64_t rpc;
@@ -484,6 +569,10 @@ int gcd_i(int a, int b) { return b ? gcd_i(b, a % b) : a; }
 // every CU (1 x 4096 x 512 bf16: 14.7 us against 21).
 NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   NormPlan p = {};
+  if (P == 1 && C / G % 8 == 0) {
+    p.block = p.rows = 1;
+    return p;
+  }
   const int cg = C / G, unit = cg / gcd_i(cg, 8) * 8;
   const int piece = esize == 2 && S % 8 == 0 && S * (C / 16) <= 256 ? 32 : 64;
   int slab = unit;
@@ -531,8 +620,33 @@ void launch_norm_first(const NormPlan& p, const NormKArgs& k, dim3 grid, hipStre
     hipLaunchKernelGGL((norm_block_kernel<TE, U, 1024, 8>), grid, dim3(1024), 0, s, k);
 }
 
+template <typename TE, int R, bool HOLD>
+hipError_t launch_norm_rows(const NormKArgs& k, int64_t S, hipStream_t s) {
+  const int64_t rows = S * k.G;
+  int L = 1;
+  while (L < 64 && L * 8 < k.C / k.G) L <<= 1;
+  int64_t blocks = (rows * L + 255) / 256;
+  const int64_t most = R == 1 ? 2048 : 1280;   // what the CUs hold at once
+  if (blocks > most) blocks = most;
+  hipLaunchKernelGGL((norm_rows_kernel<TE, R, HOLD>), dim3(unsigned(blocks)), dim3(256), 0, s, k, rows,
+                     L);
+  return hipGetLastError();
+}
+
 template <typename TE>
 hipError_t launch_norm_typed(const NormPlan& p, const NormKArgs& k, int64_t S, hipStream_t s) {
+  if (p.rows) {
+    const int r = (k.C / k.G + 511) / 512;   // at most 8: C <= NORM_MAX_C
+    if (k.G > 1)
+      return r == 1 ? launch_norm_rows<TE, 1, false>(k, S, s) : launch_norm_rows<TE, 4, false>(k, S, s);
+    switch (r) {
+      case 1: return launch_norm_rows<TE, 1, true>(k, S, s);
+      case 2: return launch_norm_rows<TE, 2, true>(k, S, s);
+      case 3: return launch_norm_rows<TE, 3, true>(k, S, s);
+      case 4: return launch_norm_rows<TE, 4, true>(k, S, s);
+      default: return launch_norm_rows<TE, 8, false>(k, S, s);
+    }
+  }
   const dim3 g1(unsigned(S * (p.block ? (k.C + p.slab - 1) / p.slab : p.chunks)));
   switch (gcd_i(k.C / k.G, 8)) {
     case 8: launch_norm_first<TE, 8>(p, k, g1, s); break;

@@ -203,3 +203,39 @@ def test_two_calls_at_once(S, P, C, G):
 @pytest.mark.parametrize("S,P,C,G,dt", [(1, 1 << 22, 8, 2, hq.BF16), (2, 1 << 20, 40, 4, hq.F32)])
 def test_long_sums(S, P, C, G, dt):
     run(S, P, C, G, dt, act="none", mean=3.0)
+
+
+ROWS = [(8, 1), (24, 1), (24, 3), (64, 8), (64, 4), (512, 1), (520, 1), (1032, 1), (1152, 1), (1152, 18), (1152, 16),
+        (1544, 1), (2048, 1), (2056, 1), (2064, 2), (4096, 1), (4096, 2), (4096, 512), (320, 32)]
+
+
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("C,G", ROWS)
+def test_one_position(C, G, dt):
+    # layer norm and per-head norms: parts of a wave, whole waves, several pieces per lane, more rows than one turn
+    for S in (1, 3, 65):
+        run(S, 1, C, G, dt, ydt=hq.F32 if S == 3 else None)
+    run(9001 if C <= 1152 else 6001, 1, C, G, dt, inplace=True, mean=30.0)
+
+
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("C,G,value", [(1152, 1, 3.5), (1152, 18, 1000.25), (2056, 1, -0.1)])
+def test_constant_rows_give_beta(C, G, value, dt):
+    # sums of equal values round, and eps is far below the square of that rounding
+    X = torch.full((70, 1, C), value, device="cuda").to(DT[dt])
+    beta = torch.linspace(-1, 1, C, device="cuda")
+    Y = hq.group_norm(hq.NormDesc(C, G, 1e-12, hq.HQ_ACT_NONE, dt, dt), X, None, beta)
+    assert torch.equal(Y, beta.to(DT[dt]).expand(70, 1, C))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_rows_stay_alone(bad):
+    # rows that share a wave: a non-finite group is NaN, its neighbours keep their values
+    X = torch.randn(40, 1, 64, device="cuda")
+    desc = hq.NormDesc(64, 4, 1e-5)
+    want = hq.group_norm(desc, X)
+    X[7, 0, 20] = bad
+    Y = hq.group_norm(desc, X)
+    assert torch.isnan(Y[7, 0, 16:32]).all()
+    Y[7, 0, 16:32] = want[7, 0, 16:32]
+    assert torch.equal(Y, want)
