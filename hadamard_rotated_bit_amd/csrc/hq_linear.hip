@@ -14,6 +14,8 @@
 #include "hq_gemm6_kernel.h"
 #include "hq_internal.h"
 
+#include <algorithm>
+
 namespace hq {
 
 // ---- few rows ------------------------------------------------------------------
@@ -707,27 +709,34 @@ enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN
 
 // Kernel and split count of a product.
 //  up to 8 rows: the vector kernel.
-//  bf16 with 128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns,
-//    whichever's rounds of one tile per CU cost less.
-//  otherwise the tile shrinks until there is one per CU: bf16 64 x 128 (1037 x
-//    1160 -> 2312: 19.6 us against 22.5 for 64 x 64) or 64 x 64 (2048 x 1152 ->
-//    1152: 13.9 us against 16.8 with two groups of waves), fp32 128 x 128 (1024 x
-//    4096 -> 4096: 206 us against 236 for 64 x 64).
-//  Fewer tiles than CUs: two groups of waves share a tile's k-steps, 64 x 64
-//    tiles (512 x 4096 -> 1152 bf16: 15.3 us against 15.7 for one group split in
-//    three over blocks; 512 x 1152 -> 1152: 7.2 us against 8.2), and 32 x 64 tiles
-//    where those are no more than the CUs (300 x 4096 -> 1152: 14.9 us against
-//    17.0 for 64 x 64 of one group split in four). fp32 computes six times as
-//    much per byte, and two groups suit it at any count; it takes 32 x 64 tiles
-//    up to 128 of them (9 x 4096 -> 4096: 18.4 us against 22.1) or where K is too
-//    short to split (2048 x 256 -> 256: 6.2 us against 7.2).
-//  What still leaves CUs idle is split over K, at 16 k-steps a block or more in
-//    bf16 (64 x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four;
-//    32 x 1152 -> 4608: 5.6 us whole against 7.3), in fp32 at 12 for 32 x 64 tiles
-//    (16 x 1152 -> 4608: 10.0 us in three against 11.2 in four) and at 24 for 64 x
-//    64 (300 x 4096 -> 1152: 33 us in five against 36 in six; 512 x 1152 -> 1152:
-//    19.7 us whole against 20.1 in three): a split costs a second launch and the
+//  bf16:
+//    128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
+//    rounds of one tile per CU cost less.
+//    Otherwise the tile shrinks until there is one per CU: 64 x 128 (1037 x 1160
+//    -> 2312: 19.6 us against 22.5 for 64 x 64), 64 x 64 (2048 x 1152 -> 1152: 13.9
+//    us against 16.8 with two groups of waves).
+//    Fewer tiles than CUs: two groups of waves share a tile's k-steps, 64 x 64
+//    tiles (512 x 4096 -> 1152: 15.3 us against 15.7 for one group split in three
+//    over blocks; 512 x 1152 -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where
+//    those are no more than the CUs (300 x 4096 -> 1152: 14.9 us against 17.0 for
+//    64 x 64 of one group split in four).
+//    What still leaves CUs idle is split over K, at 16 k-steps a block or more (64
+//    x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four; 32 x 1152
+//    -> 4608: 5.6 us whole against 7.3): a split costs a second launch and the
 //    partial sums.
+//  fp32 computes six times as much per byte and pays for its fragments' splits by
+//  the rows and columns of a wave:
+//    128 x 128 tiles where they, split over K at 12 k-steps a block or more, come to
+//    200 blocks (512 x 4096 -> 1152: 42 us in six against 46 for 64 x 64 in three;
+//    2048 x 1152 -> 1152: 45.6 us in three against 50.5; 1024 x 4096 -> 4096: 188 us
+//    in two against 200 whole and 236 for 64 x 64);
+//    32 x 64 tiles up to 128 of them (9 x 4096 -> 4096: 18.4 us against 22.1), split
+//    at 12 k-steps (16 x 1152 -> 4608: 10.0 us in three against 11.2 in four), or
+//    where K is too short to split (2048 x 256 -> 256: 6.2 us against 7.2);
+//    64 x 64 tiles otherwise: with two groups of waves, split at 24 k-steps (300 x
+//    4096 -> 1152: 33 us in five against 36 in six; 512 x 1152 -> 1152: 19.7 us whole
+//    against 20.1 in three), or more than 512 of them with one group and a third
+//    block per CU (4096 x 640 -> 640: 31.9 us against 33.6).
 struct LinPlan {
   LinKind kind;
   int splits, kper;
@@ -742,24 +751,31 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
     p.kind = r3 < r4 ? LIN_PP3 : LIN_PP4;
     return p;
   }
-  if (bf16 ? tiles(64, 128) >= 256 : tiles(128, 128) >= 256) {
-    p.kind = bf16 ? LIN_T64X128 : LIN_T128;
-    return p;
-  }
-  const int64_t t = tiles(64, 64), t32 = tiles(32, 64);
+  const int64_t t = tiles(64, 64), t32 = tiles(32, 64), t128 = tiles(128, 128);
   const int ksteps = p.kper;
+  // splits of n tiles: `blocks` in all, `least` k-steps each, at most `most`
+  auto split = [&](int64_t blocks, int64_t n, int least, int64_t most) {
+    return std::max<int64_t>(1, std::min({blocks / n, int64_t(ksteps / least), most}));
+  };
+  const int64_t split128 = split(512, t128, 12, 6);
   int64_t want = 1;
-  if (bf16) {
-    p.kind = t32 <= 256 ? LIN_T32 : t <= 256 ? LIN_T64X2 : LIN_T64;
-    if (p.kind == LIN_T32) want = std::min<int64_t>(256 / t32, ksteps / 16);
+  if (bf16 && t32 > 256) {
+    p.kind = tiles(64, 128) >= 256 ? LIN_T64X128 : t > 256 ? LIN_T64 : LIN_T64X2;
+  } else if (bf16) {
+    p.kind = LIN_T32;
+    want = split(256, t32, 16, 4);
+  } else if (t128 * split128 >= 200) {
+    p.kind = LIN_T128;
+    want = split128;
   } else if (t32 <= 128 || (t32 <= 256 && ksteps < 24)) {
     p.kind = LIN_T32;
-    want = std::min<int64_t>(512 / t32, ksteps / 12);
-  } else {
+    want = split(512, t32, 12, 8);
+  } else if (t <= 512) {
     p.kind = LIN_T64X2;
-    want = std::min<int64_t>(512 / t, ksteps / 24);
+    want = split(512, t, 24, 8);
+  } else {
+    p.kind = LIN_T64;
   }
-  want = std::min<int64_t>(want, bf16 ? 4 : 8);
   if (want > 1) {
     p.kper = int((ksteps + want - 1) / want);
     p.splits = (ksteps + p.kper - 1) / p.kper;
@@ -818,10 +834,7 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       else
         launch_tile<TE, 64, 64, 32, 32, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
-    case LIN_T64:
-      if constexpr (sizeof(TE) == 2)
-        launch_tile<TE, 64, 64, 32, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
-      break;
+    case LIN_T64: launch_tile<TE, 64, 64, 32, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
     case LIN_T64X128:
       if constexpr (sizeof(TE) == 2)
         launch_tile<TE, 64, 128, 64, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
