@@ -204,7 +204,18 @@ __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* 
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int64_t nb = n0 + wn0 + j * 32;
-      v16f lr = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      // mu c + bias, then the low-rank product on top of it
+      v16f base;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int cl = j * 32 + 8 * g + 4 * lhalf;
+        const float4 cb = *reinterpret_cast<const float4*>(P + BN + wn0 + cl);
+        const float4 bb = *reinterpret_cast<const float4*>(P + 2 * BN + wn0 + cl);
+        base[4 * g + 0] = fmaf(mu, cb.x, bb.x);
+        base[4 * g + 1] = fmaf(mu, cb.y, bb.y);
+        base[4 * g + 2] = fmaf(mu, cb.z, bb.z);
+        base[4 * g + 3] = fmaf(mu, cb.w, bb.w);
+      }
       for (int k0 = 0; k0 < ep.rank; k0 += 16) {
         float f[8];
         load8(ep.U + mc * ep.rank + k0 + 8 * lhalf, f);
@@ -212,25 +223,23 @@ __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* 
         const int64_t nr = nb + lrow < N ? nb + lrow : N - 1;
         const int64_t off = nr * ep.rank + k0 + 8 * lhalf;
         const v8bf wh = *reinterpret_cast<const v8bf*>(ep.l2_hi + off);
-        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, uh, lr, 0, 0, 0);
+        base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, uh, base, 0, 0, 0);
         if (!ep.l2_lo_zero) {
           const v8bf wl = *reinterpret_cast<const v8bf*>(ep.l2_lo + off);
-          lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wl, uh, lr, 0, 0, 0);
+          base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wl, uh, base, 0, 0, 0);
         }
-        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, ul, lr, 0, 0, 0);
+        base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, ul, base, 0, 0, 0);
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int cl = j * 32 + 8 * g + 4 * lhalf;
         const float4 sw = *reinterpret_cast<const float4*>(P + wn0 + cl);
-        const float4 cb = *reinterpret_cast<const float4*>(P + BN + wn0 + cl);
-        const float4 bb = *reinterpret_cast<const float4*>(P + 2 * BN + wn0 + cl);
         const AccT& a = acc[i][j];
         float4 y;
-        y.x = fmaf(float(a[4 * g + 0]), sx * sw.x, fmaf(mu, cb.x, bb.x)) + lr[4 * g + 0];
-        y.y = fmaf(float(a[4 * g + 1]), sx * sw.y, fmaf(mu, cb.y, bb.y)) + lr[4 * g + 1];
-        y.z = fmaf(float(a[4 * g + 2]), sx * sw.z, fmaf(mu, cb.z, bb.z)) + lr[4 * g + 2];
-        y.w = fmaf(float(a[4 * g + 3]), sx * sw.w, fmaf(mu, cb.w, bb.w)) + lr[4 * g + 3];
+        y.x = fmaf(float(a[4 * g + 0]), sx * sw.x, base[4 * g + 0]);
+        y.y = fmaf(float(a[4 * g + 1]), sx * sw.y, base[4 * g + 1]);
+        y.z = fmaf(float(a[4 * g + 2]), sx * sw.z, base[4 * g + 2]);
+        y.w = fmaf(float(a[4 * g + 3]), sx * sw.w, base[4 * g + 3]);
         *reinterpret_cast<float4*>(stg + lrow * PITCH + cl) = y;
       }
     }
