@@ -270,6 +270,19 @@ __device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[2][4], const 
       : "memory");
 }
 
+// f6_tile_origin gives the blocks of one XCD (block b runs on XCD b mod 8) a
+// contiguous range of tiles where the count n is a multiple of 8; this does it
+// for other counts of no more than one tile per CU (the first n mod 8 XCDs have
+// one tile more): a weight row is then fetched by one or two XCDs instead of
+// all (300 x 4096 -> 1152 bf16, 180 tiles: 13.8 us against 15.6). With several
+// tiles per CU the plain order, in which an XCD keeps to one tile row, is as good
+// or better (1037 x 1160 -> 2312, 323 tiles: 18.8 us against 20.3).
+__device__ __forceinline__ int xcd_tile(int tile, int n) {
+  const int odd = n & 7, x = tile & 7;
+  if (odd == 0 || n > 256) return tile;
+  return x * (n >> 3) + (x < odd ? x : odd) + (tile >> 3);
+}
+
 // BM x BN tile, waves of WM x WN (32 or 64 rows and columns), S stage buffers of 128
 // bytes per row (64 bf16 or 32 fp32 values of K), filled by buffer loads
 // straight into LDS, S - 1 stages ahead. Rows past M or N and chunks past K
@@ -302,7 +315,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int grp = wave / NW, wv = wave % NW;     // k group, wave of the tile
   int64_t m0, n0;
-  f6_tile_origin<BM, BN, 8>(int(blockIdx.x), M, N, &m0, &n0);
+  f6_tile_origin<BM, BN, 8>(xcd_tile(int(blockIdx.x), int(gridDim.x)), M, N, &m0, &n0);
   const int wm0 = (wv / WAVES_N) * WM, wn0 = (wv % WAVES_N) * WN;
   const int ldb = K * int(sizeof(TE));
   const int ksteps = (ldb + 127) / 128;
@@ -718,7 +731,7 @@ enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN
 //    Fewer tiles than CUs: two groups of waves share a tile's k-steps, 64 x 64
 //    tiles (512 x 4096 -> 1152: 15.3 us against 15.7 for one group split in three
 //    over blocks; 512 x 1152 -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where
-//    those are no more than the CUs (300 x 4096 -> 1152: 14.9 us against 17.0 for
+//    those are no more than the CUs (300 x 4096 -> 1152: 13.8 us against 17.0 for
 //    64 x 64 of one group split in four).
 //    What still leaves CUs idle is split over K, at 16 k-steps a block or more (64
 //    x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four; 32 x 1152
