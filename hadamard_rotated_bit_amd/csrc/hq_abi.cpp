@@ -329,6 +329,11 @@ int check_linear_desc(const hq_linear_desc* d) {
   return HQ_OK;
 }
 
+// Bytes from the first to the last element of the gate's rows that T rows read.
+size_t gate_bytes(const hq::LinEpi& ep, int64_t T, int64_t d_out, size_t es) {
+  return (size_t((T - 1) / ep.gate_rows) * size_t(ep.gate_ld) + size_t(d_out)) * es;
+}
+
 // Checks an epilogue for an output Y [T, d_out] of type y_dtype and lays it
 // out for the kernels (ep->bias is the caller's).
 int check_epilogue(const hq_epilogue* e, int64_t T, int64_t d_out, int y_dtype, void* Y,
@@ -354,8 +359,7 @@ int check_epilogue(const hq_epilogue* e, int64_t T, int64_t d_out, int y_dtype, 
     ep->gate = e->gate;
     ep->gate_rows = e->gate_rows < T ? e->gate_rows : T;
     ep->gate_ld = e->gate_ld;
-    const size_t rows = size_t((T - 1) / ep->gate_rows);
-    if (overlap(e->gate, (rows * size_t(e->gate_ld) + size_t(d_out)) * es, Y, ny))
+    if (overlap(e->gate, gate_bytes(*ep, T, d_out, es), Y, ny))
       return fail(HQ_ERR_INVALID_ARG, "gate overlaps Y");
   }
   if (e->residual && e->residual != Y && overlap(e->residual, ny, Y, ny))
@@ -782,12 +786,17 @@ int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X
   if (st != HQ_OK) return st;
   if (T == 0) return HQ_OK;
   if (!X || !Y) return fail(HQ_ERR_INVALID_ARG, "X and Y must be non-NULL");
-  if (overlap(X, size_t(T) * size_t(desc->d_in) * dtype_size(desc->x_dtype), Y,
-              size_t(T) * size_t(desc->d_out) * dtype_size(desc->y_dtype)))
-    return fail(HQ_ERR_INVALID_ARG, "Y overlaps X");
+  const size_t es = dtype_size(desc->y_dtype), ny = size_t(T) * size_t(desc->d_out) * es;
+  const size_t nx = size_t(T) * size_t(desc->d_in) * dtype_size(desc->x_dtype);
+  if (overlap(X, nx, Y, ny)) return fail(HQ_ERR_INVALID_ARG, "Y overlaps X");
   hq::LinEpi lin = {};
   st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &lin);
   if (st != HQ_OK) return st;
+  const size_t need = workspace_of(desc, T).total;
+  if (overlap(workspace, need, X, nx) || overlap(workspace, need, Y, ny) ||
+      overlap(workspace, need, lin.residual, ny) ||
+      overlap(workspace, need, lin.gate, gate_bytes(lin, T, desc->d_out, es)))
+    return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
   // an epilogue of nothing is hq_quant_linear's own
   const bool any = lin.act.act != hq::ACT_NONE || lin.residual || lin.gate;
   return run_quant_linear(desc, prepared, X, T, any ? &lin : nullptr, Y, workspace,
@@ -957,7 +966,9 @@ int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, con
   if (need && (overlap(workspace, need, Y, ny) || overlap(workspace, need, X, size_t(T) * din * es) ||
                overlap(workspace, need, weight, din * dout * es) ||
                overlap(workspace, need, bias, 4 * dout) ||
-               overlap(workspace, need, ep.residual, ny)))
+               overlap(workspace, need, ep.residual, ny) ||
+               overlap(workspace, need, ep.gate,
+                       gate_bytes(ep, T, desc->d_out, dtype_size(desc->y_dtype)))))
     return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
   const hipError_t e =
       hq::launch_linear(X, desc->x_dtype == HQ_BF16, T, weight, desc->d_out, desc->d_in,

@@ -687,8 +687,6 @@ size_t norm_part_bytes(int64_t S, int64_t P, int C, int G, int esize) {
 hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
   const NormPlan p = norm_plan(S, a.P, a.C, a.G, a.x_bf16 ? 2 : 4);
   NormKArgs k = {};
-  k.x = a.x;
-  k.y = a.y;
   k.gamma = a.gamma;
   k.beta = a.beta;
   k.P = a.P;
@@ -701,7 +699,17 @@ hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
   k.chunks = p.chunks;
   k.rpc = p.rpc;
   k.slab = p.slab;
-  return a.x_bf16 ? launch_norm_typed<uint16_t>(p, k, S, s) : launch_norm_typed<float>(p, k, S, s);
+  // slices of samples: a grid holds less than 2^32 threads (norm_rows_kernel
+  // loops over its rows)
+  const int64_t most = p.rows ? S : int64_t(1) << 20;
+  for (int64_t s0 = 0; s0 < S; s0 += most) {
+    const int64_t n = S - s0 < most ? S - s0 : most, off = s0 * a.P * a.C;
+    k.x = static_cast<const char*>(a.x) + off * (a.x_bf16 ? 2 : 4);
+    k.y = static_cast<char*>(a.y) + off * (a.y_bf16 ? 2 : 4);
+    const hipError_t e = a.x_bf16 ? launch_norm_typed<uint16_t>(p, k, n, s) : launch_norm_typed<float>(p, k, n, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace hq

@@ -307,7 +307,8 @@ typedef struct {
  * with its bias, then Y = residual + gate phi(V) in the GEMM's epilogue (no
  * second pass over Y). Arguments, workspace (hq_workspace_bytes) and errors as
  * hq_quant_linear; epilogue NULL, or with everything absent, is that call
- * exactly. T up to 2^26; Y must not overlap X or the gate. */
+ * exactly. T up to 2^26; Y must not overlap X or the gate, nor the workspace
+ * any of them or the residual. */
 int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X, int64_t T,
                         const hq_epilogue* epilogue, void* Y, void* workspace,
                         size_t workspace_bytes, void* stream);
@@ -333,7 +334,7 @@ size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T);
  *  workspace at least hq_linear_workspace_bytes(desc, T) bytes (NULL when that
  *  is 0), not shared with a concurrent call. T up to 2^26; T = 0 is a no-op.
  *  Neither Y nor the workspace may overlap X, weight, bias, the gate or each
- *  other. The same inputs always give the same bits (sums have a fixed order
+ *  other, nor the workspace the residual. The same inputs always give the same bits (sums have a fixed order
  *  for a given shape). fp32 operands enter the matrix units as exact sums of
  *  three bf16 parts; the parts' products below 2^-22 of the whole are left out,
  *  which is the size of an fp32 product's own rounding. An infinite or NaN

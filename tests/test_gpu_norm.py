@@ -239,3 +239,15 @@ def test_bad_rows_stay_alone(bad):
     assert torch.isnan(Y[7, 0, 16:32]).all()
     Y[7, 0, 16:32] = want[7, 0, 16:32]
     assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("C,G", [(8, 2), (8, 1)])
+def test_more_samples_than_one_grid(C, G):
+    # 2^24 blocks of 256 threads are one more thread than a grid holds
+    S = (1 << 24) + 5
+    X = torch.randn(S, 1, C, device="cuda").to(torch.bfloat16)
+    desc = hq.NormDesc(C, G, 1e-5, hq.HQ_ACT_SILU, hq.BF16, hq.BF16)
+    Y = hq.group_norm(desc, X)
+    for a in (0, (1 << 20) - 50, 1 << 23, S - 100):
+        part = X[a:a + 100].contiguous()
+        assert torch.equal(Y[a:a + 100], hq.group_norm(desc, part))

@@ -43,8 +43,8 @@ def test_workspace_only_for_split_products():
     assert lib.hq_linear_workspace_bytes(ref(), 8192) == 0       # tiles for every CU
     assert lib.hq_linear_workspace_bytes(ref(), 1) == 0          # vector kernel
     assert lib.hq_linear_workspace_bytes(ref(), 0) == 0
-    n = lib.hq_linear_workspace_bytes(ref(d_in=4096, d_out=1152), 300)
-    assert n > 0 and n % (300 * 1152 * 4) < 256                  # whole partial matrices
+    n = lib.hq_linear_workspace_bytes(ref(d_in=4096, d_out=1152), 100)
+    assert n > 0 and n % (100 * 1152 * 4) < 256                  # whole partial matrices
     assert lib.hq_linear_workspace_bytes(ref(), -1) == 0
     with pytest.raises(hq.HqError):
         hq.linear_workspace_bytes(hq.LinearDesc(64, 64), -1)
@@ -86,13 +86,16 @@ def test_call_refusals(kw, status, word):
 
 def test_workspace_refused_when_missing_or_small():
     d = ref(d_in=4096, d_out=1152)
-    n = lib.hq_linear_workspace_bytes(d, 300)
-    assert call(d=d, T=300) == -3
-    assert call(d=d, T=300, ws=0x5000, n=n - 1) == -3
+    n = lib.hq_linear_workspace_bytes(d, 100)
+    assert call(d=d, T=100) == -3
+    assert call(d=d, T=100, ws=0x5000, n=n - 1) == -3
     assert b"workspace" in lib.hq_last_error()
     # X, weight and Y of this call are at 0x10000, 0x20000000 and 0x40000000
     for at in (0x10000, 0x20000000 + 4096, 0x40000000 - 16):
-        assert call(d=d, T=300, ws=at, n=n) == -1
+        assert call(d=d, T=100, ws=at, n=n) == -1
+        assert b"workspace overlaps" in lib.hq_last_error()
+    for e in (epi(residual=0x5000), epi(gate=0x5000, gate_rows=8, gate_ld=1152)):
+        assert call(d=d, T=100, ws=0x5000, n=n, epi=e) == -1
         assert b"workspace overlaps" in lib.hq_last_error()
 
 

@@ -26,6 +26,9 @@ def call(desc=None, prep=0x1000, X=0x100000, T=16, epi=None, Y=0x40000000, ws=0x
     (dict(epi=(0, 0x40000010, None, 0, 0)), -1, b"residual overlaps"),
     (dict(epi=(0, None, 0x5000, 0, 4608)), -1, b"gate_rows"), (dict(epi=(0, None, 0x5000, 8, 4604)), -1, b"gate_ld"),
     (dict(epi=(0, None, 0x40000000, 8, 4608)), -1, b"gate overlaps"),
+    (dict(ws=0x100000), -1, b"workspace overlaps"), (dict(ws=0x40000000 + 256), -1, b"workspace overlaps"),
+    (dict(epi=(0, 0x80000100, None, 0, 0)), -1, b"workspace overlaps"),
+    (dict(epi=(0, None, 0x80000100, 8, 4608)), -1, b"workspace overlaps"),
 ])
 def test_refusals(kw, status, word):
     assert call(**kw) == status
