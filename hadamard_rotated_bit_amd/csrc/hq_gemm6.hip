@@ -26,7 +26,7 @@ static hipError_t launch_f6_cfg(const uint8_t* A, int64_t M, const uint8_t* B, i
 
 // The product with the extended epilogue (activation, gate, residual): smaller
 // tiles, three or two blocks per CU, so that one block's epilogue runs beside
-// the others' products. Measured on 8192 x 1152 -> 4608 with the tanh GELU: 66
+// the others' products. Measured on 8192 x 1152 -> 4608 with the tanh GELU: 65
 // us a call against 90 for the persistent kernel with the same epilogue in it
 // (its one wave per SIMD leaves the matrix units idle meanwhile).
 template <int BN, int WN, int S, int OCC>
