@@ -4,7 +4,7 @@
 // bf16 or fp32, fp32 accumulation, and the epilogue of hq_epilogue.h.
 //
 // Kernels, chosen by shape (linear_plan):
-//  linear_rows_kernel   M <= 8: one pass over W on the vector ALU.
+//  linear_rows_kernel   M <= 4: one pass over W on the vector ALU.
 //  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 128; few tiles share
 //                       their k-steps among groups of waves and are split over K
 //                       (partial sums in the workspace, added in split order by
@@ -30,7 +30,7 @@ template <typename TE, int TT, int NC>
 __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__ X, int M,
                                                           const TE* __restrict__ W, int64_t N,
                                                           int K, LinEpi ep) {
-  constexpr int U = TT <= 2 ? 4 : TT == 4 ? 3 : 2;   // bounded by the registers of the X pieces
+  constexpr int U = TT <= 2 ? 4 : 3;   // bounded by the registers of the X pieces
   const int lane = threadIdx.x & 63;
   const int64_t n0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * NC;
   if (n0 >= N) return;
@@ -729,7 +729,8 @@ namespace {
 enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
 
 // Kernel and split count of a product.
-//  up to 8 rows: the vector kernel.
+//  up to 4 rows: the vector kernel (4096 x 16384 bf16: 25 us at one row, 30 at four,
+//  as with tiles; at eight 43 against 30, fp32 82 against 57).
 //  bf16:
 //    128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
 //    rounds of one tile per CU cost less.
@@ -747,16 +748,19 @@ enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN
 //    partial sums.
 //  fp32 computes six times as much per byte and pays for its fragments' splits by
 //  the rows and columns of a wave:
-//    128 x 128 tiles where they, split over K at 12 k-steps a block or more, come to
-//    200 blocks (512 x 4096 -> 1152: 42 us in six against 46 for 64 x 64 in three;
+//    128 x 128 tiles for more than 64 rows where they, split over K at 12 k-steps a
+//    block or more, come to 200 blocks (512 x 4096 -> 1152: 42 us in six against 46 for 64 x 64 in three;
 //    2048 x 1152 -> 1152: 45.6 us in three against 50.5; 1024 x 4096 -> 4096: 188 us
 //    in two against 200 whole and 236 for 64 x 64);
-//    32 x 64 tiles up to 128 of them (9 x 4096 -> 4096: 18.4 us against 22.1), split
-//    at 12 k-steps (16 x 1152 -> 4608: 10.0 us in three against 11.2 in four), or
-//    where K is too short to split (2048 x 256 -> 256: 6.2 us against 7.2);
-//    64 x 64 tiles otherwise: with two groups of waves, split at 24 k-steps (300 x
-//    4096 -> 1152: 33 us in five against 36 in six; 512 x 1152 -> 1152: 19.7 us whole
-//    against 20.1 in three), or more than 512 of them with one group and a third
+//    32 x 64 tiles for one tile row or up to 128 of them (9 x 4096 -> 4096: 18.4 us
+//    against 22.1), split at 12 k-steps (16 x 1152 -> 4608: 10.0 us in three against
+//    11.2 in four) into two blocks per CU, or one for a single tile row, which
+//    streams W (16 x 8192 -> 4096: 34 us in four against 45 in eight; 128 x 4096 ->
+//    1152 the other way, 19.1 in six against 21 in four), or where K is too short to
+//    split (2048 x 256 -> 256: 6.2 us against 7.2);
+//    64 x 64 tiles otherwise: with two groups of waves, split at 12 k-steps (300 x
+//    4096 -> 1152: 33 us in five against 36 in six; 64 x 1152 -> 4608: 14.0 us in
+//    three against 20 whole), or more than 512 of them with one group and a third
 //    block per CU (4096 x 640 -> 640: 31.9 us against 33.6).
 struct LinPlan {
   LinKind kind;
@@ -764,7 +768,7 @@ struct LinPlan {
 };
 LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   LinPlan p = {LIN_ROWS, 1, (K * esize + 127) / 128};
-  if (M <= 8) return p;
+  if (M <= 4) return p;
   const bool bf16 = esize == 2;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (bf16 && tiles(256, 192) >= 128) {
@@ -785,15 +789,15 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   } else if (bf16) {
     p.kind = LIN_T32;
     want = split(256, t32, 16, 4);
-  } else if (t128 * split128 >= 200) {
+  } else if (M > 64 && t128 * split128 >= 200) {
     p.kind = LIN_T128;
     want = split128;
-  } else if (t32 <= 128 || (t32 <= 256 && ksteps < 24)) {
+  } else if (M <= 32 || t32 <= 128 || (t32 <= 256 && ksteps < 24)) {
     p.kind = LIN_T32;
-    want = split(512, t32, 12, 8);
+    want = split(M <= 32 ? 256 : 512, t32, 12, 8);
   } else if (t <= 512) {
     p.kind = LIN_T64X2;
-    want = split(512, t, 24, 8);
+    want = split(512, t, 12, 8);
   } else {
     p.kind = LIN_T64;
   }
@@ -834,8 +838,7 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
     case LIN_ROWS:
       if (M == 1) launch_rows_nc<TE, 1>(X, int(M), W, N, K, ep, s);
       else if (M == 2) launch_rows_nc<TE, 2>(X, int(M), W, N, K, ep, s);
-      else if (M <= 4) launch_rows_nc<TE, 4>(X, int(M), W, N, K, ep, s);
-      else launch_rows_nc<TE, 8>(X, int(M), W, N, K, ep, s);
+      else launch_rows_nc<TE, 4>(X, int(M), W, N, K, ep, s);
       break;
     case LIN_PP3:
     case LIN_PP4:
