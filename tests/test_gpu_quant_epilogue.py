@@ -88,6 +88,32 @@ def test_forms(form, T, N):
     check(desc, prep, X, "silu", True, 1, g, inplace=True)
 
 
+@pytest.mark.parametrize("form", ["f6_persist", "f6_persist_lr2", "f6_f32", "i8", "i8_lr2"])
+def test_more_tokens_than_the_few_token_form_takes(form):
+    kw = dict(FORMS[form])
+    desc, prep, X, g = layer(1201, kw.pop("K"), 1160, **kw)
+    check(desc, prep, X, "gelu", True, 400, g)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("K", [128, 1024, 1152, 3584, 8192])
+def test_few_tokens(K, bits):
+    # fewer stages than waves, one each, one more; several rounds of stages; rows that end inside a tile
+    for T, N, rank in ((1, 24, 0), (1, 1152, 64), (31, 40, 16), (33, 264, 0), (100, 136, 48)):
+        desc, prep, X, g = layer(T, K, N, bits, hq.BF16, hq.BF16, rank=rank, seed=K)
+        check(desc, prep, X, "gelu_tanh", True, 3, g, inplace=True)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_few_tokens_are_the_same_rows(bits):
+    # a token's outputs do not depend on how many others the call has, whatever kernel takes it
+    desc, prep, X, g = layer(3000, 1152, 1160, bits, hq.BF16, hq.BF16)
+    epi = hq.Epilogue(hq.HQ_ACT_SILU)
+    Y = hq.quant_linear(desc, prep, X, epilogue=epi)
+    for T in (1, 40, 700):
+        assert torch.equal(hq.quant_linear(desc, prep, X[:T].contiguous(), epilogue=epi), Y[:T])
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("form", ["f6_persist", "f6_f32", "group_bf16", "i8"])
 def test_activations(form, act):
