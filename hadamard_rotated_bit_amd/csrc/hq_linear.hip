@@ -5,6 +5,7 @@
 //
 // Kernels, chosen by shape (linear_plan):
 //  linear_rows_kernel   M <= 4: one pass over W on the vector ALU.
+//  linear_few_kernel    16 x 16 tiles for up to 8 rows, or 64 with a short K.
 //  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 128; few tiles share
 //                       their k-steps among groups of waves and are split over K
 //                       (partial sums in the workspace, added in split order by
@@ -701,6 +702,80 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 }
 
+// ---- a few rows -----------------------------------------------------------------
+//
+// Tiles of 16 x 16 outputs for up to 8 rows, or more with a short K: the eight
+// waves of a block take the k-steps (128 bytes of a row) in turn, fragments go from
+// memory straight into registers, U k-steps in flight, no barrier until the waves'
+// sums meet in LDS, in wave order. Lane l holds bytes 32 (l / 16) .. + 31 of row
+// l % 16 (bf16: two chunks for two v_mfma_f32_16x16x32_bf16; fp32: the eight values
+// of one split), the same k for both operands. Rows past the end repeat the last
+// one and are not stored; chunks past K are zeros. Bound by reading W (8 x 4096 ->
+// 16384 bf16: 29.7 us, 4.5 TB/s) or by latency (16 x 256 -> 1152: 2.9 us); each block
+// reads all of its 16 rows of X, so more rows with a long K take wider tiles.
+template <typename TE>
+__global__ __launch_bounds__(512) void linear_few_kernel(const TE* __restrict__ X, int64_t M,
+                                                         const TE* __restrict__ W, int64_t N, int K,
+                                                         LinEpi ep) {
+  constexpr int NW = 8, U = 4, PITCH = 20, SLOT = 16 * PITCH;
+  __shared__ __attribute__((aligned(16))) float smem[NW * SLOT];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int lrow = lane & 15, q = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * 16;
+  const int ldb = K * int(sizeof(TE)), KT = (ldb + 127) / 128;
+  const int64_t ma = m0 + lrow < M ? m0 + lrow : M - 1, nb = n0 + lrow < N ? n0 + lrow : N - 1;
+  const uint8_t* const px = reinterpret_cast<const uint8_t*>(X) + ma * ldb;
+  const uint8_t* const pw = reinterpret_cast<const uint8_t*>(W) + nb * ldb;
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = wv; s0 < KT; s0 += NW * U) {
+    v4i x[U][2], w[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {   // both chunks of an operand in a row: they share its lines
+      const int o = (s0 + NW * u) * 128 + 32 * q;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        x[u][c] = o + 16 * c < ldb ? *reinterpret_cast<const v4i*>(px + o + 16 * c) : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        w[u][c] = o + 16 * c < ldb ? *reinterpret_cast<const v4i*>(pw + o + 16 * c) : v4i{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s0 + NW * u >= KT) break;
+#define HL_FEW(W_, X_) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W_, X_, acc, 0, 0, 0)
+      if constexpr (sizeof(TE) == 2) {
+        HL_FEW(__builtin_bit_cast(v8bf, w[u][0]), __builtin_bit_cast(v8bf, x[u][0]));
+        HL_FEW(__builtin_bit_cast(v8bf, w[u][1]), __builtin_bit_cast(v8bf, x[u][1]));
+      } else {
+        const Split a = split8(x[u][0], x[u][1]), b = split8(w[u][0], w[u][1]);
+        HL_FEW(b.l, a.h);
+        HL_FEW(b.m, a.m);
+        HL_FEW(b.h, a.l);
+        HL_FEW(b.m, a.h);
+        HL_FEW(b.h, a.m);
+        HL_FEW(b.h, a.h);
+      }
+#undef HL_FEW
+    }
+  }
+  *reinterpret_cast<v4f*>(smem + wv * SLOT + lrow * PITCH + 4 * q) = acc;
+  __syncthreads();
+  const int r = int(threadIdx.x) / 2, c = 8 * (int(threadIdx.x) % 2);
+  const int64_t m = m0 + r, n = n0 + c;
+  if (r >= 16 || m >= M || n >= N) return;
+  float v[8] = {};
+  if (ep.bias) load8(ep.bias + n, v);
+#pragma unroll
+  for (int g = 0; g < NW; ++g) {
+    float a[8];
+    load8(smem + g * SLOT + r * PITCH + c, a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += a[e];
+  }
+  finish_piece(v, m, n, N, ep);
+}
+
 // Y from the splits' partial sums [splits, M, N], added in split order; one
 // lane per 8 columns. Bound by reading the partial sums (L2 / Infinity Cache).
 __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restrict__ part,
@@ -726,11 +801,16 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 
 namespace {
 
-enum LinKind { LIN_ROWS, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
+enum LinKind { LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
 
 // Kernel and split count of a product.
-//  up to 4 rows: the vector kernel (4096 x 16384 bf16: 25 us at one row, 30 at four,
-//  as with tiles; at eight 43 against 30, fp32 82 against 57).
+//  up to 4 rows: the vector kernel (4096 -> 16384 bf16: 25 us at one row, 30 at four;
+//    at eight it would take 43).
+//  16 x 16 tiles up to 64 rows where K is short (16 x 256 -> 1152 bf16: 2.9 us against
+//    3.6, fp32 3.5 against 5.6; at 128 rows 3.8 against 3.7), and for 3 (fp32: 5) to 8
+//    rows of many outputs (4 x 4096 -> 16384 bf16: 26.1 us against 30.1 for the vector
+//    kernel; 8 rows: 29.7 against 30.1 for 32 x 64 tiles, 16 rows the other way, 34.0
+//    against 30.4; 8 x 4608 -> 1152 fp32 the other way too, 16.3 against 13.7).
 //  bf16:
 //    128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
 //    rounds of one tile per CU cost less.
@@ -768,8 +848,12 @@ struct LinPlan {
 };
 LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   LinPlan p = {LIN_ROWS, 1, (K * esize + 127) / 128};
-  if (M <= 4) return p;
   const bool bf16 = esize == 2;
+  if ((p.kper <= 8 && M > 2 && M <= 64) || (N >= 4096 && M > (bf16 ? 2 : 4) && M <= 8)) {
+    p.kind = LIN_FEW;
+    return p;
+  }
+  if (M <= 4) return p;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (bf16 && tiles(256, 192) >= 128) {
     const int64_t r3 = (tiles(256, 192) + 255) / 256 * 3, r4 = (tiles(256, 256) + 255) / 256 * 4;
@@ -839,6 +923,10 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       if (M == 1) launch_rows_nc<TE, 1>(X, int(M), W, N, K, ep, s);
       else if (M == 2) launch_rows_nc<TE, 2>(X, int(M), W, N, K, ep, s);
       else launch_rows_nc<TE, 4>(X, int(M), W, N, K, ep, s);
+      break;
+    case LIN_FEW:
+      hipLaunchKernelGGL((linear_few_kernel<TE>), dim3(unsigned((N + 15) / 16), unsigned((M + 15) / 16)),
+                         dim3(512), 0, s, X, M, W, N, K, ep);
       break;
     case LIN_PP3:
     case LIN_PP4:

@@ -92,6 +92,14 @@ def test_shared_k_steps(T, N, K, dt):
     run(T, K, N, dt, act="silu", residual=True, gate_rows=7)
 
 
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("T,K,N", [(3, 8, 8), (17, 72, 40), (64, 256, 1160), (5, 4096, 4104), (8, 5128, 4096), (7, 264, 4104)])
+def test_few_rows(T, K, N, dt):
+    # k-steps shared by the waves of a block: fewer than waves, several rounds, chunks past the end of K
+    run(T, K, N, dt, act="gelu", residual=True, gate_rows=2)
+    run(T, K, N, dt, bias=False, inplace=True, residual=True)
+
+
 @pytest.mark.parametrize("dt,ydt", list(itertools.product([hq.BF16, hq.F32], repeat=2)))
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("T", [1, 7, 70, 700])
