@@ -138,10 +138,11 @@ hipError_t launch_gemm_f6g(const uint8_t* A, int64_t M, const uint8_t* B, int64_
 hipError_t launch_gemm_f6(const uint8_t* A, int64_t M, const uint8_t* B, int64_t N, int K,
                           int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s);
 
-// The same two products with the extended epilogue for few tokens (epi.ext;
-// f6: E2M3 codes, otherwise int8).
+// The same products with the extended epilogue for few tokens (epi.ext; f6:
+// E2M3 codes, otherwise int8; s_xg and s_wg as launch_gemm_f6g's, or NULL).
 hipError_t launch_gemm_few(int f6, const void* A, int64_t M, const void* B, int64_t N, int K,
-                           const GemmEpi& ep, hipStream_t s);
+                           const GemmEpi& ep, hipStream_t s, const float* s_xg = nullptr,
+                           int64_t ld_sx = 0, const float* s_wg = nullptr, int64_t ld_sw = 0);
 
 // Dense linear layer: Y = residual + gate phi(X W^T + bias), X [M, K] and
 // W [N, K] both bf16 or both fp32 (N, K multiples of 8). linear_part_bytes:

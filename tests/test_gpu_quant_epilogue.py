@@ -88,7 +88,7 @@ def test_forms(form, T, N):
     check(desc, prep, X, "silu", True, 1, g, inplace=True)
 
 
-@pytest.mark.parametrize("form", ["f6_persist", "f6_persist_lr2", "f6_f32", "i8", "i8_lr2"])
+@pytest.mark.parametrize("form", ["f6_persist", "f6_persist_lr2", "f6_f32", "i8", "i8_lr2", "group_bf16", "group_f32"])
 def test_more_tokens_than_the_few_token_form_takes(form):
     kw = dict(FORMS[form])
     desc, prep, X, g = layer(1201, kw.pop("K"), 1160, **kw)
@@ -219,3 +219,11 @@ def test_block_of_layers():
     assert float((table.double() - tref).norm() / tref.norm()) < 2 ** -8
     yref, tol = epilogue64(v, v.abs() * 2 ** -8, "none", hq.BF16, x.view(T, C), gate, P)
     assert_within(y, yref, tol, "fc2")
+
+
+@pytest.mark.parametrize("K,T,N", [(128, 1, 8), (256, 33, 40), (384, 64, 1160), (384, 2, 72)])
+def test_few_tokens_with_group_scales(K, T, N):
+    # at most 6 groups: 6 roundings in the plain call, 1 + 8 here
+    for rank in (0, 32):
+        desc, prep, X, g = layer(T, K, N, 4, hq.BF16, hq.BF16, rank=rank, group=64, seed=K)
+        check(desc, prep, X, "silu", True, 5, g)
