@@ -6,7 +6,7 @@
 // Kernels, chosen by shape (linear_plan):
 //  linear_rows_kernel   M <= 4: one pass over W on the vector ALU.
 //  linear_few_kernel    16 x 16 tiles for up to 8 rows, or 64 with a short K.
-//  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 128; few tiles share
+//  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 192; few tiles share
 //                       their k-steps among groups of waves and are split over K
 //                       (partial sums in the workspace, added in split order by
 //                       linear_reduce_kernel, which then runs the epilogue).
@@ -272,6 +272,25 @@ __device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[2][4], const 
       : "memory");
 }
 
+__device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[3][4], const uint32_t (&p)[4],
+                                          const uint32_t (&q)[4]) {
+  asm volatile(
+      "ds_read_b128 %0, %20\n ds_read_b128 %4, %20 offset:4096\n ds_read_b128 %8, %24\n"
+      "ds_read_b128 %12, %24 offset:4096\n ds_read_b128 %16, %24 offset:8192\n"
+      "ds_read_b128 %1, %21\n ds_read_b128 %5, %21 offset:4096\n ds_read_b128 %9, %25\n"
+      "ds_read_b128 %13, %25 offset:4096\n ds_read_b128 %17, %25 offset:8192\n"
+      "ds_read_b128 %2, %22\n ds_read_b128 %6, %22 offset:4096\n ds_read_b128 %10, %26\n"
+      "ds_read_b128 %14, %26 offset:4096\n ds_read_b128 %18, %26 offset:8192\n"
+      "ds_read_b128 %3, %23\n ds_read_b128 %7, %23 offset:4096\n ds_read_b128 %11, %27\n"
+      "ds_read_b128 %15, %27 offset:4096\n ds_read_b128 %19, %27 offset:8192\n s_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[0][2]), "=&v"(a[0][3]), "=&v"(a[1][0]),
+        "=&v"(a[1][1]), "=&v"(a[1][2]), "=&v"(a[1][3]), "=&v"(b[0][0]), "=&v"(b[0][1]),
+        "=&v"(b[0][2]), "=&v"(b[0][3]), "=&v"(b[1][0]), "=&v"(b[1][1]), "=&v"(b[1][2]),
+        "=&v"(b[1][3]), "=&v"(b[2][0]), "=&v"(b[2][1]), "=&v"(b[2][2]), "=&v"(b[2][3])
+      : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3])
+      : "memory");
+}
+
 // f6_tile_origin gives the blocks of one XCD (block b runs on XCD b mod 8) a
 // contiguous range of tiles where the count n is a multiple of 8; this does it
 // for other counts of no more than one tile per CU (the first n mod 8 XCDs have
@@ -312,7 +331,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
   constexpr int STAGE = 128 * (BM + BN);
   constexpr int SPITCH = 4 * WN + 16;            // staging row: WN floats and one 16-byte pad
   static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && NW % 2 == 0, "whole 1-KB units per wave");
-  static_assert(TM <= 2 && TN <= TM, "32 x 32, 64 x 32 or 64 x 64 waves");
+  static_assert(TM <= 2 && TN <= TM + 1, "waves of 32 x 32 or 64 x 32, 64 or 96");
   static_assert(G * NW * 32 * SPITCH <= S * G * STAGE, "epilogue staging fits in the stage buffers");
   static_assert((S - 1) * L <= 63, "outstanding loads fit vmcnt");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * G * STAGE];
@@ -411,7 +430,7 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
       if (part)
         store_part<WN / 8>(stg, SPITCH / 4, lane, mr, nc, M, N, mine);
       else
-        finish_rows<WN / 8, WN == 32 ? 2 : 4>(stg, SPITCH / 4, lane, mr, nc, M, N, ep);
+        finish_rows<WN / 8, WN == 32 ? 2 : WN == 96 ? 3 : 4>(stg, SPITCH / 4, lane, mr, nc, M, N, ep);
       __builtin_amdgcn_wave_barrier();
     } else {
       __syncthreads();
@@ -801,7 +820,9 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 
 namespace {
 
-enum LinKind { LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_PP3, LIN_PP4 };
+enum LinKind {
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128X192, LIN_PP3, LIN_PP4
+};
 
 // Kernel and split count of a product.
 //  up to 4 rows: the vector kernel (4096 -> 16384 bf16: 25 us at one row, 30 at four;
@@ -812,16 +833,22 @@ enum LinKind { LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_
 //    kernel; 8 rows: 29.7 against 30.1 for 32 x 64 tiles, 16 rows the other way, 34.0
 //    against 30.4; 8 x 4608 -> 1152 fp32 the other way too, 16.3 against 13.7).
 //  bf16:
-//    128 or more tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
+//    More than 128 tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
 //    rounds of one tile per CU cost less.
-//    Otherwise the tile shrinks until there is one per CU: 64 x 128 (1037 x 1160
-//    -> 2312: 19.6 us against 22.5 for 64 x 64), 64 x 64 (2048 x 1152 -> 1152: 13.9
-//    us against 16.8 with two groups of waves).
-//    Fewer tiles than CUs: two groups of waves share a tile's k-steps, 64 x 64
-//    tiles (512 x 4096 -> 1152: 15.3 us against 15.7 for one group split in three
-//    over blocks; 512 x 1152 -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where
-//    those are no more than the CUs (300 x 4096 -> 1152: 13.8 us against 17.0 for
-//    64 x 64 of one group split in four).
+//    Otherwise the tile shrinks until there is about one per CU, with two groups of
+//    waves sharing a tile's k-steps where one group would leave a SIMD one wave:
+//    128 x 192 (1024 x 4608 -> 4608: 52 us against 67 for 256 x 192 and 73 for 64 x
+//    128; 4096 x 1152 -> 1152: 20.7 against 25.4 and 24.6) where 128 x 128 come to
+//    more than one per CU; 128 x 128 (1024 x 4096 -> 4096: 40 us against 45 for 64 x
+//    128) down to one for two CUs and 24 k-steps (512 x 1152 -> 4608, 18 k-steps: 14.2
+//    us for 64 x 128 against 14.8); 64 x 128 (1037 x 1160 -> 2312: 18.6 us against
+//    22.5 for 64 x 64); 64 x 64 (2048 x 1152 -> 1152: 13.9 us), or with 48 k-steps 64 x
+//    128 split over K (1024 x 4608 -> 1152: 23.7 us in three against 27.8).
+//    Fewer 64 x 64 tiles than CUs: two groups of waves, 64 x 64 tiles (512 x 4096 ->
+//    1152: 15.3 us against 15.7 for one group split in three over blocks; 512 x 1152
+//    -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where those are no more than the
+//    CUs (300 x 4096 -> 1152: 13.8 us against 17.0 for 64 x 64 of one group split in
+//    four).
 //    What still leaves CUs idle is split over K, at 16 k-steps a block or more (64
 //    x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four; 32 x 1152
 //    -> 4608: 5.6 us whole against 7.3): a split costs a second launch and the
@@ -855,7 +882,7 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   }
   if (M <= 4) return p;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (bf16 && tiles(256, 192) >= 128) {
+  if (bf16 && tiles(256, 192) > 128) {
     const int64_t r3 = (tiles(256, 192) + 255) / 256 * 3, r4 = (tiles(256, 256) + 255) / 256 * 4;
     p.kind = r3 < r4 ? LIN_PP3 : LIN_PP4;
     return p;
@@ -868,8 +895,13 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   };
   const int64_t split128 = split(512, t128, 12, 6);
   int64_t want = 1;
-  if (bf16 && t32 > 256) {
-    p.kind = tiles(64, 128) >= 256 ? LIN_T64X128 : t > 256 ? LIN_T64 : LIN_T64X2;
+  if (bf16 && (t128 > 256 || (t128 > 128 && ksteps >= 24))) {
+    p.kind = t128 > 256 ? LIN_T128X192 : LIN_T128;
+  } else if (bf16 && (tiles(64, 128) >= 256 || (t > 256 && ksteps >= 48))) {
+    p.kind = LIN_T64X128;
+    want = split(512, tiles(64, 128), 24, 4);
+  } else if (bf16 && t32 > 256) {
+    p.kind = t > 256 ? LIN_T64 : LIN_T64X2;
   } else if (bf16) {
     p.kind = LIN_T32;
     want = split(256, t32, 16, 4);
@@ -952,8 +984,14 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
         launch_tile<TE, 64, 128, 64, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
       break;
     case LIN_T128:
-      if constexpr (sizeof(TE) == 4)
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 128, 128, 64, 64, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      else
         launch_tile<TE, 128, 128, 64, 64, 1, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
+    case LIN_T128X192:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 128, 192, 64, 96, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
   }
   hipError_t e = hipGetLastError();

@@ -100,6 +100,14 @@ def test_few_rows(T, K, N, dt):
     run(T, K, N, dt, bias=False, inplace=True, residual=True)
 
 
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("T,N", [(1100, 4040), (1100, 2312), (1000, 1160), (2050, 1160)])
+@pytest.mark.parametrize("K", [8, 72, 328, 1544, 1608, 3208])
+def test_middling_tiles(T, N, K, dt):
+    # tiles of 128 x 192, 128 x 128 and 64 x 128, whole and split, from one k-step to many, ragged on every side
+    run(T, K, N, dt, act="silu", residual=True, gate_rows=300)
+
+
 @pytest.mark.parametrize("dt,ydt", list(itertools.product([hq.BF16, hq.F32], repeat=2)))
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("T", [1, 7, 70, 700])
