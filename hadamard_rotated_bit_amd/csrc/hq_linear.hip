@@ -821,7 +821,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 namespace {
 
 enum LinKind {
-  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128X192, LIN_PP3, LIN_PP4
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
 };
 
 // Kernel and split count of a product.
@@ -834,11 +834,14 @@ enum LinKind {
 //    against 30.4; 8 x 4608 -> 1152 fp32 the other way too, 16.3 against 13.7).
 //  bf16:
 //    More than 128 tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
-//    rounds of one tile per CU cost less.
+//    rounds of one tile per CU cost less; except that 128 x 128 tiles of eight waves,
+//    two blocks per CU, take up to 32 k-steps where all of them run at once (12288 x
+//    512 -> 512: 14.3 us against 18.5; 6000 x 1000 -> 1000: 23.9 against 26.3; 6000 x
+//    4096 -> 1024, 64 k-steps: no better, 60.8 against 61.5).
 //    Otherwise the tile shrinks until there is about one per CU, with two groups of
 //    waves sharing a tile's k-steps where one group would leave a SIMD one wave:
 //    128 x 192 (1024 x 4608 -> 4608: 52 us against 67 for 256 x 192 and 73 for 64 x
-//    128; 4096 x 1152 -> 1152: 20.7 against 25.4 and 24.6) where 128 x 128 come to
+//    128; 4096 x 4608 -> 1152: 53 against 66 and 72) where 128 x 128 come to
 //    more than one per CU; 128 x 128 (1024 x 4096 -> 4096: 40 us against 45 for 64 x
 //    128) down to one for two CUs and 24 k-steps (512 x 1152 -> 4608, 18 k-steps: 14.2
 //    us for 64 x 128 against 14.8); 64 x 128 (1037 x 1160 -> 2312: 18.6 us against
@@ -882,13 +885,17 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   }
   if (M <= 4) return p;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  const int64_t t = tiles(64, 64), t32 = tiles(32, 64), t128 = tiles(128, 128);
+  const int ksteps = p.kper;
+  if (bf16 && t128 > 256 && t128 <= 512 && ksteps <= 32) {
+    p.kind = LIN_T128W8;
+    return p;
+  }
   if (bf16 && tiles(256, 192) > 128) {
     const int64_t r3 = (tiles(256, 192) + 255) / 256 * 3, r4 = (tiles(256, 256) + 255) / 256 * 4;
     p.kind = r3 < r4 ? LIN_PP3 : LIN_PP4;
     return p;
   }
-  const int64_t t = tiles(64, 64), t32 = tiles(32, 64), t128 = tiles(128, 128);
-  const int ksteps = p.kper;
   // splits of n tiles: `blocks` in all, `least` k-steps each, at most `most`
   auto split = [&](int64_t blocks, int64_t n, int least, int64_t most) {
     return std::max<int64_t>(1, std::min({blocks / n, int64_t(ksteps / least), most}));
@@ -988,6 +995,10 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
         launch_tile<TE, 128, 128, 64, 64, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
       else
         launch_tile<TE, 128, 128, 64, 64, 1, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
+    case LIN_T128W8:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 128, 128, 64, 32, 1, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
     case LIN_T128X192:
       if constexpr (sizeof(TE) == 2)
