@@ -411,8 +411,10 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 # The current stream's handle without building a Stream object (0.1 us instead
-# of 1 us, a tenth of a small call), where torch has the function.
+# of 1 us, a tenth of a small call) and the current device of an initialised
+# runtime (a GPU tensor is at hand), where torch has the functions.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(device: int) -> int:
@@ -432,8 +434,15 @@ class Epilogue:
     gate: Optional[torch.Tensor] = None
     gate_rows: int = 0
 
+    def __post_init__(self):
+        if self.residual is None and self.gate is None:   # the same struct for every call
+            raw = _lib.HqEpilogue(self.act, None, None, self.gate_rows, 0)
+            object.__setattr__(self, "_ref", ctypes.byref(raw))
+
     def _c(self, T: int, d_out: int, dtype: torch.dtype, device: int):
         g, r, ld = self.gate, self.residual, 0
+        if r is None and g is None:
+            return self._ref
         if r is not None:
             _fits(r, "residual", dtype, (T, d_out), device)
         if g is not None:
@@ -453,7 +462,7 @@ class Epilogue:
 def _quant_linear_epi(desc, prepared, X, out, workspace, epilogue):
     T = X.shape[0]
     device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
-    if device != torch.cuda.current_device():   # kernels launch on the current device
+    if device != _current_gpu():   # kernels launch on the current device
         with torch.cuda.device(device):
             return _quant_linear_epi(desc, prepared, X, out, workspace, epilogue)
     ydt = _TORCH[desc.y_dtype]
@@ -507,7 +516,7 @@ def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,
     T = X.shape[0]
     xdt = _TORCH[desc.x_dtype]
     device = _gpu_of(X, "X", xdt, (T, desc.d_in))
-    if device != torch.cuda.current_device():   # kernels launch on the current device
+    if device != _current_gpu():   # kernels launch on the current device
         with torch.cuda.device(device):
             return linear(desc, X, weight, bias, epilogue, out, workspace)
     _fits(weight, "weight", _TORCH[desc.w_dtype], (desc.d_out, desc.d_in), device)
@@ -565,7 +574,7 @@ def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = 
         raise ValueError(f"X must be [samples, positions, channels], got {tuple(X.shape)}")
     S, P, C = X.shape[0], X.shape[1], desc.channels
     device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (S, P, C))
-    if device != torch.cuda.current_device():   # kernels launch on the current device
+    if device != _current_gpu():   # kernels launch on the current device
         with torch.cuda.device(device):
             return group_norm(desc, X, gamma, beta, out, workspace)
     if gamma is not None:
