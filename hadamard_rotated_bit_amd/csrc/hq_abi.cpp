@@ -797,8 +797,12 @@ int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X
       overlap(workspace, need, lin.residual, ny) ||
       overlap(workspace, need, lin.gate, gate_bytes(lin, T, desc->d_out, es)))
     return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
-  // an epilogue of nothing is hq_quant_linear's own
-  const bool any = lin.act.act != hq::ACT_NONE || lin.residual || lin.gate;
+  // an epilogue of nothing is hq_quant_linear's own, or for few tokens the kernel
+  // that gives the same bits sooner (38 x 1280 -> 5896 W4A4: 19.0 us against 8.0);
+  // with group-wise scales its sums have another order
+  const int engine = code_fmt_of(desc) == hq::CODES_E2M3 ? hq::GEMM_FEW_F6 : hq::GEMM_FEW_I8;
+  const bool any = lin.act.act != hq::ACT_NONE || lin.residual || lin.gate ||
+                   (!desc->group && hq::gemm_few_fits(engine, T, desc->d_out));
   return run_quant_linear(desc, prepared, X, T, any ? &lin : nullptr, Y, workspace,
                           workspace_bytes, static_cast<hipStream_t>(stream));
 }

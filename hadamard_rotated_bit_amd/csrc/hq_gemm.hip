@@ -83,10 +83,7 @@ hipError_t launch_gemm(const int8_t* A, int64_t M, const int8_t* B, int64_t N, i
                        int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s) {
   if (M <= 0 || N <= 0) return hipSuccess;
   if (epi && epi->ext) {
-    // up to three 32 x 32 tiles for two CUs: 96 x 4096 -> 4096, 384 tiles, 22.6 us a
-    // call against 23.2; 128 x 1152 -> 4608, 576 tiles, the other way, 13.6 against 12.8
-    if (2 * (((M + 31) / 32) * ((N + 31) / 32)) <= 3 * cu_count())
-      return launch_gemm_few(0, A, M, B, N, K, *epi, s);
+    if (gemm_few_fits(GEMM_FEW_I8, M, N)) return launch_gemm_few(GEMM_FEW_I8, A, M, B, N, K, *epi, s);
     // where 128 x 128 tiles leave CUs idle, 128 x 64 (2000 x 1152 -> 1152: 16.9
     // us a call against 20.5; 8192 x 4096 -> 4096 the other way, 230 against 192)
     if (((M + 127) / 128) * ((N + 127) / 128) < cu_count())

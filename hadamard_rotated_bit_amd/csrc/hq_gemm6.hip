@@ -71,10 +71,7 @@ hipError_t launch_gemm_f6(const uint8_t* A, int64_t M, const uint8_t* B, int64_t
     if (cu_cache[dev] > 0) cus = cu_cache[dev];
   }
   if (epi && epi->ext) {
-    // up to four 32 x 32 tiles per CU: 160 x 1152 -> 4608, 720 tiles, 10.6 us a call
-    // against 12.4, 256 x 4096 -> 4096, 1024 tiles, 18.2 against 20.0; 300 x 4096 ->
-    // 4096, 1280 tiles, the other way, 21.0 against 20.2
-    if (((M + 31) / 32) * ((N + 31) / 32) <= 4 * cus) return launch_gemm_few(1, A, M, B, N, K, *epi, s);
+    if (gemm_few_fits(GEMM_FEW_F6, M, N)) return launch_gemm_few(GEMM_FEW_F6, A, M, B, N, K, *epi, s);
     // where 128 x 128 tiles leave CUs idle, 128 x 64 (2000 x 1152 -> 1152: 16.6
     // us a call against 19.4; 4353 x 4608 -> 1152 the other way, 52 against 48)
     if (((M + 127) / 128) * ((N + 127) / 128) < cus)

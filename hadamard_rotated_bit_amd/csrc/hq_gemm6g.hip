@@ -318,11 +318,8 @@ hipError_t launch_gemm_f6g(const uint8_t* A, int64_t M, const uint8_t* B, int64_
   const int64_t ntiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   GemmEpi ep = *epi;
   ep.prescaled = 1;
-  // up to four 32 x 32 tiles per CU (128 x 4608 -> 1152: 18.1 us a call against 58.3,
-  // 256 x 4096 -> 4096, 1024 tiles, 38 against 55; 512 x 1152 -> 4608, 2304 tiles, the
-  // other way, 38.6 against 27.0)
-  if (ep.ext && ((M + 31) / 32) * ((N + 31) / 32) <= 4 * 256)
-    return launch_gemm_few(1, A, M, B, N, K, ep, s, s_xg, ld_sx, s_wg, ld_sw);
+  if (ep.ext && gemm_few_fits(GEMM_FEW_F6G, M, N))
+    return launch_gemm_few(GEMM_FEW_F6G, A, M, B, N, K, ep, s, s_xg, ld_sx, s_wg, ld_sw);
   if (ep.ext)
     hipLaunchKernelGGL((gemm_f6g_kernel<BM, BN, 64, 64, 4, F6_GROUP, 2, 3, true>),
                        dim3(unsigned(ntiles)), dim3(256), 0, s, A, M, B, N, K, ep, s_xg, ld_sx,

@@ -208,25 +208,40 @@ __global__ __launch_bounds__(64 * FEW_NW) void gemm_few_kernel(const uint8_t* __
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    // the tiled kernels' expressions, term by term (the same bits)
     y[e] = fmaf(mu, cb[e], bb[e]);
-    if (ep.rank) y[e] += __uint_as_float(s[FEW_NW * SLOT + e]);
     y[e] = ep.prescaled ? float(sum[e]) + y[e] : fmaf(float(sum[e]), sx * sw[e], y[e]);
+    if (ep.rank) y[e] += __uint_as_float(s[FEW_NW * SLOT + e]);
   }
   finish_piece(y, m, n, N, ep.lin);
 }
 
 }  // namespace
 
-hipError_t launch_gemm_few(int f6, const void* A, int64_t M, const void* B, int64_t N, int K,
+// Four tiles per CU on the FP6 engine (a call of 160 x 1152 -> 4608, 720 tiles: 10.6
+// us against 12.4 with the tiled kernel; 256 x 4096 -> 4096, 1024 tiles: 18.2 against
+// 20.0; 300 x 4096 -> 4096, 1280 tiles, the other way, 21.0 against 20.2), also with
+// group-wise scales (1024 tiles: 38 against 55; 512 x 1152 -> 4608, 2304 tiles, the
+// other way, 38.6 against 27.0); three for two CUs with int8 codes (96 x 4096 ->
+// 4096, 384 tiles: 22.6 against 23.2; 128 x 1152 -> 4608, 576 tiles, the other way,
+// 13.6 against 12.8).
+bool gemm_few_fits(int engine, int64_t M, int64_t N) {
+  return ((M + 31) / 32) * ((N + 31) / 32) <= (engine == GEMM_FEW_I8 ? 384 : 1024);
+}
+
+hipError_t launch_gemm_few(int engine, const void* A, int64_t M, const void* B, int64_t N, int K,
                            const GemmEpi& ep, hipStream_t s, const float* s_xg, int64_t ld_sx,
                            const float* s_wg, int64_t ld_sw) {
   if (K % 128) return hipErrorInvalidValue;
   const dim3 grid(unsigned((N + 31) / 32), unsigned((M + 31) / 32)), block(64 * FEW_NW);
   const uint8_t *a = static_cast<const uint8_t*>(A), *b = static_cast<const uint8_t*>(B);
   const GroupScales gs = {s_xg, ld_sx, s_wg, ld_sw};
-  if (s_xg) hipLaunchKernelGGL(gemm_few_kernel<EngF6G>, grid, block, 0, s, a, M, b, N, K, ep, gs);
-  else if (f6) hipLaunchKernelGGL(gemm_few_kernel<EngF6>, grid, block, 0, s, a, M, b, N, K, ep, gs);
-  else hipLaunchKernelGGL(gemm_few_kernel<EngI8>, grid, block, 0, s, a, M, b, N, K, ep, gs);
+  if (engine == GEMM_FEW_F6G)
+    hipLaunchKernelGGL(gemm_few_kernel<EngF6G>, grid, block, 0, s, a, M, b, N, K, ep, gs);
+  else if (engine == GEMM_FEW_F6)
+    hipLaunchKernelGGL(gemm_few_kernel<EngF6>, grid, block, 0, s, a, M, b, N, K, ep, gs);
+  else
+    hipLaunchKernelGGL(gemm_few_kernel<EngI8>, grid, block, 0, s, a, M, b, N, K, ep, gs);
   return hipGetLastError();
 }
 

@@ -2,6 +2,8 @@
 // its tuning harness. See hq_gemm.hip for the operation and the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "hq_device.h"
 #include "hq_epilogue.h"
 #include "hq_gemm_types.h"
@@ -166,8 +168,7 @@ __device__ __forceinline__ void gemm_epilogue(AccT (&acc)[TM][TN], uint8_t* smem
 }
 
 // Dequant epilogue followed by Y = residual + gate phi(y) (hq_epilogue.h): the
-// values of gemm_epilogue (the low-rank product accumulates onto mu c + b instead
-// of being added to it), staged in fp32 per 32-row slice in a part of the
+// values of gemm_epilogue, staged in fp32 per 32-row slice in a part of the
 // idle LDS that belongs to the wave and taken back as rows of eight columns
 // per lane, so that residual, gate and Y move in whole row segments and phi is
 // written once, in a rolled loop (unrolled over the accumulators its code
@@ -208,17 +209,33 @@ __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* 
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int64_t nb = n0 + wn0 + j * 32;
-      // mu c + bias, then the low-rank product on top of it
-      v16f base;
+      const AccT& a = acc[i][j];
+      // the expressions of gemm_epilogue, term by term (the same bits)
+      auto stage = [&](auto with_lr, const v16f& lr) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int cl = j * 32 + 8 * g + 4 * lhalf;
-        const float4 cb = *reinterpret_cast<const float4*>(P + BN + wn0 + cl);
-        const float4 bb = *reinterpret_cast<const float4*>(P + 2 * BN + wn0 + cl);
-        base[4 * g + 0] = fmaf(mu, cb.x, bb.x);
-        base[4 * g + 1] = fmaf(mu, cb.y, bb.y);
-        base[4 * g + 2] = fmaf(mu, cb.z, bb.z);
-        base[4 * g + 3] = fmaf(mu, cb.w, bb.w);
+        for (int g = 0; g < 4; ++g) {
+          const int cl = j * 32 + 8 * g + 4 * lhalf;
+          const float4 sw = *reinterpret_cast<const float4*>(P + wn0 + cl);
+          const float4 cb = *reinterpret_cast<const float4*>(P + BN + wn0 + cl);
+          const float4 bb = *reinterpret_cast<const float4*>(P + 2 * BN + wn0 + cl);
+          float4 y;
+          y.x = fmaf(float(a[4 * g + 0]), sx * sw.x, fmaf(mu, cb.x, bb.x));
+          y.y = fmaf(float(a[4 * g + 1]), sx * sw.y, fmaf(mu, cb.y, bb.y));
+          y.z = fmaf(float(a[4 * g + 2]), sx * sw.z, fmaf(mu, cb.z, bb.z));
+          y.w = fmaf(float(a[4 * g + 3]), sx * sw.w, fmaf(mu, cb.w, bb.w));
+          if constexpr (decltype(with_lr)::value) {
+            y.x += lr[4 * g + 0];
+            y.y += lr[4 * g + 1];
+            y.z += lr[4 * g + 2];
+            y.w += lr[4 * g + 3];
+          }
+          *reinterpret_cast<float4*>(stg + lrow * PITCH + cl) = y;
+        }
+      };
+      v16f lr = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      if (!ep.rank) {
+        stage(std::false_type{}, lr);
+        continue;
       }
       for (int k0 = 0; k0 < ep.rank; k0 += 16) {
         float f[8];
@@ -227,25 +244,14 @@ __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* 
         const int64_t nr = nb + lrow < N ? nb + lrow : N - 1;
         const int64_t off = nr * ep.rank + k0 + 8 * lhalf;
         const v8bf wh = *reinterpret_cast<const v8bf*>(ep.l2_hi + off);
-        base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, uh, base, 0, 0, 0);
+        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, uh, lr, 0, 0, 0);
         if (!ep.l2_lo_zero) {
           const v8bf wl = *reinterpret_cast<const v8bf*>(ep.l2_lo + off);
-          base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wl, uh, base, 0, 0, 0);
+          lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wl, uh, lr, 0, 0, 0);
         }
-        base = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, ul, base, 0, 0, 0);
+        lr = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wh, ul, lr, 0, 0, 0);
       }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int cl = j * 32 + 8 * g + 4 * lhalf;
-        const float4 sw = *reinterpret_cast<const float4*>(P + wn0 + cl);
-        const AccT& a = acc[i][j];
-        float4 y;
-        y.x = fmaf(float(a[4 * g + 0]), sx * sw.x, base[4 * g + 0]);
-        y.y = fmaf(float(a[4 * g + 1]), sx * sw.y, base[4 * g + 1]);
-        y.z = fmaf(float(a[4 * g + 2]), sx * sw.z, base[4 * g + 2]);
-        y.w = fmaf(float(a[4 * g + 3]), sx * sw.w, base[4 * g + 3]);
-        *reinterpret_cast<float4*>(stg + lrow * PITCH + cl) = y;
-      }
+      stage(std::true_type{}, lr);
     }
     __builtin_amdgcn_wave_barrier();
     finish_rows<4 * TN, Q>(stg, PITCH, lane, m0 + wm0 + 32 * i, n0 + wn0, M, N, ep.lin);

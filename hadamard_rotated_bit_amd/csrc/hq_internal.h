@@ -138,9 +138,12 @@ hipError_t launch_gemm_f6g(const uint8_t* A, int64_t M, const uint8_t* B, int64_
 hipError_t launch_gemm_f6(const uint8_t* A, int64_t M, const uint8_t* B, int64_t N, int K,
                           int32_t* acc_out, int64_t ldc, const GemmEpi* epi, hipStream_t s);
 
-// The same products with the extended epilogue for few tokens (epi.ext; f6:
-// E2M3 codes, otherwise int8; s_xg and s_wg as launch_gemm_f6g's, or NULL).
-hipError_t launch_gemm_few(int f6, const void* A, int64_t M, const void* B, int64_t N, int K,
+// The same products with the extended epilogue for few tokens (epi.ext): E2M3
+// codes, E2M3 codes with group-wise scales (s_xg and s_wg as launch_gemm_f6g's) or
+// int8 codes. gemm_few_fits: whether an M x N product is small enough for it.
+enum { GEMM_FEW_F6, GEMM_FEW_F6G, GEMM_FEW_I8 };
+bool gemm_few_fits(int engine, int64_t M, int64_t N);
+hipError_t launch_gemm_few(int engine, const void* A, int64_t M, const void* B, int64_t N, int K,
                            const GemmEpi& ep, hipStream_t s, const float* s_xg = nullptr,
                            int64_t ld_sx = 0, const float* s_wg = nullptr, int64_t ld_sw = 0);
 

@@ -104,6 +104,18 @@ def test_few_tokens(K, bits):
         check(desc, prep, X, "gelu_tanh", True, 3, g, inplace=True)
 
 
+@pytest.mark.parametrize("form", list(FORMS))
+def test_nothing_to_do_gives_the_plain_calls_bits(form):
+    # no epilogue, and a residual of zeros (whatever kernel takes either), at few tokens and at many
+    for T, N in ((1, 8), (38, 1160), (300, 264), (1201, 1160)):
+        kw = dict(FORMS[form])
+        desc, prep, X, g = layer(T, kw.pop("K"), N, **kw)
+        Y = hq.quant_linear(desc, prep, X)
+        assert torch.equal(hq.quant_linear(desc, prep, X, epilogue=hq.Epilogue()), Y)
+        if not desc.group:      # group-wise sums have an order of their own in every kernel
+            assert torch.equal(hq.quant_linear(desc, prep, X, epilogue=hq.Epilogue(residual=torch.zeros_like(Y))), Y)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_few_tokens_are_the_same_rows(bits):
     # a token's outputs do not depend on how many others the call has, whatever kernel takes it
