@@ -569,9 +569,12 @@ int gcd_i(int a, int b) { return b ? gcd_i(b, a % b) : a; }
 // where a sample's slabs share an XCD's L2 and wider ones would leave CUs idle
 // (the same in bf16: 9.7 us against 11.8); where all positions are less than
 // one pass of 256 lanes, they are doubled. Up to 8 rows per lane a block keeps
-// its slab in registers (1 x 1024 x 512 fp32: 8.4 us against 12.9 for two
-// launches); longer ones take the chunked form, which spreads a sample over
-// every CU (1 x 4096 x 512 bf16: 14.7 us against 21).
+// its slab in registers (1 x 1024 x 512 fp32: 8.4 us against 9.6 for two
+// launches); longer ones, and those that would be less than 48 blocks of 1024
+// threads (2 x 1024 x 640 bf16, 32 blocks: 11.2 us against 12.6; 50 x 3000 x 8, 50
+// blocks, the other way, 9.2 against 10.0), take the chunked form, which spreads a
+// sample over every CU, at 4 rows per lane or more (1 x 4096 x 320 bf16: 11.7 us
+// against 13.1 with 8, 1 x 65536 x 16 fp32: 11.0 against 13.3).
 NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   NormPlan p = {};
   if (P == 1 && C / G % 8 == 0) {
@@ -587,6 +590,7 @@ NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   for (int nt : {256, 1024}) {
     const int VR = slab / 8;
     if (VR > nt || slab / cg > NORM_BLOCK_GROUPS) continue;
+    if (nt == 1024 && S * ((C + slab - 1) / slab) < 48) continue;
     const int64_t need = (P + nt / VR - 1) / (nt / VR);   // rows per lane
     if (need <= 8) {
       p.block = 1;
@@ -599,7 +603,7 @@ NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   p.nt = C <= 2048 ? 256 : 1024;
   const int RY = p.nt / (C / 8);
   int64_t want = (1024 + S - 1) / S;                      // about four blocks per CU
-  const int64_t most = (P + RY * 8 - 1) / (RY * 8);       // at least 8 rows per lane
+  const int64_t most = (P + RY * 4 - 1) / (RY * 4);       // at least 4 rows per lane
   if (want > most) want = most;
   p.rpc = (P + want - 1) / want;
   p.chunks = int((P + p.rpc - 1) / p.rpc);
