@@ -101,9 +101,10 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__
 // upper 16 bits of x (a bf16 by truncation), m those of x - h and l = x - h - m,
 // which has 8 bits left, all three exact. The product keeps
 //   x w = h h + (h m + m h) + (h l + m m + l h)
-// and leaves m l, l m and l l, at most 2^-22 and on average 2^-24 of |x w|, the
-// size of the fp32 rounding of the product itself; sums stay in fp32. Six MFMAs
-// of 32 cycles per 16 k instead of eight v_mfma_f32_32x32x2_f32 of 64 cycles.
+// and leaves m l and l m, each at most 2^-22 of |x w| (with |x| in [2^e, 2^(e+1)):
+// m < 2^(e-7), l < 2^(e-15)), and l l below 2^-29; sums stay in fp32. Six MFMAs of 32
+// cycles per 16 k instead of eight v_mfma_f32_32x32x2_f32 of 64 cycles. With m
+// rounded to nearest the two are half as large, but every size took 2 to 4 % longer.
 // (The split of an infinity is inf, NaN, NaN: an infinite operand gives NaN.)
 // The 8 values per lane are two chunks, substeps 2 t and 2 t + 1: any pairing
 // of k is the same sum, as both operands use the same one.
@@ -136,26 +137,25 @@ __device__ __forceinline__ v16f mfma_bf16(const v8bf& w, const v8bf& x, const v1
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, c, 0, 0, 0);
 }
 
-// Accumulators started at the bias: register r of strip j belongs to column
-// n + 32 j + 8 (r / 4) + r % 4 (the same for every row), zero without a bias.
-template <int TM, int TN>
-__device__ __forceinline__ void bias_acc(v16f (&acc)[TM][TN], const float* __restrict__ bias,
-                                         int64_t n, int64_t N) {
+// The bias as accumulators: register r of strip j belongs to column n + 32 j +
+// 8 (r / 4) + r % 4 (the same for every row), zero without a bias. bf16 products
+// start from it; an fp32 one would round all six of its terms at the bias's size, so
+// it is added to their sum.
+template <int TN>
+__device__ __forceinline__ void bias_strips(v16f (&b)[TN], const float* __restrict__ bias, int64_t n,
+                                            int64_t N) {
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int64_t c = n + 32 * j + 8 * g;
-      const float4 b = bias && c < N ? *reinterpret_cast<const float4*>(bias + c)
+      const float4 v = bias && c < N ? *reinterpret_cast<const float4*>(bias + c)
                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      acc[0][j][4 * g] = b.x;
-      acc[0][j][4 * g + 1] = b.y;
-      acc[0][j][4 * g + 2] = b.z;
-      acc[0][j][4 * g + 3] = b.w;
+      b[j][4 * g] = v.x;
+      b[j][4 * g + 1] = v.y;
+      b[j][4 * g + 2] = v.z;
+      b[j][4 * g + 3] = v.w;
     }
-#pragma unroll
-    for (int i = 1; i < TM; ++i) acc[i][j] = acc[0][j];
-  }
 }
 
 // A wave's staged 32 rows as raw sums into part [M, N].
@@ -384,8 +384,15 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
     pb[s] = co + uint32_t((BM + wn0 + lrow) * 128);
   }
 
-  v16f acc[TM][TN];
-  bias_acc<TM, TN>(acc, part || grp ? nullptr : ep.bias, n0 + wn0 + 4 * lhalf, N);
+  v16f acc[TM][TN], bias[TN];
+  bias_strips<TN>(bias, part || grp ? nullptr : ep.bias, n0 + wn0 + 4 * lhalf, N);
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if constexpr (sizeof(TE) == 2) acc[i][j] = bias[j];
+      else acc[i][j] = v16f{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    }
 #pragma unroll
   for (int p = 0; p < S - 1; ++p) HL_ISSUE(p);
   int buf = 0;
@@ -407,6 +414,13 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 #undef HL_ISSUE
   wait_vm_lgkm0<0>();  // no LDS write may land in the staging area (or after the block ends)
   __builtin_amdgcn_s_barrier();
+
+  if constexpr (sizeof(TE) == 4) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] += bias[j];
+  }
 
   // Each wave stages its 32-row slices in its own part of the LDS and takes
   // them back as rows, eight consecutive columns per lane: whole row segments
@@ -783,8 +797,8 @@ __global__ __launch_bounds__(512) void linear_few_kernel(const TE* __restrict__ 
   const int r = int(threadIdx.x) / 2, c = 8 * (int(threadIdx.x) % 2);
   const int64_t m = m0 + r, n = n0 + c;
   if (r >= 16 || m >= M || n >= N) return;
-  float v[8] = {};
-  if (ep.bias) load8(ep.bias + n, v);
+  float v[8] = {}, b[8] = {};
+  if (ep.bias) load8(ep.bias + n, b);
 #pragma unroll
   for (int g = 0; g < NW; ++g) {
     float a[8];
@@ -792,6 +806,8 @@ __global__ __launch_bounds__(512) void linear_few_kernel(const TE* __restrict__ 
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += a[e];
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] += b[e];
   finish_piece(v, m, n, N, ep);
 }
 
@@ -805,14 +821,16 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
   if (i >= M * npr) return;
   const int64_t m = i / npr, n = (i - m * npr) * 8;
   const float* p = part + m * N + n;
-  float v[8] = {};
-  if (ep.bias) load8(ep.bias + n, v);
+  float v[8] = {}, b[8] = {};
+  if (ep.bias) load8(ep.bias + n, b);
   for (int s = 0; s < splits; ++s) {
     float a[8];
     load8(p + int64_t(s) * M * N, a);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += a[e];
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] += b[e];
   finish_piece(v, m, n, N, ep);
 }
 

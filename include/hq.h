@@ -336,8 +336,8 @@ size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T);
  *  Neither Y nor the workspace may overlap X, weight, bias, the gate or each
  *  other, nor the workspace the residual. The same inputs always give the same bits (sums have a fixed order
  *  for a given shape). fp32 operands enter the matrix units as exact sums of
- *  three bf16 parts; the parts' products below 2^-22 of the whole are left out,
- *  which is the size of an fp32 product's own rounding. An infinite or NaN
+ *  three bf16 parts; of a product's nine partial ones the two that are at most
+ *  2^-22 of it (2^-25 on average) and the one below 2^-29 are left out. An infinite or NaN
  *  value of X or weight makes the outputs it enters infinite or NaN, and no
  *  others. */
 int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,

@@ -270,3 +270,17 @@ def test_graph_replays_match_eager(T, K, N):
         assert torch.equal(out, Ya if rep % 2 == 0 else Yb), f"replay {rep}"
         assert torch.equal(other, Yb)
     del graph
+
+
+@pytest.mark.parametrize("T", [1, 4, 7, 40, 300, 700, 2100])
+@pytest.mark.parametrize("K,N", [(8, 1160), (24, 4104), (264, 2312), (2056, 136)])
+def test_large_bias_of_an_fp32_sum(T, K, N):
+    # the bias is added once, to the whole sum. Roundings of the sum: its K values in
+    # any order, the six terms of a product, 2 x 2^-22 = 8 U32 for the two left out
+    X, W, b, _ = make(T, K, N, hq.F32, seed=9)
+    b = 1000.0 * b
+    x, w = X.double(), W.double()
+    v = x @ w.t().contiguous() + b.double()
+    tol = (K + 6 + 8) * U32 * (x.abs() @ w.abs().t().contiguous()) + U32 * v.abs()
+    Y = hq.linear(hq.LinearDesc(K, N), X, W, b)
+    assert_within(Y, v, tol * (1 + U32) + 1e-30, f"T={T} K={K} N={N}")
