@@ -284,3 +284,22 @@ def test_large_bias_of_an_fp32_sum(T, K, N):
     tol = (K + 6 + 8) * U32 * (x.abs() @ w.abs().t().contiguous()) + U32 * v.abs()
     Y = hq.linear(hq.LinearDesc(K, N), X, W, b)
     assert_within(Y, v, tol * (1 + U32) + 1e-30, f"T={T} K={K} N={N}")
+
+
+@pytest.mark.parametrize("dt,T,K,N", [(hq.BF16, 1_100_003, 8, 2048), (hq.F32, 1_100_003, 16, 2048), (hq.BF16, 2_200_001, 1024, 8)])
+def test_more_than_32_bits_of_elements(dt, T, K, N):
+    # X or Y has more than 2^31 elements; rows at both ends and around the wraps against calls of their own
+    X, W, b, g = make(T, K, N, dt)
+    gate = torch.randn(3, N, generator=g, device="cuda").to(DT[dt])
+    rows = -(-T // 3)
+    desc = hq.LinearDesc(K, N, dt, dt, dt)
+    Y = hq.linear(desc, X, W, b, epilogue=hq.Epilogue(hq.HQ_ACT_RELU, gate=gate, gate_rows=rows))
+    wide = max(K, N)
+    for at in (0, 2 ** 31 // wide - 40, 2 ** 30 // wide - 40, 2 ** 29 // wide - 40, T - 80):
+        part = slice(at, at + 80)
+        x, w = X[part].double(), W.double()
+        v = x @ w.t().contiguous() + b.double()
+        err = (K + 16) * U32 * (x.abs() @ w.abs().t().contiguous()) + 8 * U32 * (v.abs() + b.abs().double())
+        G = gate[torch.arange(at, at + 80, device="cuda") // rows]
+        y, tol = epilogue64(v, err, "relu", dt, None, G, 1)
+        assert_within(Y[part], y, tol, f"rows from {at}")

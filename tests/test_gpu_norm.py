@@ -251,3 +251,14 @@ def test_more_samples_than_one_grid(C, G):
     for a in (0, (1 << 20) - 50, 1 << 23, S - 100):
         part = X[a:a + 100].contiguous()
         assert torch.equal(Y[a:a + 100], hq.group_norm(desc, part))
+
+
+@pytest.mark.parametrize("S,P,C,G", [(1_100_003, 1, 2048, 1), (3, 400_000, 2048, 32), (20_000, 60, 2048, 8)])
+def test_more_than_32_bits_of_elements(S, P, C, G):
+    # samples around the wraps against calls of their own
+    X = torch.randn(S, P, C, device="cuda", dtype=torch.bfloat16)
+    desc = hq.NormDesc(C, G, 1e-5, hq.HQ_ACT_SILU, hq.BF16, hq.BF16)
+    Y = hq.group_norm(desc, X)
+    for at in {0, min(S - 1, 2 ** 31 // (P * C)), min(S - 1, 2 ** 30 // (P * C)), S - 1}:
+        y, tol = norm64(X[at:at + 1], G, None, None, 1e-5, "silu", hq.BF16)
+        assert_within(Y[at].view(-1, C), y.view(-1, C), tol.view(-1, C), f"sample {at}")
