@@ -295,7 +295,7 @@ __device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[3][4], const 
 // contiguous range of tiles where the count n is a multiple of 8; this does it
 // for other counts of no more than one tile per CU (the first n mod 8 XCDs have
 // one tile more): a weight row is then fetched by one or two XCDs instead of
-// all (300 x 4096 -> 1152 bf16, 180 tiles: 13.8 us against 15.6). With several
+// all (300 x 4096 -> 1152 bf16, 180 tiles of two groups: 13.8 us against 15.6). With several
 // tiles per CU the plain order, in which an XCD keeps to one tile row, is as good
 // or better (1037 x 1160 -> 2312, 323 tiles: 18.8 us against 20.3).
 __device__ __forceinline__ int xcd_tile(int tile, int n) {
@@ -317,7 +317,7 @@ __device__ __forceinline__ int xcd_tile(int tile, int n) {
 // g + G, ...; one barrier per G steps), for products with too few tiles to fill
 // the CUs: their sums meet in LDS, in group order.
 // Few tiles are bound by the latency of their k-steps (300 x 4096 -> 1152 bf16:
-// 13.8 us; 1037 x 1160 -> 2312: 18.3 us, where rows of 2320 bytes straddle the
+// 11.9 us; 1037 x 1160 -> 2312: 18.3 us, where rows of 2320 bytes straddle the
 // 128-byte lines), fp32 by the vector instructions of the splits beside the MFMAs
 // (8192 x 4096 -> 4096: 1.36 ms, 202 TFLOP/s; 12288 x 256 -> 256: 17.6 us).
 template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
@@ -839,7 +839,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 namespace {
 
 enum LinKind {
-  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
 };
 
 // Kernel and split count of a product.
@@ -868,8 +868,10 @@ enum LinKind {
 //    Fewer 64 x 64 tiles than CUs: two groups of waves, 64 x 64 tiles (512 x 4096 ->
 //    1152: 15.3 us against 15.7 for one group split in three over blocks; 512 x 1152
 //    -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where those are no more than the
-//    CUs (300 x 4096 -> 1152: 13.8 us against 17.0 for 64 x 64 of one group split in
-//    four).
+//    CUs (300 x 1152 -> 1152: 6.2 us against 6.7), four groups from 32 k-steps on
+//    where a split would not leave each block as many (300 x 4096 -> 1152: 11.9 us
+//    against 13.6 with two; 77 x 2048 -> 1280: 7.6 against 8.3 with two and a split;
+//    128 x 4096 -> 1152, 72 tiles, the other way, 10.9 against 10.4).
 //    What still leaves CUs idle is split over K, at 16 k-steps a block or more (64
 //    x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four; 32 x 1152
 //    -> 4608: 5.6 us whole against 7.3): a split costs a second launch and the
@@ -928,8 +930,9 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   } else if (bf16 && t32 > 256) {
     p.kind = t > 256 ? LIN_T64 : LIN_T64X2;
   } else if (bf16) {
-    p.kind = LIN_T32;
-    want = split(256, t32, 16, 4);
+    const bool four = ksteps >= 32 && split(256, t32, 32, 4) == 1;
+    p.kind = four ? LIN_T32X4 : LIN_T32;
+    want = four ? 1 : split(256, t32, 16, 4);
   } else if (M > 64 && t128 * split128 >= 200) {
     p.kind = LIN_T128;
     want = split128;
@@ -997,6 +1000,10 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       }
       break;
     case LIN_T32: launch_tile<TE, 32, 64, 32, 32, 2, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
+    case LIN_T32X4:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 32, 64, 32, 32, 4, 3, 1>(X, M, W, N, K, p, part, ep, s);
+      break;
     case LIN_T64X2:
       if constexpr (sizeof(TE) == 2)
         launch_tile<TE, 64, 64, 32, 32, 2, 3, 1>(X, M, W, N, K, p, part, ep, s);

@@ -85,10 +85,10 @@ def test_wide_tiles(T, N, K):
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
-@pytest.mark.parametrize("K", [8, 64, 72, 136, 192, 328, 1096, 2056])
-@pytest.mark.parametrize("T,N", [(9, 72), (100, 1160), (590, 1160)])
+@pytest.mark.parametrize("K", [8, 64, 72, 136, 192, 328, 1096, 2056, 2248, 4104])
+@pytest.mark.parametrize("T,N", [(9, 72), (100, 1160), (250, 1160), (590, 1160)])
 def test_shared_k_steps(T, N, K, dt):
-    # two groups of waves on a tile's k-steps: fewer steps than groups, odd and even counts, with and without a split
+    # two and four groups of waves on a tile's k-steps: fewer steps than groups, odd and even counts, with and without a split
     run(T, K, N, dt, act="silu", residual=True, gate_rows=7)
 
 
