@@ -295,9 +295,10 @@ __device__ __forceinline__ void lds_kstep(v4i (&a)[2][4], v4i (&b)[3][4], const 
 // contiguous range of tiles where the count n is a multiple of 8; this does it
 // for other counts of no more than one tile per CU (the first n mod 8 XCDs have
 // one tile more): a weight row is then fetched by one or two XCDs instead of
-// all (300 x 4096 -> 1152 bf16, 180 tiles of two groups: 13.8 us against 15.6). With several
+// all (300 x 4096 -> 1152 bf16, 180 tiles of two groups: 13.8 us against 15.6; 367 x
+// 3808 -> 6896, 162 tiles of 128 x 128: 33.6 against 36.3). With several
 // tiles per CU the plain order, in which an XCD keeps to one tile row, is as good
-// or better (1037 x 1160 -> 2312, 323 tiles: 18.8 us against 20.3).
+// or better (1037 x 1160 -> 2312 in 323 tiles of 64 x 128: 18.8 us against 20.3).
 __device__ __forceinline__ int xcd_tile(int tile, int n) {
   const int odd = n & 7, x = tile & 7;
   if (odd == 0 || n > 256) return tile;
@@ -317,7 +318,7 @@ __device__ __forceinline__ int xcd_tile(int tile, int n) {
 // g + G, ...; one barrier per G steps), for products with too few tiles to fill
 // the CUs: their sums meet in LDS, in group order.
 // Few tiles are bound by the latency of their k-steps (300 x 4096 -> 1152 bf16:
-// 11.9 us; 1037 x 1160 -> 2312: 18.3 us, where rows of 2320 bytes straddle the
+// 11.9 us; 1037 x 1160 -> 2312: 16.7 us, where rows of 2320 bytes straddle the
 // 128-byte lines), fp32 by the vector instructions of the splits beside the MFMAs
 // (8192 x 4096 -> 4096: 1.36 ms, 202 TFLOP/s; 12288 x 256 -> 256: 17.6 us).
 template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
@@ -839,7 +840,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 namespace {
 
 enum LinKind {
-  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128X2, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
 };
 
 // Kernel and split count of a product.
@@ -856,22 +857,24 @@ enum LinKind {
 //    two blocks per CU, take up to 32 k-steps where all of them run at once (12288 x
 //    512 -> 512: 14.3 us against 18.5; 6000 x 1000 -> 1000: 23.9 against 26.3; 6000 x
 //    4096 -> 1024, 64 k-steps: no better, 60.8 against 61.5).
-//    Otherwise the tile shrinks until there is about one per CU, with two groups of
-//    waves sharing a tile's k-steps where one group would leave a SIMD one wave:
-//    128 x 192 (1024 x 4608 -> 4608: 52 us against 67 for 256 x 192 and 73 for 64 x
-//    128; 4096 x 4608 -> 1152: 53 against 66 and 72) where 128 x 128 come to
-//    more than one per CU; 128 x 128 (1024 x 4096 -> 4096: 40 us against 45 for 64 x
-//    128) down to one for two CUs and 24 k-steps (512 x 1152 -> 4608, 18 k-steps: 14.2
-//    us for 64 x 128 against 14.8); 64 x 128 (1037 x 1160 -> 2312: 18.6 us against
-//    22.5 for 64 x 64); 64 x 64 (2048 x 1152 -> 1152: 13.9 us), or with 48 k-steps 64 x
-//    128 split over K (1024 x 4608 -> 1152: 23.7 us in three against 27.8).
-//    Fewer 64 x 64 tiles than CUs: two groups of waves, 64 x 64 tiles (512 x 4096 ->
-//    1152: 15.3 us against 15.7 for one group split in three over blocks; 512 x 1152
-//    -> 1152: 7.2 us against 8.2), and 32 x 64 tiles where those are no more than the
-//    CUs (300 x 1152 -> 1152: 6.2 us against 6.7), four groups from 32 k-steps on
-//    where a split would not leave each block as many (300 x 4096 -> 1152: 11.9 us
-//    against 13.6 with two; 77 x 2048 -> 1280: 7.6 against 8.3 with two and a split;
-//    128 x 4096 -> 1152, 72 tiles, the other way, 10.9 against 10.4).
+//    Otherwise the tile shrinks until there is about one per CU:
+//    more than one 128 x 128 per CU: 128 x 192 with two groups of waves on a tile's
+//    k-steps (1024 x 4608 -> 4608: 52 us against 67 for 256 x 192 and 59 for 128 x
+//    128; 4096 x 4608 -> 1152: 53 against 66 and 59);
+//    more than one for two CUs: 128 x 128, eight waves and three stages (1037 x 1160
+//    -> 2312: 17.2 us against 19.6 for 64 x 128; 367 x 3808 -> 6896: 33.7 against 64),
+//    or two groups of four where most CUs have one and K is long (1024 x 4096 -> 4096:
+//    40.0 us against 42.6);
+//    more 64 x 64 than CUs: 64 x 128 with two groups of eight waves (512 x 4096 ->
+//    4096: 24.5 us against 30.7 for one group of four, 1024 x 1152 -> 1152: 9.4 against
+//    10.0 for 64 x 64);
+//    fewer: 64 x 64 with two groups (512 x 4096 -> 1152: 15.3 us against 15.7 for one
+//    group split in three over blocks; 256 x 4096 -> 4096: 15.8 us against 20.2 for 64
+//    x 128), and 32 x 64 tiles where those are no more than the CUs (300 x 1152 ->
+//    1152: 6.2 us against 6.7), with four groups from 32 k-steps on where a split would
+//    not leave each block as many (300 x 4096 -> 1152: 11.9 us against 13.6 with two;
+//    77 x 2048 -> 1280: 7.6 against 8.3 with two and a split; 128 x 4096 -> 1152, 72
+//    tiles, the other way, 10.9 against 10.4).
 //    What still leaves CUs idle is split over K, at 16 k-steps a block or more (64
 //    x 4096 -> 4096: 11.9 us in two against 13.2 whole and 12.7 in four; 32 x 1152
 //    -> 4608: 5.6 us whole against 7.3): a split costs a second launch and the
@@ -922,13 +925,10 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   };
   const int64_t split128 = split(512, t128, 12, 6);
   int64_t want = 1;
-  if (bf16 && (t128 > 256 || (t128 > 128 && ksteps >= 24))) {
-    p.kind = t128 > 256 ? LIN_T128X192 : LIN_T128;
-  } else if (bf16 && (tiles(64, 128) >= 256 || (t > 256 && ksteps >= 48))) {
-    p.kind = LIN_T64X128;
-    want = split(512, tiles(64, 128), 24, 4);
+  if (bf16 && t128 > 128) {
+    p.kind = t128 > 256 ? LIN_T128X192 : t128 > 192 && ksteps >= 48 ? LIN_T128X2 : LIN_T128;
   } else if (bf16 && t32 > 256) {
-    p.kind = t > 256 ? LIN_T64 : LIN_T64X2;
+    p.kind = t > 256 ? LIN_T64X128 : LIN_T64X2;
   } else if (bf16) {
     const bool four = ksteps >= 32 && split(256, t32, 32, 4) == 1;
     p.kind = four ? LIN_T32X4 : LIN_T32;
@@ -1010,16 +1010,23 @@ hipError_t launch_typed(const TE* X, int64_t M, const TE* W, int64_t N, int K, f
       else
         launch_tile<TE, 64, 64, 32, 32, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
-    case LIN_T64: launch_tile<TE, 64, 64, 32, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s); break;
+    case LIN_T64:
+      if constexpr (sizeof(TE) == 4)
+        launch_tile<TE, 64, 64, 32, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
     case LIN_T64X128:
       if constexpr (sizeof(TE) == 2)
-        launch_tile<TE, 64, 128, 64, 32, 1, 3, 2>(X, M, W, N, K, p, part, ep, s);
+        launch_tile<TE, 64, 128, 32, 32, 2, 3, 1>(X, M, W, N, K, p, part, ep, s);
       break;
     case LIN_T128:
       if constexpr (sizeof(TE) == 2)
-        launch_tile<TE, 128, 128, 64, 64, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
+        launch_tile<TE, 128, 128, 64, 32, 1, 3, 1>(X, M, W, N, K, p, part, ep, s);
       else
         launch_tile<TE, 128, 128, 64, 64, 1, 2, 2>(X, M, W, N, K, p, part, ep, s);
+      break;
+    case LIN_T128X2:
+      if constexpr (sizeof(TE) == 2)
+        launch_tile<TE, 128, 128, 64, 64, 2, 2, 2>(X, M, W, N, K, p, part, ep, s);
       break;
     case LIN_T128W8:
       if constexpr (sizeof(TE) == 2)
