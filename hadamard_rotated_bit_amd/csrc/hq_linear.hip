@@ -881,8 +881,9 @@ enum LinKind {
 //    partial sums.
 //  fp32 computes six times as much per byte and pays for its fragments' splits by
 //  the rows and columns of a wave:
-//    128 x 128 tiles for more than 64 rows where they, split over K at 12 k-steps a
-//    block or more, come to 200 blocks (512 x 4096 -> 1152: 42 us in six against 46 for 64 x 64 in three;
+//    128 x 128 tiles for more than 64 rows and outputs (6724 x 2344 -> 64: 41 us, with
+//    64 x 64 in four 26) where they, split over K at 12 k-steps a block or more, come
+//    to 200 blocks (512 x 4096 -> 1152: 42 us in six against 46 for 64 x 64 in three;
 //    2048 x 1152 -> 1152: 45.6 us in three against 50.5; 1024 x 4096 -> 4096: 188 us
 //    in two against 200 whole and 236 for 64 x 64);
 //    32 x 64 tiles for one tile row or up to 128 of them (9 x 4096 -> 4096: 18.4 us
@@ -893,7 +894,8 @@ enum LinKind {
 //    split (2048 x 256 -> 256: 6.2 us against 7.2);
 //    64 x 64 tiles otherwise: with two groups of waves, split at 12 k-steps (300 x
 //    4096 -> 1152: 33 us in five against 36 in six; 64 x 1152 -> 4608: 14.0 us in
-//    three against 20 whole), or more than 512 of them with one group and a third
+//    three against 20 whole), where they are half the CUs at 40 (8192 x 1152 -> 128,
+//    256 tiles: 21.4 us whole against 25.6 in two), or more than 512 of them with one group and a third
 //    block per CU (4096 x 640 -> 640: 31.9 us against 33.6).
 struct LinPlan {
   LinKind kind;
@@ -933,7 +935,7 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
     const bool four = ksteps >= 32 && split(256, t32, 32, 4) == 1;
     p.kind = four ? LIN_T32X4 : LIN_T32;
     want = four ? 1 : split(256, t32, 16, 4);
-  } else if (M > 64 && t128 * split128 >= 200) {
+  } else if (M > 64 && N > 64 && t128 * split128 >= 200) {
     p.kind = LIN_T128;
     want = split128;
   } else if (M <= 32 || t32 <= 128 || (t32 <= 256 && ksteps < 24)) {
@@ -941,7 +943,7 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
     want = split(M <= 32 ? 256 : 512, t32, 12, 8);
   } else if (t <= 512) {
     p.kind = LIN_T64X2;
-    want = split(512, t, 12, 8);
+    want = split(512, t, t > 128 ? 40 : 12, 8);
   } else {
     p.kind = LIN_T64;
   }

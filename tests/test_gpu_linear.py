@@ -101,7 +101,7 @@ def test_few_rows(T, K, N, dt):
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
-@pytest.mark.parametrize("T,N", [(1100, 4040), (1100, 2312), (1000, 1160), (2050, 1160), (6001, 1000)])
+@pytest.mark.parametrize("T,N", [(6724, 64), (12300, 8), (1100, 4040), (1100, 2312), (1000, 1160), (2050, 1160), (6001, 1000)])
 @pytest.mark.parametrize("K", [8, 72, 328, 1544, 1608, 3208])
 def test_middling_tiles(T, N, K, dt):
     # tiles of 128 x 192, 128 x 128 and 64 x 128, whole and split, from one k-step to many, ragged on every side
