@@ -5,7 +5,7 @@
 //
 // Kernels, chosen by shape (linear_plan):
 //  linear_rows_kernel   M <= 4: one pass over W on the vector ALU.
-//  linear_few_kernel    16 x 16 tiles for up to 8 rows, or 64 with a short K.
+//  linear_few_kernel    16 x 16 tiles for products of few tiles.
 //  linear_tile_kernel   MFMA tiles of 32 x 64 to 128 x 192; few tiles share
 //                       their k-steps among groups of waves and are split over K
 //                       (partial sums in the workspace, added in split order by
@@ -738,15 +738,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 // ---- a few rows -----------------------------------------------------------------
 //
-// Tiles of 16 x 16 outputs for up to 8 rows, or more with a short K: the eight
-// waves of a block take the k-steps (128 bytes of a row) in turn, fragments go from
-// memory straight into registers, U k-steps in flight, no barrier until the waves'
-// sums meet in LDS, in wave order. Lane l holds bytes 32 (l / 16) .. + 31 of row
-// l % 16 (bf16: two chunks for two v_mfma_f32_16x16x32_bf16; fp32: the eight values
-// of one split), the same k for both operands. Rows past the end repeat the last
-// one and are not stored; chunks past K are zeros. Bound by reading W (8 x 4096 ->
-// 16384 bf16: 29.7 us, 4.5 TB/s) or by latency (16 x 256 -> 1152: 2.9 us); each block
-// reads all of its 16 rows of X, so more rows with a long K take wider tiles.
+// Tiles of 16 x 16 outputs for products of few tiles: the eight waves of a block
+// take the k-steps (128 bytes of a row) in turn, fragments go from memory straight
+// into registers, U k-steps in flight, no barrier until the waves' sums meet in LDS,
+// in wave order. Lane l holds bytes 32 (l / 16) .. + 31 of row l % 16 (bf16: two chunks
+// for two v_mfma_f32_16x16x32_bf16; fp32: the eight values of one split), the same k
+// for both operands. Rows past the end repeat the last one and are not stored; chunks
+// past K are zeros. Bound by latency (16 x 256 -> 1152 bf16: 2.9 us) or by what each
+// block reads, its 16 rows of X and of W: many tiles with a long K take wider ones.
 template <typename TE>
 __global__ __launch_bounds__(512) void linear_few_kernel(const TE* __restrict__ X, int64_t M,
                                                          const TE* __restrict__ W, int64_t N, int K,
@@ -846,11 +845,14 @@ enum LinKind {
 // Kernel and split count of a product.
 //  up to 4 rows: the vector kernel (4096 -> 16384 bf16: 25 us at one row, 30 at four;
 //    at eight it would take 43).
-//  16 x 16 tiles up to 64 rows where K is short (16 x 256 -> 1152 bf16: 2.9 us against
-//    3.6, fp32 3.5 against 5.6; at 128 rows 3.8 against 3.7), and for 3 (fp32: 5) to 8
-//    rows of many outputs (4 x 4096 -> 16384 bf16: 26.1 us against 30.1 for the vector
-//    kernel; 8 rows: 29.7 against 30.1 for 32 x 64 tiles, 16 rows the other way, 34.0
-//    against 30.4; 8 x 4608 -> 1152 fp32 the other way too, 16.3 against 13.7).
+//  16 x 16 tiles, waves sharing the k-steps, up to one tile per CU and 48 k-steps (16 x
+//    1152 -> 1152 bf16: 4.4 us against 5.6 for 32 x 64 tiles, fp32 6.7 against 9.2;
+//    912 x 576 -> 24 fp32: 4.7 against 8.6; at 72 k-steps 10.6 against 8.9), up to two
+//    per CU and 24 k-steps in fp32 (64 x 768 -> 1152: 8.2 us against 9.3, at 36 the other
+//    way, 10.8 against 9.9) or 4 in bf16 (8 x 1152 -> 4608 still 5.8 against 6.0 at 18,
+//    as half the rows are not there; 64 x 768 -> 1152 the other way, 5.0 against 4.8),
+//    and for 3 or 4 bf16 rows of many outputs (4 x 4096 -> 16384: 26.1 us against 30.1
+//    for the vector kernel).
 //  bf16:
 //    More than 128 tiles of 256 x 192: the wide tiles, 192 or 256 columns, whichever's
 //    rounds of one tile per CU cost less; except that 128 x 128 tiles of eight waves,
@@ -904,12 +906,17 @@ struct LinPlan {
 LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   LinPlan p = {LIN_ROWS, 1, (K * esize + 127) / 128};
   const bool bf16 = esize == 2;
-  if ((p.kper <= 8 && M > 2 && M <= 64) || (N >= 4096 && M > (bf16 ? 2 : 4) && M <= 8)) {
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  const int64_t t16 = tiles(16, 16);
+  const int least = M <= 4 ? 8 : M <= 8 ? 64 : 48;   // k-steps of a tile that has a CU
+  const bool few = (t16 <= 256 && p.kper <= least) ||
+                   (t16 <= 512 && p.kper <= (!bf16 ? 24 : M <= 4 ? 8 : M <= 8 ? 18 : 4)) ||
+                   (M <= 4 && N >= 4096);
+  if (few && M > (bf16 ? 2 : 4)) {
     p.kind = LIN_FEW;
     return p;
   }
   if (M <= 4) return p;
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   const int64_t t = tiles(64, 64), t32 = tiles(32, 64), t128 = tiles(128, 128);
   const int ksteps = p.kper;
   if (bf16 && t128 > 256 && t128 <= 512 && ksteps <= 32) {

@@ -93,7 +93,8 @@ def test_shared_k_steps(T, N, K, dt):
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
-@pytest.mark.parametrize("T,K,N", [(3, 8, 8), (17, 72, 40), (64, 256, 1160), (5, 4096, 4104), (8, 5128, 4096), (7, 264, 4104)])
+@pytest.mark.parametrize("T,K,N", [(3, 8, 8), (17, 72, 40), (64, 256, 1160), (5, 4096, 4104), (8, 5128, 4096), (7, 264, 4104),
+                                   (4000, 520, 8), (900, 1544, 24), (60, 776, 1160), (250, 3080, 256)])
 def test_few_rows(T, K, N, dt):
     # k-steps shared by the waves of a block: fewer than waves, several rounds, chunks past the end of K
     run(T, K, N, dt, act="gelu", residual=True, gate_rows=2)
