@@ -839,7 +839,8 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 namespace {
 
 enum LinKind {
-  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128, LIN_T128, LIN_T128X2, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128,
+  LIN_T128, LIN_T128X2, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
 };
 
 // Kernel and split count of a product.
@@ -908,8 +909,8 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   const bool bf16 = esize == 2;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   const int64_t t16 = tiles(16, 16);
-  const int least = M <= 4 ? 8 : M <= 8 ? 64 : 48;   // k-steps of a tile that has a CU
-  const bool few = (t16 <= 256 && p.kper <= least) ||
+  const int most = M <= 4 ? 8 : M <= 8 ? 64 : 48;   // k-steps, where every tile has a CU
+  const bool few = (t16 <= 256 && p.kper <= most) ||
                    (t16 <= 512 && p.kper <= (!bf16 ? 24 : M <= 4 ? 8 : M <= 8 ? 18 : 4)) ||
                    (M <= 4 && N >= 4096);
   if (few && M > (bf16 ? 2 : 4)) {

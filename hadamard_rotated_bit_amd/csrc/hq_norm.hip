@@ -715,7 +715,8 @@ hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
     const int64_t n = S - s0 < most ? S - s0 : most, off = s0 * a.P * a.C;
     k.x = static_cast<const char*>(a.x) + off * (a.x_bf16 ? 2 : 4);
     k.y = static_cast<char*>(a.y) + off * (a.y_bf16 ? 2 : 4);
-    const hipError_t e = a.x_bf16 ? launch_norm_typed<uint16_t>(p, k, n, s) : launch_norm_typed<float>(p, k, n, s);
+    const hipError_t e = a.x_bf16 ? launch_norm_typed<uint16_t>(p, k, n, s)
+                                  : launch_norm_typed<float>(p, k, n, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
