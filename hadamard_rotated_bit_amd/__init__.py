@@ -23,7 +23,8 @@ from . import _lib
 from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU,
                    HQ_CENTER_CHANNEL, HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CODES_E2M3,
                    HQ_CODES_I8, HQ_GEMM_AUTO, HQ_GEMM_I8, HQ_INT_ACT_GELU, HQ_INT_ACT_NONE,
-                   HQ_INT_ACT_RELU, HQ_INT_ACT_SILU, HQ_INT_DH, HQ_INT_WH, HqDesc, HqError,
+                   HQ_INT_ACT_RELU, HQ_INT_ACT_SILU, HQ_INT_DH, HQ_INT_WH, HQ_NORM_BLOCK,
+                   HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED, HQ_NORM_ROWS, HqDesc, HqError,
                    HqLayout, check, load)
 
 F32, BF16 = 0, 1
@@ -561,6 +562,13 @@ def group_norm_workspace_bytes(desc: NormDesc, samples: int, positions: int) -> 
         if samples < 0 or positions < 0:
             raise HqError(_lib.HQ_ERR_INVALID_ARG, "samples and positions must be >= 0")
     return n
+
+
+def group_norm_plan(desc: NormDesc, samples: int, positions: int) -> _lib.HqNormPlan:
+    """How group_norm runs a call of this size (hq_group_norm_plan)."""
+    out = _lib.HqNormPlan()
+    check(load().hq_group_norm_plan(desc._ref, samples, positions, ctypes.byref(out)))
+    return out
 
 
 def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = None,

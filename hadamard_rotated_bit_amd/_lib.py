@@ -50,7 +50,12 @@ class HqNormDesc(ctypes.Structure):
                 ["channels", "groups", "act", "x_dtype", "y_dtype"]] + [("eps", ctypes.c_float)]
 
 
+class HqNormPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("slices", ctypes.c_int32), ("grid", ctypes.c_int64)]
+
+
 HQ_CODES_I8, HQ_CODES_E2M3 = 0, 1
+HQ_NORM_ROWS, HQ_NORM_BLOCK, HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED = 0, 1, 2, 3
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_I8 = 0, 1
 HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CENTER_CHANNEL = 0, 1, 2
@@ -89,6 +94,7 @@ _SIGS = {
     "hq_linear": (ctypes.c_int, [_L, _P, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
     "hq_norm_validate": (ctypes.c_int, [_N]),
     "hq_group_norm_workspace_bytes": (ctypes.c_size_t, [_N, _I64, _I64]),
+    "hq_group_norm_plan": (ctypes.c_int, [_N, _I64, _I64, ctypes.POINTER(HqNormPlan)]),
     "hq_group_norm": (ctypes.c_int, [_N, _P, _P, _P, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
     "hq_channel_center": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     "hq_act_quantize": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P]),

@@ -993,6 +993,25 @@ size_t hq_group_norm_workspace_bytes(const hq_norm_desc* desc, int64_t samples,
                                       int(dtype_size(desc->x_dtype))));
 }
 
+int hq_group_norm_plan(const hq_norm_desc* desc, int64_t samples, int64_t positions,
+                       hq_norm_plan* out) {
+  g_err.clear();
+  int st = check_norm_desc(desc);
+  if (st == HQ_OK) st = check_positions(samples, positions);
+  if (st != HQ_OK) return st;
+  if (!out) return fail(HQ_ERR_INVALID_ARG, "out is NULL");
+  static_assert(int(HQ_NORM_ROWS) == hq::NORM_ROWS && int(HQ_NORM_BLOCK) == hq::NORM_BLOCK &&
+                    int(HQ_NORM_CHUNKS) == hq::NORM_CHUNKS &&
+                    int(HQ_NORM_CHUNKS_JOINED) == hq::NORM_CHUNKS_JOINED,
+                "the same values");
+  const hq::NormPlanInfo p = hq::norm_plan_info(samples, positions, desc->channels, desc->groups,
+                                                int(dtype_size(desc->x_dtype)));
+  out->kernel = p.kernel;
+  out->slices = p.slices;
+  out->grid = p.grid;
+  return HQ_OK;
+}
+
 int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, const float* beta,
                   int64_t samples, int64_t positions, void* Y, void* workspace,
                   size_t workspace_bytes, void* stream) {

@@ -173,6 +173,14 @@ struct NormArgs {
   void* part;
 };
 size_t norm_part_bytes(int64_t S, int64_t P, int C, int G, int esize);
+// How a call runs: the form (the C ABI's hq_norm_kernel), the launches that its
+// samples are cut into, and the threads of its largest one.
+enum { NORM_ROWS, NORM_BLOCK, NORM_CHUNKS, NORM_CHUNKS_JOINED };
+struct NormPlanInfo {
+  int kernel, slices;
+  int64_t grid;
+};
+NormPlanInfo norm_plan_info(int64_t S, int64_t P, int C, int G, int esize);
 hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s);
 
 // Integer-only DH / WH layers with integer requantisation.

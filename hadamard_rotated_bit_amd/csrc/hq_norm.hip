@@ -30,6 +30,8 @@
 #include "hq_epilogue.h"
 #include "hq_internal.h"
 
+#include <algorithm>
+
 namespace hq {
 
 struct NormKArgs {
@@ -559,6 +561,8 @@ struct NormPlan {
   int subs;          // parts of a chunk in the second pass and their rows,
   int64_t rps;
   int join;          // 1: norm_join_kernel between the passes
+  int64_t slice;     // samples per launch
+  int64_t grid;      // threads of the call's largest launch
 };
 
 int gcd_i(int a, int b) { return b ? gcd_i(b, a % b) : a; }
@@ -575,7 +579,7 @@ int gcd_i(int a, int b) { return b ? gcd_i(b, a % b) : a; }
 // blocks, the other way, 9.2 against 10.0), take the chunked form, which spreads a
 // sample over every CU, at 4 rows per lane or more (1 x 4096 x 320 bf16: 11.7 us
 // against 13.1 with 8, 1 x 65536 x 16 fp32: 11.0 against 13.3).
-NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
+NormPlan norm_form(int64_t S, int64_t P, int C, int G, int esize) {
   NormPlan p = {};
   if (P == 1 && C / G % 8 == 0) {
     p.block = p.rows = 1;
@@ -615,6 +619,43 @@ NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
   return p;
 }
 
+// norm_rows_kernel: lanes per row of w channels, pieces of 8 channels per lane (one
+// up to 512 channels, at most 8: C <= NORM_MAX_C), and blocks, no more than the CUs
+// hold at once.
+int norm_rows_lanes(int w) {
+  int L = 1;
+  while (L < 64 && L * 8 < w) L <<= 1;
+  return L;
+}
+int norm_rows_pieces(int C, int G) {
+  const int r = (C / G + 511) / 512;
+  if (r == 1) return 1;
+  return G > 1 ? 4 : r <= 4 ? r : 8;
+}
+int64_t norm_rows_blocks(int64_t rows, int L, int R) {
+  return std::min<int64_t>((rows * L + 255) / 256, R == 1 ? 2048 : 1280);
+}
+
+// The form, and how many samples one launch takes: a grid holds less than 2^32
+// threads (kept to half of that here), and a sample may be hundreds of blocks. Slices
+// are whole eights where they can be (norm_block_kernel's order of slabs).
+NormPlan norm_plan(int64_t S, int64_t P, int C, int G, int esize) {
+  NormPlan p = norm_form(S, P, C, G, esize);
+  p.slice = S;
+  if (p.rows) {
+    const int R = norm_rows_pieces(C, G);
+    p.grid = 256 * norm_rows_blocks(S * G, norm_rows_lanes(C / G), R);
+    return p;
+  }
+  // blocks per sample of the first and the second pass (join: 256 threads for a group)
+  const int64_t blocks = p.block ? (C + p.slab - 1) / p.slab : int64_t(p.chunks) * p.subs;
+  const int64_t threads = std::max<int64_t>(blocks * p.nt, p.join ? int64_t(G) * 256 : 0);
+  const int64_t most = (int64_t(1) << 31) / threads;
+  if (S > most) p.slice = most >= 8 ? most & ~int64_t(7) : most;
+  p.grid = p.slice * threads;
+  return p;
+}
+
 template <typename TE, int U>
 void launch_norm_first(const NormPlan& p, const NormKArgs& k, dim3 grid, hipStream_t s) {
   if (!p.block && p.nt == 256)
@@ -632,11 +673,8 @@ void launch_norm_first(const NormPlan& p, const NormKArgs& k, dim3 grid, hipStre
 template <typename TE, int R, bool HOLD>
 hipError_t launch_norm_rows(const NormKArgs& k, int64_t S, hipStream_t s) {
   const int64_t rows = S * k.G;
-  int L = 1;
-  while (L < 64 && L * 8 < k.C / k.G) L <<= 1;
-  int64_t blocks = (rows * L + 255) / 256;
-  const int64_t most = R == 1 ? 2048 : 1280;   // what the CUs hold at once
-  if (blocks > most) blocks = most;
+  const int L = norm_rows_lanes(k.C / k.G);
+  const int64_t blocks = norm_rows_blocks(rows, L, R);
   hipLaunchKernelGGL((norm_rows_kernel<TE, R, HOLD>), dim3(unsigned(blocks)), dim3(256), 0, s, k, rows,
                      L);
   return hipGetLastError();
@@ -645,7 +683,7 @@ hipError_t launch_norm_rows(const NormKArgs& k, int64_t S, hipStream_t s) {
 template <typename TE>
 hipError_t launch_norm_typed(const NormPlan& p, const NormKArgs& k, int64_t S, hipStream_t s) {
   if (p.rows) {
-    const int r = (k.C / k.G + 511) / 512;   // at most 8: C <= NORM_MAX_C
+    const int r = norm_rows_pieces(k.C, k.G);
     if (k.G > 1)
       return r == 1 ? launch_norm_rows<TE, 1, false>(k, S, s) : launch_norm_rows<TE, 4, false>(k, S, s);
     switch (r) {
@@ -693,6 +731,16 @@ size_t norm_part_bytes(int64_t S, int64_t P, int C, int G, int esize) {
   return p.block ? 0 : sizeof(float2) * size_t(S) * size_t(G) * size_t(p.chunks + p.join);
 }
 
+NormPlanInfo norm_plan_info(int64_t S, int64_t P, int C, int G, int esize) {
+  NormPlanInfo i = {};
+  if (S <= 0 || P <= 0) return i;
+  const NormPlan p = norm_plan(S, P, C, G, esize);
+  i.kernel = p.rows ? NORM_ROWS : p.block ? NORM_BLOCK : p.join ? NORM_CHUNKS_JOINED : NORM_CHUNKS;
+  i.slices = int((S + p.slice - 1) / p.slice);
+  i.grid = p.grid;
+  return i;
+}
+
 hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
   const NormPlan p = norm_plan(S, a.P, a.C, a.G, a.x_bf16 ? 2 : 4);
   NormKArgs k = {};
@@ -708,11 +756,8 @@ hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s) {
   k.chunks = p.chunks;
   k.rpc = p.rpc;
   k.slab = p.slab;
-  // slices of samples: a grid holds less than 2^32 threads (norm_rows_kernel
-  // loops over its rows)
-  const int64_t most = p.rows ? S : int64_t(1) << 20;
-  for (int64_t s0 = 0; s0 < S; s0 += most) {
-    const int64_t n = S - s0 < most ? S - s0 : most, off = s0 * a.P * a.C;
+  for (int64_t s0 = 0; s0 < S; s0 += p.slice) {
+    const int64_t n = std::min(S - s0, p.slice), off = s0 * a.P * a.C;
     k.x = static_cast<const char*>(a.x) + off * (a.x_bf16 ? 2 : 4);
     k.y = static_cast<char*>(a.y) + off * (a.y_bf16 ? 2 : 4);
     const hipError_t e = a.x_bf16 ? launch_norm_typed<uint16_t>(p, k, n, s)

@@ -380,6 +380,25 @@ int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, c
                   int64_t samples, int64_t positions, void* Y, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/* Which kernels a hq_group_norm call runs. */
+typedef enum {
+  HQ_NORM_ROWS = 0,          /* one position, groups of whole 8-channel pieces      */
+  HQ_NORM_BLOCK = 1,         /* one launch, a sample's slab of groups per block     */
+  HQ_NORM_CHUNKS = 2,        /* statistics of chunks of positions, then the output  */
+  HQ_NORM_CHUNKS_JOINED = 3  /* the same, the chunks joined by a launch between     */
+} hq_norm_kernel;
+typedef struct {
+  int32_t kernel;  /* hq_norm_kernel                                            */
+  int32_t slices;  /* launches of each kernel: more samples than a grid of 2^31
+                      threads holds take several                                */
+  int64_t grid;    /* threads of the largest launch                             */
+} hq_norm_plan;
+
+/* Bookkeeping, host-only (for testing and profiling): how hq_group_norm runs a
+ * call of this size; all zero for a call that does nothing. */
+int hq_group_norm_plan(const hq_norm_desc* desc, int64_t samples, int64_t positions,
+                       hq_norm_plan* out);
+
 /* ---- Stage entry points (the same kernels, for testing and profiling) ---- */
 
 /* Per-channel centring statistics (center = 2 only; T >= 1), the per-channel
