@@ -10,10 +10,13 @@
 // Statistics never subtract large sums. A lane owns 8 consecutive channels
 // (one 16- or 32-byte load per row) and takes, per unit of channels that share
 // a group, the mean of the rows in its registers and then the squares about
-// that mean; batches, lanes and chunks are joined in a fixed tree by
+// that mean; batches and lanes are joined in a fixed tree by
 //   mean = m_a + d n_b / n,   M2 = M2_a + M2_b + d^2 n_a n_b / n,   d = m_b - m_a,
-// and the units of a group by mean_g = avg m_u, M2_g = sum M2_u + n (m_u -
-// mean_g)^2. Everything is fp32; groups may have any width.
+// and the units of a group, and its chunks, by mean_g = avg m_u, M2_g = sum M2_u +
+// n (m_u - mean_g)^2. An average rounds, by several units in sums of many values, so
+// each one, m', is followed by the sum s1 of the n differences from it beside that of
+// their squares: mean = m' + s1 / n, M2 = s2 - s1^2 / n. A group of equal values then
+// has exactly their value as its mean. Everything is fp32; groups may have any width.
 //
 // Forms (norm_plan):
 //  norm_rows_kernel    one position, groups of whole 8-channel pieces: a wave or
@@ -72,13 +75,19 @@ __device__ __forceinline__ void stat_merge(Stat<NS>& a, float nb, const float (&
   a.n = nt;
 }
 
+// s2 - c, the sum of squares about a rounded mean less its correction c = s1^2 / n
+// (no larger than s2 but for roundings). An s2 past the largest float stays infinite.
+__device__ __forceinline__ float about_mean(float s2, float c) {
+  return c < s2 ? s2 - c : s2 < INFINITY ? 0.0f : s2;   // NaN stays
+}
+
 // The statistics of the first `n` of the R rows in `x` (each lane its own n),
 // merged into `a`.
 template <typename TE, int U, int R>
 __device__ __forceinline__ void stat_rows(Stat<8 / U>& a, Raw8<TE> (&x)[R], int n) {
   constexpr int NS = 8 / U;
   if (n <= 0) return;
-  float m[NS] = {}, q[NS] = {};
+  float m[NS] = {}, s[NS] = {}, q[NS] = {};
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (i < n) {
@@ -106,9 +115,16 @@ __device__ __forceinline__ void stat_rows(Stat<8 / U>& a, Raw8<TE> (&x)[R], int 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = v[e] - m[e / U];
+        s[e / U] += d;
         q[e / U] = fmaf(d, d, q[e / U]);
       }
     }
+  }
+#pragma unroll
+  for (int e = 0; e < NS; ++e) {
+    const float c = s[e] * inv;
+    m[e] += c;
+    q[e] = about_mean(q[e], c * s[e]);
   }
   stat_merge<NS>(a, nv, m, q);
 }
@@ -189,13 +205,15 @@ __device__ __forceinline__ void group_stats(const float* cm, const float* cq, in
     float s = 0.0f;
     for (int c = l; c < cu; c += lg) s += cm[g * cu + c];
     const float mean = lanes_sum(s, lg) * inv;
-    float q = 0.0f;
+    float s1 = 0.0f, q = 0.0f;
     for (int c = l; c < cu; c += lg) {
       const float d = cm[g * cu + c] - mean;
+      s1 += d;
       q += fmaf(n * d, d, cq[g * cu + c]);
     }
+    s1 = lanes_sum(s1, lg);
     q = lanes_sum(q, lg);
-    if (l == 0) out(g, mean, q);
+    if (l == 0) out(g, fmaf(s1, inv, mean), about_mean(q, n * (s1 * inv) * s1));
   }
 }
 
@@ -438,10 +456,17 @@ __device__ __forceinline__ float chunk_rows(const NormKArgs& k, int c) {
   return float(left < k.rpc ? left : k.rpc);
 }
 
+// (mean, M2) of a group's chunks from their average, the rows' sum s1 of differences
+// from it and the squares s2 about it over all the group's channels.
+__device__ __forceinline__ float2 joined(const NormKArgs& k, float mean, float s1, float s2) {
+  const float c = s1 / float(k.P);
+  return make_float2(mean + c, about_mean(s2, float(k.C / k.G) * c * s1));
+}
+
 // The chunks (up to 1024) of each (sample, group) joined into one: a block
 // each, the partial results in registers, mean first, then the squares about it.
 __global__ __launch_bounds__(256) void norm_join_kernel(NormKArgs k, float2* __restrict__ out) {
-  __shared__ float red[2][4];
+  __shared__ float red[3][4];
   const float2* p = k.part + int64_t(blockIdx.x) * k.chunks;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   float2 v[4];
@@ -460,17 +485,23 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormKArgs k, float2* __r
   __syncthreads();
   const float mean = ((red[0][0] + red[0][1]) + (red[0][2] + red[0][3])) / float(k.P);
   const float cg = float(k.C / k.G);
-  float q = 0.0f;
+  float s1 = 0.0f, q = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float d = v[i].x - mean;
+    s1 += w[i] > 0.0f ? d * w[i] : 0.0f;
     q += w[i] > 0.0f ? fmaf(d * d, w[i] * cg, v[i].y) : 0.0f;
   }
+  s1 = group_sum<64>(s1);
   q = group_sum<64>(q);
-  if (lane == 0) red[1][wave] = q;
+  if (lane == 0) {
+    red[1][wave] = s1;
+    red[2][wave] = q;
+  }
   __syncthreads();
   if (threadIdx.x == 0)
-    out[blockIdx.x] = make_float2(mean, (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]));
+    out[blockIdx.x] = joined(k, mean, (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]),
+                             (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]));
 }
 
 // Normalises rows of sample s. Chunk c of the first pass is cut into `subs`
@@ -523,10 +554,11 @@ __global__ __launch_bounds__(NT) void norm_apply_kernel(NormKArgs k, const float
       const float w = l < join_n ? chunk_rows(k, l) : 0.0f;
       const float mean = lanes_sum(r.x * w, lq) / float(k.P);
       const float d = r.x - mean;
-      const float q = lanes_sum(w > 0.0f ? fmaf(d * d, w * float(cg), r.y) : 0.0f, lq);
+      const float s1 = lanes_sum(w > 0.0f ? d * w : 0.0f, lq);
+      const float2 j = joined(k, mean, s1, lanes_sum(w > 0.0f ? fmaf(d * d, w * float(cg), r.y) : 0.0f, lq));
       if (l == 0) {
-        gm[g] = mean;
-        gr[g] = rstd_of(q, k);
+        gm[g] = j.x;
+        gr[g] = rstd_of(j.y, k);
       }
     }
   }
