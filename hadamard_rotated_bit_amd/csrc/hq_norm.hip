@@ -70,7 +70,7 @@ __device__ __forceinline__ void stat_merge(Stat<NS>& a, float nb, const float (&
   for (int e = 0; e < NS; ++e) {
     const float d = mb[e] - a.mean[e];
     a.mean[e] = fmaf(d, r, a.mean[e]);
-    a.m2[e] += fmaf(d * d, w, m2b[e]);
+    a.m2[e] += fmaf(d * w, d, m2b[e]);   // in this order 0 where w is, also for a d^2 past the floats
   }
   a.n = nt;
 }

@@ -375,7 +375,9 @@ size_t hq_group_norm_workspace_bytes(const hq_norm_desc* desc, int64_t samples,
  *  are the same. workspace at least hq_group_norm_workspace_bytes bytes (NULL
  *  when that is 0), not shared with a concurrent call. samples x positions up
  *  to 2^26; 0 of either is a no-op. A sample's NaN or infinity stays in its
- *  own sample and group. The same inputs always give the same bits. */
+ *  own sample and group. A variance past the largest float (values some 1e19
+ *  apart) is infinite: finite values of such a group give phi(beta). The same
+ *  inputs always give the same bits. */
 int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, const float* beta,
                   int64_t samples, int64_t positions, void* Y, void* workspace,
                   size_t workspace_bytes, void* stream);

@@ -54,3 +54,21 @@ def test_means_far_from_zero(S, P, C, G):
     Y = hq.group_norm(hq.NormDesc(C, G), X)
     assert_within(Y.view(-1, C), z.reshape(-1, C), tol.expand_as(x).reshape(-1, C) + U32 * z.abs().reshape(-1, C) + 1e-30,
                   f"S={S} P={P} C={C} G={G}")
+
+
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("C,G", [(64, 8), (512, 1), (1152, 1), (320, 32), (4096, 2)])
+@pytest.mark.parametrize("P", [1, 2, 300, 6001])
+def test_squares_past_the_largest_float(P, C, G, dt):
+    # a group whose variance is no float has an infinite one: phi(beta), not a value the
+    # size of the input; the other groups and samples keep theirs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(P + C)
+    X = torch.randn(3, P, C, generator=g, device="cuda").to(DT[dt])
+    beta = torch.linspace(-1, 1, C, device="cuda")
+    desc = hq.NormDesc(C, G, x_dtype=dt, y_dtype=dt)
+    want = hq.group_norm(desc, X, None, beta)
+    w = C // G
+    X[1, :, :w] = (torch.randn(P, w, generator=g, device="cuda") * 1e30).to(DT[dt])
+    want[1, :, :w] = beta[:w].to(DT[dt])
+    assert torch.equal(hq.group_norm(desc, X, None, beta), want)
