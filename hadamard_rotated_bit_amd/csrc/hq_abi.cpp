@@ -793,6 +793,10 @@ int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X
   st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &lin);
   if (st != HQ_OK) return st;
   const size_t need = workspace_of(desc, T).total;
+  hq_prepared_layout L;
+  layout_of(desc, &L);
+  if (overlap(prepared, L.total, Y, ny) || overlap(prepared, L.total, workspace, need))
+    return fail(HQ_ERR_INVALID_ARG, "Y or the workspace overlaps prepared");
   if (overlap(workspace, need, X, nx) || overlap(workspace, need, Y, ny) ||
       overlap(workspace, need, lin.residual, ny) ||
       overlap(workspace, need, lin.gate, gate_bytes(lin, T, desc->d_out, es)))

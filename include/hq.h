@@ -307,8 +307,8 @@ typedef struct {
  * with its bias, then Y = residual + gate phi(V) in the GEMM's epilogue (no
  * second pass over Y). Arguments, workspace (hq_workspace_bytes) and errors as
  * hq_quant_linear; epilogue NULL, or with everything absent, is that call
- * exactly. T up to 2^26; Y must not overlap X or the gate, nor the workspace
- * any of them or the residual. */
+ * exactly. T up to 2^26; Y must not overlap X, prepared or the gate, nor the
+ * workspace any of them or the residual. */
 int hq_quant_linear_epi(const hq_desc* desc, const void* prepared, const void* X, int64_t T,
                         const hq_epilogue* epilogue, void* Y, void* workspace,
                         size_t workspace_bytes, void* stream);

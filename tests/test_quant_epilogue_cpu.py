@@ -37,3 +37,14 @@ def test_refusals(kw, status, word):
 
 def test_empty_call_is_a_no_op():
     assert call(T=0, X=None, Y=None, prep=None, ws=None, n=0) == 0
+
+
+BLOB = lib.hq_prepared_bytes(Desc(1152, 4608, 128, 4, 4, 1, False, 0, BF16, BF16, BF16)._ref)
+
+
+@pytest.mark.parametrize("kw", [dict(prep=0x40000000), dict(prep=0x40000000 - BLOB + 256), dict(prep=0x40000000 + 16 * 4608 * 2 - 256),
+                                dict(prep=0x80000000), dict(prep=0x80000000 - BLOB + 256), dict(ws=0x1000 + BLOB - 256)])
+def test_written_buffers_must_not_overlap_the_weights(kw):
+    # Y at 0x40000000, the workspace at 0x80000000, the blob at 0x1000 where not given
+    assert call(**kw) == -1
+    assert b"overlaps prepared" in lib.hq_last_error()
