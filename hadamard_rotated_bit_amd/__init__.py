@@ -460,6 +460,21 @@ class Epilogue:
         return ctypes.byref(_lib.HqEpilogue(self.act, _addr(r), _addr(g), self.gate_rows, ld))
 
 
+def _need_prepared(desc: Desc, prepared: torch.Tensor, device: int) -> None:
+    """``prepared`` is a blob of ``desc``'s size on GPU ``device`` (what it holds:
+    check_prepared)."""
+    if not isinstance(prepared, torch.Tensor) or not prepared.is_contiguous():
+        raise ValueError("prepared must be a contiguous tensor")
+    if prepared.get_device() != device:
+        raise ValueError(f"prepared is on {prepared.device}, X on cuda:{device}")
+    need = getattr(desc, "_blob_bytes", None)   # the descriptor's own: asked for once
+    if need is None:
+        need = prepared_bytes(desc)
+        object.__setattr__(desc, "_blob_bytes", need)
+    if prepared.nbytes < need:
+        raise ValueError(f"prepared has {prepared.nbytes} bytes, {need} needed")
+
+
 def _quant_linear_epi(desc, prepared, X, out, workspace, epilogue):
     T = X.shape[0]
     device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
@@ -471,8 +486,7 @@ def _quant_linear_epi(desc, prepared, X, out, workspace, epilogue):
         out = torch.empty(T, desc.d_out, dtype=ydt, device=X.device)
     else:
         _fits(out, "out", ydt, (T, desc.d_out), device)
-    if prepared.get_device() != device:
-        raise ValueError(f"prepared is on {prepared.device}, X on cuda:{device}")
+    _need_prepared(desc, prepared, device)
     ep = epilogue._c(T, desc.d_out, ydt, device)
     lib = load()
     ws, ws_addr, ws_bytes = _workspace_of(workspace, lib.hq_workspace_bytes(desc._ref, T), X, device)

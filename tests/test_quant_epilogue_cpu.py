@@ -48,3 +48,17 @@ def test_written_buffers_must_not_overlap_the_weights(kw):
     # Y at 0x40000000, the workspace at 0x80000000, the blob at 0x1000 where not given
     assert call(**kw) == -1
     assert b"overlaps prepared" in lib.hq_last_error()
+
+
+def test_python_checks_the_weights():
+    import torch
+
+    import hadamard_rotated_bit_amd as hq
+    d = Desc(1152, 4608, 128, 4, 4, 1, False, 0, BF16, BF16, BF16)
+    blob = torch.zeros(BLOB, dtype=torch.uint8)
+    hq._need_prepared(d, blob, -1)
+    for bad, word in ((blob[:-1], "needed"), (torch.zeros(2 * BLOB, dtype=torch.uint8)[::2], "contiguous"), (None, "tensor")):
+        with pytest.raises(ValueError, match=word):
+            hq._need_prepared(d, bad, -1)
+    with pytest.raises(ValueError, match="prepared is on"):
+        hq._need_prepared(d, blob, 0)
