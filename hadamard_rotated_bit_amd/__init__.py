@@ -23,8 +23,12 @@ from . import _lib
 from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU,
                    HQ_CENTER_CHANNEL, HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CODES_E2M3,
                    HQ_CODES_I8, HQ_GEMM_AUTO, HQ_GEMM_I8, HQ_INT_ACT_GELU, HQ_INT_ACT_NONE,
-                   HQ_INT_ACT_RELU, HQ_INT_ACT_SILU, HQ_INT_DH, HQ_INT_WH, HQ_NORM_BLOCK,
-                   HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED, HQ_NORM_ROWS, HqDesc, HqError,
+                   HQ_INT_ACT_RELU, HQ_INT_ACT_SILU, HQ_INT_DH, HQ_INT_WH,
+                   HQ_LINEAR_256X192, HQ_LINEAR_256X256, HQ_LINEAR_FEW, HQ_LINEAR_ROWS,
+                   HQ_LINEAR_T32, HQ_LINEAR_T32X4, HQ_LINEAR_T64, HQ_LINEAR_T64X2,
+                   HQ_LINEAR_T64X128, HQ_LINEAR_T128, HQ_LINEAR_T128W8, HQ_LINEAR_T128X2,
+                   HQ_LINEAR_T128X192, HQ_NORM_BLOCK, HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED,
+                   HQ_NORM_ROWS, HqDesc, HqError,
                    HqLayout, check, load)
 
 F32, BF16 = 0, 1
@@ -518,6 +522,13 @@ def linear_workspace_bytes(desc: LinearDesc, T: int) -> int:
         if T < 0:
             raise HqError(_lib.HQ_ERR_INVALID_ARG, "T must be >= 0")
     return n
+
+
+def linear_plan(desc: LinearDesc, T: int) -> _lib.HqLinearPlan:
+    """How linear runs T rows (hq_linear_plan_of)."""
+    out = _lib.HqLinearPlan()
+    check(load().hq_linear_plan_of(desc._ref, T, ctypes.byref(out)))
+    return out
 
 
 def linear(desc: LinearDesc, X: torch.Tensor, weight: torch.Tensor,

@@ -50,11 +50,18 @@ class HqNormDesc(ctypes.Structure):
                 ["channels", "groups", "act", "x_dtype", "y_dtype"]] + [("eps", ctypes.c_float)]
 
 
+class HqLinearPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("splits", ctypes.c_int32)]
+
+
 class HqNormPlan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("slices", ctypes.c_int32), ("grid", ctypes.c_int64)]
 
 
 HQ_CODES_I8, HQ_CODES_E2M3 = 0, 1
+HQ_LINEAR_ROWS, HQ_LINEAR_FEW, HQ_LINEAR_T32, HQ_LINEAR_T32X4, \
+    HQ_LINEAR_T64X2, HQ_LINEAR_T64, HQ_LINEAR_T64X128, HQ_LINEAR_T128, \
+    HQ_LINEAR_T128X2, HQ_LINEAR_T128W8, HQ_LINEAR_T128X192, HQ_LINEAR_256X192, HQ_LINEAR_256X256 = range(13)
 HQ_NORM_ROWS, HQ_NORM_BLOCK, HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED = 0, 1, 2, 3
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_I8 = 0, 1
@@ -91,6 +98,7 @@ _SIGS = {
     "hq_quant_linear_epi": (ctypes.c_int, [_D, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
     "hq_linear_validate": (ctypes.c_int, [_L]),
     "hq_linear_workspace_bytes": (ctypes.c_size_t, [_L, _I64]),
+    "hq_linear_plan_of": (ctypes.c_int, [_L, _I64, ctypes.POINTER(HqLinearPlan)]),
     "hq_linear": (ctypes.c_int, [_L, _P, _P, _P, _I64, _E, _P, _P, ctypes.c_size_t, _P]),
     "hq_norm_validate": (ctypes.c_int, [_N]),
     "hq_group_norm_workspace_bytes": (ctypes.c_size_t, [_N, _I64, _I64]),

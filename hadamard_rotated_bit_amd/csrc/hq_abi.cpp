@@ -946,6 +946,24 @@ size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T) {
   return align256(hq::linear_part_bytes(T, desc->d_out, desc->d_in, int(dtype_size(desc->x_dtype))));
 }
 
+int hq_linear_plan_of(const hq_linear_desc* desc, int64_t T, hq_linear_plan* out) {
+  g_err.clear();
+  int st = check_linear_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
+  if (st != HQ_OK) return st;
+  if (!out) return fail(HQ_ERR_INVALID_ARG, "out is NULL");
+  static_assert(int(HQ_LINEAR_ROWS) == hq::LIN_ROWS && int(HQ_LINEAR_T64) == hq::LIN_T64 &&
+                    int(HQ_LINEAR_256X256) == hq::LIN_PP4,
+                "the same values");
+  out->kernel = out->splits = 0;
+  if (T == 0) return HQ_OK;
+  const hq::LinPlan p =
+      hq::linear_plan(T, desc->d_out, desc->d_in, int(dtype_size(desc->x_dtype)));
+  out->kernel = p.kind;
+  out->splits = p.splits;
+  return HQ_OK;
+}
+
 int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,
               int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
               size_t workspace_bytes, void* stream) {

@@ -153,6 +153,19 @@ hipError_t launch_gemm_few(int engine, const void* A, int64_t M, const void* B, 
 size_t linear_part_bytes(int64_t M, int64_t N, int K, int esize);
 hipError_t launch_linear(const void* X, int bf16, int64_t M, const void* W, int64_t N, int K,
                          void* part, const LinEpi& ep, hipStream_t s);
+// The kernel of a product (the C ABI's hq_linear_kernel) and its splits over K: a
+// kernel per row count, waves sharing 16 x 16 tiles, MFMA tiles of ROWSxCOLUMNS (X2,
+// X4: groups of waves on a tile's k-steps; W8: two blocks of eight waves per CU) and
+// the wide bf16 tiles.
+enum LinKind {
+  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128,
+  LIN_T128, LIN_T128X2, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
+};
+struct LinPlan {
+  LinKind kind;
+  int splits, kper;
+};
+LinPlan linear_plan(int64_t M, int64_t N, int K, int esize);
 // The activation `act` (hq_act) as the kernels take it.
 ActCoef act_coef(int act);
 

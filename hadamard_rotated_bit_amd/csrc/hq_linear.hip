@@ -836,13 +836,6 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(const float* __restr
 
 // ---- host side --------------------------------------------------------------------
 
-namespace {
-
-enum LinKind {
-  LIN_ROWS, LIN_FEW, LIN_T32, LIN_T32X4, LIN_T64X2, LIN_T64, LIN_T64X128,
-  LIN_T128, LIN_T128X2, LIN_T128W8, LIN_T128X192, LIN_PP3, LIN_PP4
-};
-
 // Kernel and split count of a product.
 //  up to 4 rows: the vector kernel (4096 -> 16384 bf16: 25 us at one row, 30 at four;
 //    at eight it would take 43).
@@ -900,10 +893,6 @@ enum LinKind {
 //    three against 20 whole), where they are half the CUs at 40 (8192 x 1152 -> 128,
 //    256 tiles: 21.4 us whole against 25.6 in two), or more than 512 of them with one group and a third
 //    block per CU (4096 x 640 -> 640: 31.9 us against 33.6).
-struct LinPlan {
-  LinKind kind;
-  int splits, kper;
-};
 LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   LinPlan p = {LIN_ROWS, 1, (K * esize + 127) / 128};
   const bool bf16 = esize == 2;
@@ -961,6 +950,8 @@ LinPlan linear_plan(int64_t M, int64_t N, int K, int esize) {
   }
   return p;
 }
+
+namespace {
 
 template <typename TE, int TT>
 void launch_rows_nc(const TE* X, int M, const TE* W, int64_t N, int K, const LinEpi& ep,

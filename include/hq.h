@@ -344,6 +344,31 @@ int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, con
               int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
               size_t workspace_bytes, void* stream);
 
+/* Which kernel a hq_linear call runs. */
+typedef enum {
+  HQ_LINEAR_ROWS = 0,      /* up to 4 rows, vector ALU                             */
+  HQ_LINEAR_FEW = 1,       /* 16 x 16 tiles, waves sharing the k-steps             */
+  HQ_LINEAR_T32 = 2,       /* 32 x 64 tiles, two groups of waves on the k-steps    */
+  HQ_LINEAR_T32X4 = 3,     /* the same, four groups (bf16)                         */
+  HQ_LINEAR_T64X2 = 4,     /* 64 x 64, two groups                                  */
+  HQ_LINEAR_T64 = 5,       /* 64 x 64, one group (fp32)                            */
+  HQ_LINEAR_T64X128 = 6,   /* 64 x 128, two groups (bf16)                          */
+  HQ_LINEAR_T128 = 7,      /* 128 x 128                                            */
+  HQ_LINEAR_T128X2 = 8,    /* 128 x 128, two groups (bf16)                         */
+  HQ_LINEAR_T128W8 = 9,    /* 128 x 128, two blocks of eight waves per CU (bf16)   */
+  HQ_LINEAR_T128X192 = 10, /* 128 x 192, two groups (bf16)                         */
+  HQ_LINEAR_256X192 = 11,  /* wide tiles (bf16)                                    */
+  HQ_LINEAR_256X256 = 12
+} hq_linear_kernel;
+typedef struct {
+  int32_t kernel;  /* hq_linear_kernel                                            */
+  int32_t splits;  /* parts of d_in whose sums a second kernel adds; 1: not split */
+} hq_linear_plan;
+
+/* Bookkeeping, host-only (for testing and profiling): how hq_linear runs T
+ * rows; all zero for T = 0. */
+int hq_linear_plan_of(const hq_linear_desc* desc, int64_t T, hq_linear_plan* out);
+
 /* Group norm descriptor: channels a multiple of 8 up to 4096; groups dividing
  * it (any width: channels / groups need not be a multiple of 8); act an
  * hq_act; x_dtype and y_dtype any hq_dtype; eps >= 0. */
