@@ -5,6 +5,7 @@ import itertools
 import pytest
 
 import hadamard_rotated_bit_amd as hq
+from test_gpu_norm_kernels import CASES, form
 
 LIMIT = 1 << 26     # samples x positions
 
@@ -54,3 +55,11 @@ def test_refusals():
     with pytest.raises(hq.HqError):
         hq.group_norm_plan(hq.NormDesc(64, 7), 1, 1)
     assert hq.load().hq_group_norm_plan(d._ref, 1, 1, None) == -1
+
+
+@pytest.mark.parametrize("dt", [hq.F32, hq.BF16])
+def test_gpu_shapes_run_the_form_they_are_listed_for(dt):
+    for case in CASES:
+        kernel, S, P, C, G = case.values
+        assert form(S, P, C, G, dt) == kernel, case.id
+    assert {c.values[0] for c in CASES} == {hq.HQ_NORM_ROWS, hq.HQ_NORM_BLOCK, hq.HQ_NORM_CHUNKS, hq.HQ_NORM_CHUNKS_JOINED}
