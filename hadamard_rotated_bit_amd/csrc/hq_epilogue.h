@@ -16,11 +16,13 @@ namespace hq {
 __device__ __forceinline__ float relu_f32(float x) { return x < 0.0f ? 0.0f : x; }  // keeps NaN
 
 // SiLU, GELU and its tanh form are all x / (1 + 2^(x P(x^2))): P is the
-// constant -log2(e) for SiLU (DEG 0) and linear for the tanh form (DEG 1, fp32
-// accuracy), and for GELU with a bf16 result (DEG 6) the fit of -log2(Phi(x) /
-// Phi(-x)) / x on |x| <= 5 (relative error of phi at most 1.1e-4 there: 1/37
-// of a bf16 half step; beyond, x^2 is held at 25 and phi differs from x or 0
-// by less than 1.5e-5 in absolute value). One exp2 and one reciprocal per value;
+// constant -log2(e) for SiLU (DEG 0) and linear for the tanh form (DEG 1), and
+// for GELU with a bf16 result (DEG 6) the fit of -log2(Phi(x) / Phi(-x)) / x on
+// |x| <= 5 (relative error of phi at most 1.1e-4 there: 1/37 to 1/18 of a bf16
+// half step, which is 2^-8 to 2^-9 of the value; beyond, x^2 is held at 25 and phi
+// differs from x or 0 by less than 1.5e-5 in absolute value). The exponent x P
+// carries about two (DEG 0) to five (DEG 1) fp32 roundings, each |x P| 2^-24 ln 2 of
+// the result where x < 0. One exp2 and one reciprocal per value;
 // the degree is fixed per loop, as the exponent's terms are what the vector
 // ALU spends on it.
 template <int DEG>
@@ -37,7 +39,8 @@ __device__ __forceinline__ float act_sigmoid(float x, const ActCoef& a) {
 
 // GELU for an fp32 result: max(x, 0) - |x| h(|x|), h(a) = Phi(-a) =
 // e^(-a^2/2) times a degree-10 fit in t = 1 / (1 + 0.4 a) (relative error
-// 1.4e-8); no difference of near-equal numbers for any x. a is held at 40,
+// 1.4e-8); no difference of near-equal numbers for any x. a^2 / 2 carries three
+// roundings, each a^2 / 2 x 2^-24 of h. a is held at 40,
 // where h is 0 in fp32, so that +-inf give inf and 0.
 __device__ __forceinline__ float gelu_full(float x) {
   const float a = fminf(fabsf(x), 40.0f);
