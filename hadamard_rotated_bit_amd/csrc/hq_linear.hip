@@ -99,7 +99,8 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(const TE* __restrict__
 //
 // fp32 operands run on the bf16 matrix units too: x = h + m + l with h the
 // upper 16 bits of x (a bf16 by truncation), m those of x - h and l = x - h - m,
-// which has 8 bits left, all three exact. The product keeps
+// which has 8 bits left, all three exact (|x| >= 2^-110: below, l is cut at 2^-133, the
+// smallest bf16; the matrix unit keeps subnormals). The product keeps
 //   x w = h h + (h m + m h) + (h l + m m + l h)
 // and leaves m l and l m, each at most 2^-22 of |x w| (with |x| in [2^e, 2^(e+1)):
 // m < 2^(e-7), l < 2^(e-15)), and l l below 2^-29; sums stay in fp32. Six MFMAs of 32

@@ -277,9 +277,9 @@ int hq_quant_linear_noalloc(const hq_desc* desc, const void* prepared, const voi
  * exponent of e^-x is rounded to fp32, which tells in the small results far
  * from 0 (measured: 14 x 2^-24 at V >= -3, 204 x 2^-24 at V >= -10); results
  * below 2^-119 may be 0. For bf16 Y it is a relative 1.1e-4 (GELU, |V| up to 5;
- * beyond it 1.5e-5 absolute) or better, a small part of the rounding to bf16. NaN goes through
- * every activation, +inf stays +inf; -inf gives 0 with ReLU and, where the
- * formula reads -inf * 0, NaN or 0. */
+ * beyond it 1.5e-5 absolute) or better, a small part of the rounding to bf16.
+ * NaN goes through every activation, +inf stays +inf; -inf gives 0 with ReLU
+ * and, where the formula reads -inf * 0, NaN or 0. */
 typedef enum {
   HQ_ACT_NONE = 0,
   HQ_ACT_RELU = 1,      /* max(x, 0)                                           */
@@ -337,12 +337,13 @@ size_t hq_linear_workspace_bytes(const hq_linear_desc* desc, int64_t T);
  *  workspace at least hq_linear_workspace_bytes(desc, T) bytes (NULL when that
  *  is 0), not shared with a concurrent call. T up to 2^26; T = 0 is a no-op.
  *  Neither Y nor the workspace may overlap X, weight, bias, the gate or each
- *  other, nor the workspace the residual. The same inputs always give the same bits (sums have a fixed order
- *  for a given shape). fp32 operands enter the matrix units as exact sums of
- *  three bf16 parts; of a product's nine partial ones the two that are at most
- *  2^-22 of it (2^-25 on average) and the one below 2^-29 are left out. An infinite or NaN
- *  value of X or weight makes the outputs it enters infinite or NaN, and no
- *  others. */
+ *  other, nor the workspace the residual. The same inputs always give the same
+ *  bits (sums have a fixed order for a given shape). From 5 rows on fp32 operands
+ *  enter the matrix units as sums of three bf16 parts, exact from 2^-110 on
+ *  (1e-33; smaller values are cut at 2^-133, the smallest bf16); of a product's
+ *  nine partial ones the two that are at most 2^-22 of it (2^-25 on average) and
+ *  the one below 2^-29 are left out. An infinite or NaN value of X or weight makes
+ *  the outputs it enters infinite or NaN, and no others. */
 int hq_linear(const hq_linear_desc* desc, const void* X, const void* weight, const float* bias,
               int64_t T, const hq_epilogue* epilogue, void* Y, void* workspace,
               size_t workspace_bytes, void* stream);

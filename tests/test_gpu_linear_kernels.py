@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import hadamard_rotated_bit_amd as hq
-from epilogue_ref import DT
+from epilogue_ref import DT, U32, assert_within
 from test_gpu_linear import make, run
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +128,22 @@ def test_graph_replays(dt, T, K, N):
         assert torch.equal(out, Ya if rep % 2 == 0 else Yb), f"replay {rep}"
         assert torch.equal(other, Yb)
     del graph
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300, 2100])
+@pytest.mark.parametrize("e", [-100, -109, -112, -118, -126, -130, -140, -149])
+@pytest.mark.parametrize("small", ["X", "W"])
+def test_smallest_fp32_operands(T, e, small):
+    # one operand at 2^e, the other at 2^100: what a part of a split loses is less than
+    # 2^-133 of the small operand and, below 2^-110, nothing else than that
+    K, N = 264, 136
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T - e)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").double()
+    X, W = (r(T, K) * 2.0 ** (e if small == "X" else 100)).float(), (r(N, K) * 2.0 ** (e if small == "W" else 100)).float()
+    x, w = X.double(), W.double()
+    v = x @ w.t().contiguous()
+    size = x.abs() @ w.abs().t().contiguous()
+    lost = 2.0 ** -133 * (w.abs().sum(1)[None, :] if small == "X" else x.abs().sum(1)[:, None])
+    tol = (K + 6 + 8) * U32 * (size + lost) + (lost if T > 4 else 0.0) + 2.0 ** -149
+    assert_within(hq.linear(hq.LinearDesc(K, N), X, W), v, tol.expand_as(v), f"T={T} e={e} {small}")
