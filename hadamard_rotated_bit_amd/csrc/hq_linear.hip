@@ -957,13 +957,17 @@ namespace {
 template <typename TE, int TT>
 void launch_rows_nc(const TE* X, int M, const TE* W, int64_t N, int K, const LinEpi& ep,
                     hipStream_t s) {
-  // columns per wave: more reuse of X per load of W where there are waves enough
-  if (N >= 4096)
-    hipLaunchKernelGGL((linear_rows_kernel<TE, TT, 2>), dim3(unsigned((N + 7) / 8)), dim3(256), 0, s,
-                       X, M, W, N, K, ep);
-  else
-    hipLaunchKernelGGL((linear_rows_kernel<TE, TT, 1>), dim3(unsigned((N + 3) / 4)), dim3(256), 0, s,
-                       X, M, W, N, K, ep);
+  // columns per wave: more reuse of X per load of W where there are waves enough (3
+  // and 4 bf16 rows of as many outputs take linear_few_kernel)
+  if constexpr (sizeof(TE) == 4 || TT <= 2) {
+    if (N >= 4096) {
+      hipLaunchKernelGGL((linear_rows_kernel<TE, TT, 2>), dim3(unsigned((N + 7) / 8)), dim3(256), 0,
+                         s, X, M, W, N, K, ep);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((linear_rows_kernel<TE, TT, 1>), dim3(unsigned((N + 3) / 4)), dim3(256), 0, s,
+                     X, M, W, N, K, ep);
 }
 
 template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
