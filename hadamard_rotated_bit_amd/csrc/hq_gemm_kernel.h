@@ -172,10 +172,11 @@ __device__ __forceinline__ void gemm_epilogue(AccT (&acc)[TM][TN], uint8_t* smem
 // idle LDS that belongs to the wave and taken back as rows of eight columns
 // per lane, so that residual, gate and Y move in whole row segments and phi is
 // written once, in a rolled loop (unrolled over the accumulators its code
-// overflowed the registers). Bound by its vector instructions, about 20 per
-// output with the tanh GELU: 8192 x 1152 -> 4608 on the FP6 engine 55 us against
-// 39 without one, 4353 x 4608 -> 1152 gated 31 us. LDSB: bytes of LDS there are;
-// Q: see finish_rows.
+// overflowed the registers). About 20 vector instructions per output with the tanh
+// GELU: 8192 x 1152 -> 4608 on the FP6 engine 51 us against 39 without one, vector
+// issue 50 % and MFMAs 20 % of the busy cycles, as blocks of equal work stay in step;
+// 4353 x 4608 -> 1152 gated 30 us, where vector issue is 15 % and the loads are waited
+// for. LDSB: bytes of LDS there are; Q: see finish_rows.
 template <int BM, int BN, int TM, int TN, int NW, int LDSB, int Q, typename AccT>
 __device__ __forceinline__ void gemm_epilogue_ext(AccT (&acc)[TM][TN], uint8_t* smem, int tid,
                                                   int lane, int64_t m0, int64_t n0, int wm0,

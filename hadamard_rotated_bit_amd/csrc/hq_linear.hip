@@ -319,9 +319,9 @@ __device__ __forceinline__ int xcd_tile(int tile, int n) {
 // g + G, ...; one barrier per G steps), for products with too few tiles to fill
 // the CUs: their sums meet in LDS, in group order.
 // Few tiles are bound by the latency of their k-steps (300 x 4096 -> 1152 bf16:
-// 11.9 us; 1037 x 1160 -> 2312: 16.7 us, where rows of 2320 bytes straddle the
+// 12.0 us; 1037 x 1160 -> 2312: 16.8 us, where rows of 2320 bytes straddle the
 // 128-byte lines), fp32 by the vector instructions of the splits beside the MFMAs
-// (8192 x 4096 -> 4096: 1.36 ms, 202 TFLOP/s; 12288 x 256 -> 256: 17.6 us).
+// (8192 x 4096 -> 4096: 1.38 ms, 199 TFLOP/s; 12288 x 256 -> 256: 17.7 us).
 template <typename TE, int BM, int BN, int WM, int WN, int G, int S, int OCC>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64 * G)
 __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
@@ -493,8 +493,9 @@ __attribute__((amdgpu_waves_per_eu(OCC))) void linear_tile_kernel(
 // newer loads (they retire in order), the same sequence in every k-step;
 // stages past the end are issued against an empty descriptor and move nothing.
 // Bound by the MFMAs under the chip's power limit: 8192 x 4096 -> 4096 with GELU
-// 200 us, 1.37 PFLOP/s; 8192 x 4608 -> 1152 gated 86 us, 1.0 PFLOP/s, as its 192
-// tiles leave a quarter of the CUs idle.
+// 201 us, 1.37 PFLOP/s, in a long run (241 us in the first thirty calls after idle);
+// 8192 x 4608 -> 1152 gated 86 us (95), 1.0 PFLOP/s, as its 192 tiles leave a quarter
+// of the CUs idle.
 // LDS rows and their swizzle are those of linear_tile_kernel; the rows of A
 // are stored half by half (rows 64 r + 32 i + .. of half i together), those of
 // B strip by strip, so that each piece is one contiguous range.

@@ -356,8 +356,7 @@ constexpr int NORM_BLOCK_GROUPS = 512;   // groups per slab at most
 
 // Block (slab, sample): R rows per lane in registers. Bound by the one read and
 // write of its slab by as many CUs as there are slabs (8 x 1536 x 256 fp32, 128
-// blocks: 13.1 us, 1.9 TB/s) and, for short ones, by the barriers of the tree (3
-// x 77 x 320: 5.7 us).
+// blocks: 13.9 us, 1.8 TB/s) and by the barriers of the tree (3 x 77 x 320: 6.4 us).
 template <typename TE, int U, int NT, int R>
 __global__ __launch_bounds__(NT) void norm_block_kernel(NormKArgs k) {
   constexpr int NS = 8 / U;
@@ -407,8 +406,8 @@ __global__ __launch_bounds__(NT) void norm_block_kernel(NormKArgs k) {
 
 // Partial statistics of chunk c of sample s (block s chunks + c). A batch of
 // rows is loaded before the one in registers is summed. 512 x 512 x 128 bf16
-// (one sample of 2^18 positions): 16.4 us, 4.1 TB/s; norm_apply_kernel on the
-// same: 21 us, 6.4 TB/s of reads and writes.
+// (one sample of 2^18 positions): 16.8 us, 4.0 TB/s; norm_apply_kernel on the
+// same: 20.4 us, 6.6 TB/s of reads and writes.
 template <typename TE, int U, int NT>
 __global__ __launch_bounds__(NT) void norm_stats_kernel(NormKArgs k) {
   constexpr int NS = 8 / U;
