@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import Optional
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -28,7 +28,8 @@ from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_A
                    HQ_LINEAR_T32, HQ_LINEAR_T32X4, HQ_LINEAR_T64, HQ_LINEAR_T64X2,
                    HQ_LINEAR_T64X128, HQ_LINEAR_T128, HQ_LINEAR_T128W8, HQ_LINEAR_T128X2,
                    HQ_LINEAR_T128X192, HQ_NORM_BLOCK, HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED,
-                   HQ_NORM_ROWS, HqDesc, HqError,
+                   HQ_NORM_ROWS, HQ_POS_F32, HQ_POS_I32, HQ_RMS_CODES, HQ_RMS_SUM, HQ_RMS_Y,
+                   HQ_ROPE_HALVES, HQ_ROPE_MAX_AXES, HQ_ROPE_PAIRS, HqDesc, HqError,
                    HqLayout, check, load)
 
 F32, BF16 = 0, 1
@@ -624,6 +625,234 @@ def group_norm(desc: NormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = 
         workspace, lib.hq_group_norm_workspace_bytes(desc._ref, S, P), X, device)
     check(lib.hq_group_norm(desc._ref, X.data_ptr(), _addr(gamma), _addr(beta), S, P,
                             out.data_ptr(), ws_addr, ws_bytes, _stream_of(device)))
+    return out
+
+
+# ---- RMS norm, rotary positions, adapters ------------------------------------
+
+@dataclasses.dataclass(frozen=True)
+class RmsNormDesc:
+    """RMS-norm descriptor; mirrors hq_rms_desc. ``outputs``: a sum of HQ_RMS_Y
+    (the norm), HQ_RMS_SUM (X + residual) and HQ_RMS_CODES (int8 codes of the norm
+    with a scale per row)."""
+    channels: int
+    eps: float = 1e-6
+    outputs: int = HQ_RMS_Y
+    x_dtype: int = F32
+    y_dtype: int = F32
+
+    def __post_init__(self):
+        raw = _lib.HqRmsDesc(self.channels, self.outputs, self.x_dtype, self.y_dtype, self.eps)
+        object.__setattr__(self, "_raw", raw)
+        object.__setattr__(self, "_ref", ctypes.byref(raw))
+
+
+class RmsNorm(NamedTuple):
+    """rms_norm's outputs; None for those the descriptor does not ask for."""
+    y: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
+def rms_norm(desc: RmsNormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+             residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             sum_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+             scales: Optional[torch.Tensor] = None) -> RmsNorm:
+    """RMS norm of h = X + residual for X [T, channels] (hq_rms_norm): y = h gamma /
+    sqrt(mean(h^2) + eps), h itself, and y as int8 ``codes`` [T, channels] with
+    ``scales`` [T] (y ~ codes * scales), which gemm_dequant takes for a layer of
+    block 1 and 8-bit activations. ``sum_out`` (h) and ``out`` (y) may be X or
+    residual; outputs not given are allocated."""
+    if X.dim() != 2:
+        raise ValueError(f"X must be [T, channels], got {tuple(X.shape)}")
+    shape, xdt = (X.shape[0], desc.channels), _TORCH[desc.x_dtype]
+    device = _gpu_of(X, "X", xdt, shape)
+    if device != _current_gpu():   # kernels launch on the current device
+        with torch.cuda.device(device):
+            return rms_norm(desc, X, gamma, residual, out, sum_out, codes, scales)
+    if residual is not None:
+        _fits(residual, "residual", xdt, shape, device)
+    if gamma is not None:
+        _fits(gamma, "gamma", torch.float32, (desc.channels,), device)
+    want = desc.outputs
+
+    def output(t, name, dtype, size, flag):
+        if not want & flag:
+            if t is not None:
+                raise ValueError(f"{name} is not among the descriptor's outputs")
+            return None
+        if t is None:
+            return torch.empty(size, dtype=dtype, device=X.device)
+        _fits(t, name, dtype, size, device)
+        return t
+
+    out = output(out, "out", _TORCH[desc.y_dtype], shape, HQ_RMS_Y)
+    sum_out = output(sum_out, "sum_out", xdt, shape, HQ_RMS_SUM)
+    codes = output(codes, "codes", torch.int8, shape, HQ_RMS_CODES)
+    scales = output(scales, "scales", torch.float32, shape[:1], HQ_RMS_CODES)
+    check(load().hq_rms_norm(desc._ref, X.data_ptr(), _addr(residual), _addr(gamma), shape[0],
+                             _addr(sum_out), _addr(out), _addr(codes), _addr(scales),
+                             _stream_of(device)))
+    return RmsNorm(out, sum_out, codes, scales)
+
+
+@dataclasses.dataclass(frozen=True)
+class RopeDesc:
+    """Rotary-position descriptor; mirrors hq_rope_desc. ``pairs``: the rotated pairs
+    of each axis; ``layout``: HQ_ROPE_PAIRS (neighbours) or HQ_ROPE_HALVES; ``norm``:
+    an RMS norm of each head before its rotation; ``inverse``: the opposite rotation;
+    ``pos_dtype``: HQ_POS_I32 or HQ_POS_F32."""
+    q_heads: int
+    k_heads: int
+    head_dim: int
+    pairs: Tuple[int, ...]
+    layout: int = HQ_ROPE_PAIRS
+    norm: bool = False
+    eps: float = 1e-6
+    inverse: bool = False
+    pos_dtype: int = HQ_POS_I32
+    x_dtype: int = F32
+    y_dtype: int = F32
+
+    def __post_init__(self):
+        pairs = tuple(int(p) for p in self.pairs)
+        if not 1 <= len(pairs) <= HQ_ROPE_MAX_AXES:
+            raise ValueError(f"pairs must name 1 to {HQ_ROPE_MAX_AXES} axes, got {pairs}")
+        object.__setattr__(self, "pairs", pairs)
+        raw = _lib.HqRopeDesc(self.q_heads, self.k_heads, self.head_dim, len(pairs),
+                              (ctypes.c_int32 * HQ_ROPE_MAX_AXES)(*pairs), self.layout,
+                              int(self.norm), int(self.inverse), self.pos_dtype, self.x_dtype,
+                              self.y_dtype, self.eps)
+        object.__setattr__(self, "_raw", raw)
+        object.__setattr__(self, "_ref", ctypes.byref(raw))
+
+
+def rope_freqs(desc: RopeDesc, theta: float = 10000.0, per_axis: bool = True,
+               device="cuda") -> torch.Tensor:
+    """The usual frequencies of ``desc``'s pairs, float64 (rope takes any others as
+    well): theta^(-i / p) for pair i of an axis of p pairs, or with ``per_axis``
+    false theta^(-i / P) for pair i of all P (the axes share one sequence)."""
+    total = sum(desc.pairs)
+    axes = desc.pairs if per_axis else (total,)
+    e = torch.cat([torch.arange(p, dtype=torch.float64) / max(p, 1) for p in axes])
+    return torch.pow(torch.tensor(float(theta), dtype=torch.float64), -e).to(device)
+
+
+def _rows_of(t: torch.Tensor, name: str, dtype: torch.dtype, T: int, width: int) -> int:
+    """Checks a [T, >= width] tensor whose rows may be strided; returns its row pitch."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] < width:
+        raise ValueError(f"{name} must have shape ({T}, >= {width}), got {tuple(t.shape)}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.stride(0) if T > 1 else -(-t.shape[1] // 8) * 8
+
+
+def rope(desc: RopeDesc, X: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+         gamma_q: Optional[torch.Tensor] = None, gamma_k: Optional[torch.Tensor] = None,
+         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions on the q and k heads at the start of each row of X [T, >=
+    (q_heads + k_heads) head_dim] (hq_rope), behind an RMS norm of each head with
+    ``desc.norm``. ``positions`` [T, axes], ``freqs`` float64 (rope_freqs). X and
+    ``out`` may have strided rows (a packed projection); ``out`` may be X itself: q and
+    k are then turned in place. Returns ``out``, allocated as [T, (q_heads + k_heads)
+    head_dim] when it is not given."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a tensor [T, channels]")
+    T, width = X.shape[0], (desc.q_heads + desc.k_heads) * desc.head_dim
+    ldx = _rows_of(X, "X", _TORCH[desc.x_dtype], T, width)
+    device = X.get_device()
+    if device != _current_gpu():   # kernels launch on the current device
+        with torch.cuda.device(device):
+            return rope(desc, X, positions, freqs, gamma_q, gamma_k, out)
+    _fits(positions, "positions", torch.float32 if desc.pos_dtype == HQ_POS_F32 else torch.int32,
+          (T, len(desc.pairs)), device)
+    _fits(freqs, "freqs", torch.float64, (sum(desc.pairs),), device)
+    for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if g is not None:
+            _fits(g, name, torch.float32, (desc.head_dim,), device)
+    if out is None:
+        out = torch.empty((T, width), dtype=_TORCH[desc.y_dtype], device=X.device)
+        ldy = width
+    else:
+        ldy = _rows_of(out, "out", _TORCH[desc.y_dtype], T, width)
+        if out.get_device() != device:
+            raise ValueError(f"out is on {out.device}, X on cuda:{device}")
+    check(load().hq_rope(desc._ref, X.data_ptr(), ldx, positions.data_ptr(), freqs.data_ptr(),
+                         _addr(gamma_q), _addr(gamma_k), T, out.data_ptr(), ldy,
+                         _stream_of(device)))
+    return out
+
+
+@dataclasses.dataclass(frozen=True)
+class AdapterDesc:
+    """Descriptor of low-rank adapters beside a projection; mirrors hq_adapter_desc
+    (x_dtype = w_dtype; ``rank`` the largest of the adapters)."""
+    d_in: int
+    d_out: int
+    rank: int
+    x_dtype: int = F32
+    w_dtype: int = F32
+    y_dtype: int = F32
+
+    def __post_init__(self):
+        raw = _lib.HqAdapterDesc(self.d_in, self.d_out, self.rank, self.x_dtype, self.w_dtype,
+                                 self.y_dtype)
+        object.__setattr__(self, "_raw", raw)
+        object.__setattr__(self, "_ref", ctypes.byref(raw))
+
+
+def adapters_workspace_bytes(desc: AdapterDesc, T: int) -> int:
+    """Workspace bytes of adapters for T rows."""
+    n = load().hq_adapters_workspace_bytes(desc._ref, T)
+    if n == 0:
+        check(load().hq_adapter_validate(desc._ref))
+        if T < 0:
+            raise HqError(_lib.HQ_ERR_INVALID_ARG, "T must be >= 0")
+    return n
+
+
+def adapters(desc: AdapterDesc, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+             ids: torch.Tensor, scales: Optional[torch.Tensor] = None,
+             base: Optional[torch.Tensor] = None, epilogue: Optional[Epilogue] = None,
+             out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = residual + gate * phi(base + scales[a] B_a (A_a X)) row by row, a = ids[row]
+    (hq_adapters): the low-rank adapters of many requests beside a projection that gave
+    ``base`` [T, d_out] (absent: zeros). X [T, d_in], A [count, rank, d_in], B [count,
+    d_out, rank], ids int32 [T] (outside 0 .. count - 1: no adapter). ``out`` may be
+    base itself; ``workspace`` (adapters_workspace_bytes(desc, T) bytes) is allocated
+    when it is needed and not given."""
+    if X.dim() != 2:
+        raise ValueError(f"X must be [T, d_in], got {tuple(X.shape)}")
+    T, wdt, ydt = X.shape[0], _TORCH[desc.w_dtype], _TORCH[desc.y_dtype]
+    device = _gpu_of(X, "X", _TORCH[desc.x_dtype], (T, desc.d_in))
+    if device != _current_gpu():   # kernels launch on the current device
+        with torch.cuda.device(device):
+            return adapters(desc, X, A, B, ids, scales, base, epilogue, out, workspace)
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A must be [count, rank, d_in]")
+    count = A.shape[0]
+    _fits(A, "A", wdt, (count, desc.rank, desc.d_in), device)
+    _fits(B, "B", wdt, (count, desc.d_out, desc.rank), device)
+    _fits(ids, "ids", torch.int32, (T,), device)
+    if scales is not None:
+        _fits(scales, "scales", torch.float32, (count,), device)
+    if base is not None:
+        _fits(base, "base", ydt, (T, desc.d_out), device)
+    if out is None:
+        out = torch.empty((T, desc.d_out), dtype=ydt, device=X.device)
+    else:
+        _fits(out, "out", ydt, (T, desc.d_out), device)
+    ep = None if epilogue is None else epilogue._c(T, desc.d_out, ydt, device)
+    lib = load()
+    ws, ws_addr, ws_bytes = _workspace_of(
+        workspace, lib.hq_adapters_workspace_bytes(desc._ref, T), X, device)
+    check(lib.hq_adapters(desc._ref, X.data_ptr(), A.data_ptr(), B.data_ptr(), count,
+                          ids.data_ptr(), _addr(scales), _addr(base), T, ep, out.data_ptr(),
+                          ws_addr, ws_bytes, _stream_of(device)))
     return out
 
 

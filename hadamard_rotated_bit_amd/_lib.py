@@ -50,6 +50,22 @@ class HqNormDesc(ctypes.Structure):
                 ["channels", "groups", "act", "x_dtype", "y_dtype"]] + [("eps", ctypes.c_float)]
 
 
+class HqRmsDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ["channels", "outputs", "x_dtype", "y_dtype"]] + [
+        ("eps", ctypes.c_float)]
+
+
+class HqRopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ["q_heads", "k_heads", "head_dim", "axes"]] + [
+        ("pairs", ctypes.c_int32 * 4)] + [(n, ctypes.c_int32) for n in
+        ["layout", "norm", "inverse", "pos_dtype", "x_dtype", "y_dtype"]] + [("eps", ctypes.c_float)]
+
+
+class HqAdapterDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ["d_in", "d_out", "rank", "x_dtype", "w_dtype", "y_dtype"]]
+
+
 class HqLinearPlan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("splits", ctypes.c_int32)]
 
@@ -64,6 +80,10 @@ HQ_LINEAR_ROWS, HQ_LINEAR_FEW, HQ_LINEAR_T32, HQ_LINEAR_T32X4, \
     HQ_LINEAR_T128X2, HQ_LINEAR_T128W8, HQ_LINEAR_T128X192, HQ_LINEAR_256X192, HQ_LINEAR_256X256 = range(13)
 HQ_NORM_ROWS, HQ_NORM_BLOCK, HQ_NORM_CHUNKS, HQ_NORM_CHUNKS_JOINED = 0, 1, 2, 3
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
+HQ_RMS_Y, HQ_RMS_SUM, HQ_RMS_CODES = 1, 2, 4
+HQ_ROPE_PAIRS, HQ_ROPE_HALVES = 0, 1
+HQ_POS_I32, HQ_POS_F32 = 0, 1
+HQ_ROPE_MAX_AXES = 4
 HQ_GEMM_AUTO, HQ_GEMM_I8 = 0, 1
 HQ_CENTER_NONE, HQ_CENTER_TOKEN, HQ_CENTER_CHANNEL = 0, 1, 2
 HQ_INT_WH, HQ_INT_DH = 0, 1
@@ -78,6 +98,9 @@ _W = ctypes.POINTER(HqIntDesc)
 _E = ctypes.POINTER(HqEpilogue)
 _L = ctypes.POINTER(HqLinearDesc)
 _N = ctypes.POINTER(HqNormDesc)
+_R = ctypes.POINTER(HqRmsDesc)
+_O = ctypes.POINTER(HqRopeDesc)
+_A = ctypes.POINTER(HqAdapterDesc)
 _I64 = ctypes.c_int64
 _SIGS = {
     "hq_abi_version": (ctypes.c_int, []),
@@ -104,6 +127,14 @@ _SIGS = {
     "hq_group_norm_workspace_bytes": (ctypes.c_size_t, [_N, _I64, _I64]),
     "hq_group_norm_plan": (ctypes.c_int, [_N, _I64, _I64, ctypes.POINTER(HqNormPlan)]),
     "hq_group_norm": (ctypes.c_int, [_N, _P, _P, _P, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "hq_rms_validate": (ctypes.c_int, [_R]),
+    "hq_rms_norm": (ctypes.c_int, [_R, _P, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    "hq_rope_validate": (ctypes.c_int, [_O]),
+    "hq_rope": (ctypes.c_int, [_O, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P]),
+    "hq_adapter_validate": (ctypes.c_int, [_A]),
+    "hq_adapters_workspace_bytes": (ctypes.c_size_t, [_A, _I64]),
+    "hq_adapters": (ctypes.c_int, [_A, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _I64, _E, _P, _P,
+                                   ctypes.c_size_t, _P]),
     "hq_channel_center": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     "hq_act_quantize": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P]),
     "hq_act_quantize_ws": (ctypes.c_int, [_D, _P, _P, _I64, _P, _P, _P, _P, _P,

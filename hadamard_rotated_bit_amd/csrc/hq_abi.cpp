@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/hq.h"
@@ -405,6 +406,93 @@ int check_positions(int64_t S, int64_t P) {
     return fail(HQ_ERR_UNSUPPORTED, "samples x positions must be at most %lld (got %lld x %lld)",
                 (long long)kMaxRows, (long long)S, (long long)P);
   return HQ_OK;
+}
+
+// ---- RMS norm, rotary positions, adapters -------------------------------------
+
+int check_rms_desc(const hq_rms_desc* d) {
+  if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
+  if (d->channels <= 0)
+    return fail(HQ_ERR_INVALID_ARG, "channels must be positive (got %d)", d->channels);
+  int st = check_dtype(d->x_dtype, "x_dtype");
+  if (st == HQ_OK) st = check_dtype(d->y_dtype, "y_dtype");
+  if (st != HQ_OK) return st;
+  if (d->outputs <= 0 || d->outputs > (HQ_RMS_Y | HQ_RMS_SUM | HQ_RMS_CODES))
+    return fail(HQ_ERR_INVALID_ARG, "outputs must be a sum of HQ_RMS_* (got %d)", d->outputs);
+  if (!(d->eps > 0.0f) || !std::isfinite(d->eps))
+    return fail(HQ_ERR_INVALID_ARG, "eps must be finite and > 0 (got %g)", double(d->eps));
+  if (d->channels % 8 || d->channels > hq::RMS_MAX_C)
+    return fail(HQ_ERR_UNSUPPORTED, "channels must be a multiple of 8 up to %d (got %d)",
+                hq::RMS_MAX_C, d->channels);
+  return HQ_OK;
+}
+
+int rope_pairs(const hq_rope_desc* d) {
+  int n = 0;
+  for (int i = 0; i < d->axes; ++i) n += d->pairs[i];
+  return n;
+}
+
+int check_rope_desc(const hq_rope_desc* d) {
+  if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
+  if (d->q_heads < 0 || d->k_heads < 0 || d->head_dim <= 0)
+    return fail(HQ_ERR_INVALID_ARG, "heads must be >= 0 and head_dim positive (got %d, %d, %d)",
+                d->q_heads, d->k_heads, d->head_dim);
+  if (d->axes < 1 || d->axes > HQ_ROPE_MAX_AXES)
+    return fail(HQ_ERR_INVALID_ARG, "axes must be 1 to %d (got %d)", HQ_ROPE_MAX_AXES, d->axes);
+  for (int i = 0; i < d->axes; ++i)
+    if (d->pairs[i] < 0 || d->pairs[i] > hq::ROPE_MAX_PAIRS)
+      return fail(HQ_ERR_INVALID_ARG, "pairs of axis %d must be 0 to %d (got %d)", i,
+                  hq::ROPE_MAX_PAIRS, d->pairs[i]);
+  if (d->layout != HQ_ROPE_PAIRS && d->layout != HQ_ROPE_HALVES)
+    return fail(HQ_ERR_INVALID_ARG, "layout %d is not an hq_rope_layout", d->layout);
+  if (d->pos_dtype != HQ_POS_I32 && d->pos_dtype != HQ_POS_F32)
+    return fail(HQ_ERR_INVALID_ARG, "pos_dtype %d is not an hq_pos_dtype", d->pos_dtype);
+  if ((d->norm != 0 && d->norm != 1) || (d->inverse != 0 && d->inverse != 1))
+    return fail(HQ_ERR_INVALID_ARG, "norm and inverse must be 0 or 1 (got %d, %d)", d->norm,
+                d->inverse);
+  int st = check_dtype(d->x_dtype, "x_dtype");
+  if (st == HQ_OK) st = check_dtype(d->y_dtype, "y_dtype");
+  if (st != HQ_OK) return st;
+  if (d->norm && (!(d->eps > 0.0f) || !std::isfinite(d->eps)))
+    return fail(HQ_ERR_INVALID_ARG, "eps must be finite and > 0 (got %g)", double(d->eps));
+  if (d->norm && d->inverse)
+    return fail(HQ_ERR_UNSUPPORTED, "inverse takes no norm (it would not undo one)");
+  if (d->q_heads > 1024 || d->k_heads > 1024 || d->q_heads + d->k_heads < 1 ||
+      d->q_heads + d->k_heads > 1024)
+    return fail(HQ_ERR_UNSUPPORTED, "1 to 1024 heads are supported (got %d + %d)", d->q_heads,
+                d->k_heads);
+  if (d->head_dim % 8 || d->head_dim > 2 * hq::ROPE_MAX_PAIRS)
+    return fail(HQ_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 up to %d (got %d)",
+                2 * hq::ROPE_MAX_PAIRS, d->head_dim);
+  const int n = rope_pairs(d);
+  if (n % 4 || n < 4 || n > d->head_dim / 2)
+    return fail(HQ_ERR_UNSUPPORTED,
+                "the pairs of all axes must be a multiple of 4 from 4 to head_dim / 2 = %d (got %d)",
+                d->head_dim / 2, n);
+  return HQ_OK;
+}
+
+int check_adapter_desc(const hq_adapter_desc* d) {
+  if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
+  const hq_linear_desc lin = {d->d_in, d->d_out, d->x_dtype, d->w_dtype, d->y_dtype};
+  const int st = check_linear_desc(&lin);
+  if (st != HQ_OK) return st;
+  if (d->rank <= 0 || d->rank % 8 || d->rank > hq::ADAPT_MAX_RANK)
+    return fail(HQ_ERR_UNSUPPORTED, "rank must be a multiple of 8 up to %d (got %d)",
+                hq::ADAPT_MAX_RANK, d->rank);
+  return HQ_OK;
+}
+
+// One operand's bytes, for checks of many against many.
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlaps_any(const void* p, size_t n, std::initializer_list<Span> of) {
+  for (const Span& o : of)
+    if (overlap(p, n, o.p, o.n)) return true;
+  return false;
 }
 
 // The hot path, with the extended epilogue where `lin` is given.
@@ -1078,6 +1166,190 @@ int hq_group_norm(const hq_norm_desc* desc, const void* X, const float* gamma, c
   a.part = need ? workspace : nullptr;
   const hipError_t e = hq::launch_group_norm(a, samples, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? HQ_OK : hip_fail(e, "group norm kernel launch");
+}
+
+int hq_rms_validate(const hq_rms_desc* desc) {
+  g_err.clear();
+  return check_rms_desc(desc);
+}
+
+int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, const float* gamma,
+                int64_t T, void* H, void* Y, int8_t* codes, float* scales, void* stream) {
+  g_err.clear();
+  int st = check_rms_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
+  if (st != HQ_OK) return st;
+  if (T == 0) return HQ_OK;
+  if (!(desc->outputs & HQ_RMS_SUM)) H = nullptr;
+  if (!(desc->outputs & HQ_RMS_Y)) Y = nullptr;
+  if (!(desc->outputs & HQ_RMS_CODES)) codes = nullptr, scales = nullptr;
+  if (!X || (desc->outputs & HQ_RMS_SUM && !H) || (desc->outputs & HQ_RMS_Y && !Y) ||
+      (desc->outputs & HQ_RMS_CODES && (!codes || !scales)))
+    return fail(HQ_ERR_INVALID_ARG, "X and every output of the descriptor must be non-NULL");
+  if (misaligned(X) || misaligned(residual) || misaligned(gamma) || misaligned(H) ||
+      misaligned(Y) || misaligned(codes) || misaligned(scales))
+    return fail(HQ_ERR_INVALID_ARG,
+                "X, residual, gamma, H, Y, codes and scales must be 16-byte aligned");
+  const size_t C = size_t(desc->channels), n = size_t(T) * C;
+  const size_t nx = n * dtype_size(desc->x_dtype), ny = n * dtype_size(desc->y_dtype);
+  const bool same = desc->x_dtype == desc->y_dtype;
+  const Span x = {X, nx}, r = {residual, nx}, g = {gamma, 4 * C}, none = {nullptr, 0};
+  if (overlaps_any(H, nx, {H == X ? none : x, H == residual ? none : r, g}))
+    return fail(HQ_ERR_INVALID_ARG, "H overlaps an input (it may be X or residual itself)");
+  if (overlaps_any(Y, ny, {same && Y == X ? none : x, same && Y == residual ? none : r, g}))
+    return fail(HQ_ERR_INVALID_ARG,
+                "Y overlaps an input (it may be X or residual itself, in the same type)");
+  if (overlaps_any(codes, n, {x, r, g}) || overlaps_any(scales, 4 * size_t(T), {x, r, g}))
+    return fail(HQ_ERR_INVALID_ARG, "codes or scales overlap an input");
+  if (overlaps_any(H, nx, {{Y, ny}, {codes, n}, {scales, 4 * size_t(T)}}) ||
+      overlaps_any(Y, ny, {{codes, n}, {scales, 4 * size_t(T)}}) ||
+      overlap(codes, n, scales, 4 * size_t(T)))
+    return fail(HQ_ERR_INVALID_ARG, "outputs overlap each other");
+  hq::RmsArgs a = {};
+  a.x = X;
+  a.r = residual;
+  a.gamma = gamma;
+  a.h = H;
+  a.y = Y;
+  a.codes = reinterpret_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.T = T;
+  a.C = desc->channels;
+  a.eps = desc->eps;
+  a.x_bf16 = desc->x_dtype == HQ_BF16;
+  a.y_bf16 = desc->y_dtype == HQ_BF16;
+  const hipError_t e = hq::launch_rms_norm(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HQ_OK : hip_fail(e, "RMS norm kernel launch");
+}
+
+int hq_rope_validate(const hq_rope_desc* desc) {
+  g_err.clear();
+  return check_rope_desc(desc);
+}
+
+int hq_rope(const hq_rope_desc* desc, const void* X, int64_t ldx, const void* positions,
+            const double* freqs, const float* gamma_q, const float* gamma_k, int64_t T, void* Y,
+            int64_t ldy, void* stream) {
+  g_err.clear();
+  int st = check_rope_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
+  if (st != HQ_OK) return st;
+  const int64_t width = int64_t(desc->q_heads + desc->k_heads) * desc->head_dim;
+  constexpr int64_t kMaxPitch = int64_t(1) << 30;
+  if (ldx < width || ldy < width || ldx % 8 || ldy % 8 || ldx > kMaxPitch || ldy > kMaxPitch)
+    return fail(HQ_ERR_INVALID_ARG,
+                "ldx and ldy must be multiples of 8 from (q_heads + k_heads) head_dim = %lld to "
+                "2^30 (got %lld, %lld)",
+                (long long)width, (long long)ldx, (long long)ldy);
+  if (T == 0) return HQ_OK;
+  if (!X || !positions || !freqs || !Y)
+    return fail(HQ_ERR_INVALID_ARG, "X, positions, freqs and Y must be non-NULL");
+  if (!desc->norm && (gamma_q || gamma_k))
+    return fail(HQ_ERR_INVALID_ARG, "gamma_q and gamma_k must be NULL without norm");
+  if (misaligned(X) || misaligned(Y) || misaligned(freqs) || misaligned(gamma_q) ||
+      misaligned(gamma_k))
+    return fail(HQ_ERR_INVALID_ARG, "X, Y, freqs, gamma_q and gamma_k must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(positions) & 3)
+    return fail(HQ_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  const size_t nx = size_t((T - 1) * ldx + width) * dtype_size(desc->x_dtype);
+  const size_t ny = size_t((T - 1) * ldy + width) * dtype_size(desc->y_dtype);
+  const bool in_place = X == Y && ldx == ldy && desc->x_dtype == desc->y_dtype;
+  if (!in_place && overlap(X, nx, Y, ny))
+    return fail(HQ_ERR_INVALID_ARG,
+                "Y overlaps X (it may be X itself, in the same type and pitch)");
+  const size_t ng = 4 * size_t(desc->head_dim);
+  if (overlaps_any(Y, ny, {{positions, 4 * size_t(T) * size_t(desc->axes)},
+                           {freqs, 8 * size_t(rope_pairs(desc))}, {gamma_q, ng}, {gamma_k, ng}}))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps positions, freqs or a gamma");
+  hq::RopeArgs a = {};
+  a.x = X;
+  a.y = Y;
+  a.pos = positions;
+  a.freqs = freqs;
+  a.gamma_q = gamma_q;
+  a.gamma_k = gamma_k;
+  a.T = T;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.Hq = desc->q_heads;
+  a.Hk = desc->k_heads;
+  a.D = desc->head_dim;
+  a.axes = desc->axes;
+  static_assert(HQ_ROPE_MAX_AXES == hq::ROPE_MAX_AXES, "the same limit");
+  for (int i = 0; i < desc->axes; ++i) a.end[i] = a.pairs += desc->pairs[i];
+  a.halves = desc->layout == HQ_ROPE_HALVES;
+  a.norm = desc->norm;
+  a.inverse = desc->inverse;
+  a.pos_f32 = desc->pos_dtype == HQ_POS_F32;
+  a.x_bf16 = desc->x_dtype == HQ_BF16;
+  a.y_bf16 = desc->y_dtype == HQ_BF16;
+  a.eps = desc->eps;
+  const hipError_t e = hq::launch_rope(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HQ_OK : hip_fail(e, "rotary position kernel launch");
+}
+
+int hq_adapter_validate(const hq_adapter_desc* desc) {
+  g_err.clear();
+  return check_adapter_desc(desc);
+}
+
+size_t hq_adapters_workspace_bytes(const hq_adapter_desc* desc, int64_t T) {
+  g_err.clear();
+  if (check_adapter_desc(desc) != HQ_OK || check_rows(T) != HQ_OK) return 0;
+  return align256(hq::adapters_part_bytes(T, desc->rank));
+}
+
+int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const void* B,
+                int32_t count, const int32_t* ids, const float* scales, const void* base, int64_t T,
+                const hq_epilogue* epilogue, void* Y, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  g_err.clear();
+  int st = check_adapter_desc(desc);
+  if (st == HQ_OK) st = check_rows(T);
+  if (st != HQ_OK) return st;
+  if (count < 0) return fail(HQ_ERR_INVALID_ARG, "count must be >= 0 (got %d)", count);
+  if (T == 0) return HQ_OK;
+  if (!X || !ids || !Y || (count && (!A || !B)))
+    return fail(HQ_ERR_INVALID_ARG, "X, A, B, ids and Y must be non-NULL");
+  if (misaligned(X) || misaligned(A) || misaligned(B) || misaligned(scales) || misaligned(base) ||
+      misaligned(Y) || misaligned(workspace))
+    return fail(HQ_ERR_INVALID_ARG,
+                "X, A, B, scales, base, Y and workspace must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(ids) & 3)
+    return fail(HQ_ERR_INVALID_ARG, "ids must be 4-byte aligned");
+  const size_t es = dtype_size(desc->x_dtype), din = size_t(desc->d_in), dout = size_t(desc->d_out);
+  const size_t ey = dtype_size(desc->y_dtype), ny = size_t(T) * dout * ey;
+  const size_t nw = size_t(count) * size_t(desc->rank) * es;
+  const Span x = {X, size_t(T) * din * es}, a = {A, nw * din}, b = {B, nw * dout},
+             id = {ids, 4 * size_t(T)}, sc = {scales, 4 * size_t(count)}, ba = {base, ny},
+             none = {nullptr, 0};
+  if (overlaps_any(Y, ny, {x, a, b, id, sc, base == Y ? none : ba}))
+    return fail(HQ_ERR_INVALID_ARG, "Y overlaps an input (it may be base itself)");
+  hq::AdaptArgs k = {};
+  st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &k.ep);
+  if (st != HQ_OK) return st;
+  const size_t need = align256(hq::adapters_part_bytes(T, desc->rank));
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
+                workspace ? workspace_bytes : size_t(0), need);
+  if (need && overlaps_any(workspace, need, {x, a, b, id, sc, ba, {Y, ny}, {k.ep.residual, ny},
+                                             {k.ep.gate, gate_bytes(k.ep, T, desc->d_out, ey)}}))
+    return fail(HQ_ERR_INVALID_ARG, "workspace overlaps an operand");
+  k.x = X;
+  k.a = A;
+  k.b = B;
+  k.ids = ids;
+  k.scales = scales;
+  k.base = base;
+  k.u = need ? static_cast<float*>(workspace) : nullptr;
+  k.T = T;
+  k.K = desc->d_in;
+  k.N = desc->d_out;
+  k.rank = desc->rank;
+  k.count = count;
+  k.bf16 = desc->x_dtype == HQ_BF16;
+  const hipError_t e = hq::launch_adapters(k, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? HQ_OK : hip_fail(e, "adapter kernel launch");
 }
 
 int hq_int_validate(const hq_int_desc* desc) {

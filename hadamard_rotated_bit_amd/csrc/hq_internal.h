@@ -196,6 +196,63 @@ struct NormPlanInfo {
 NormPlanInfo norm_plan_info(int64_t S, int64_t P, int C, int G, int esize);
 hipError_t launch_group_norm(const NormArgs& a, int64_t S, hipStream_t s);
 
+// RMS norm of h = x + r (r NULL: x) over T rows of C channels (a multiple of 8 up to
+// RMS_MAX_C): h, y and codes with scales, each where its pointer is given.
+constexpr int RMS_MAX_C = 8192;
+struct RmsArgs {
+  const void* x;
+  const void* r;
+  const float* gamma;
+  void* h;
+  void* y;
+  uint8_t* codes;
+  float* scales;
+  int64_t T;
+  int C;
+  float eps;
+  int x_bf16, y_bf16;   // h has x's type
+};
+hipError_t launch_rms_norm(const RmsArgs& a, hipStream_t s);
+
+// Rotary positions on the Hq + Hk heads of D channels (a multiple of 8 up to 256) at the
+// start of each of T rows: `pairs` pairs (a multiple of 4), end[i] the first pair behind
+// axis i. pos [T, axes].
+constexpr int ROPE_MAX_PAIRS = 128;
+constexpr int ROPE_MAX_AXES = 4;
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const void* pos;
+  const double* freqs;
+  const float* gamma_q;
+  const float* gamma_k;
+  int64_t T, ldx, ldy;
+  int Hq, Hk, D, pairs, axes, end[ROPE_MAX_AXES];
+  int halves, norm, inverse, pos_f32, x_bf16, y_bf16;
+  float eps;
+  int split;            // waves per token (the launcher's)
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
+// Low-rank adapters beside a shared projection: a [count, rank, K], b [count, N, rank],
+// ids [T] (outside 0 .. count - 1: none), scales [count] or NULL, base [T, N] or NULL in
+// the output's type. adapters_part_bytes: the workspace, given as `u`.
+struct AdaptArgs {
+  const void* x;
+  const void* a;
+  const void* b;
+  const int32_t* ids;
+  const float* scales;
+  const void* base;
+  float* u;
+  int64_t T;
+  int K, N, rank, count, bf16;
+  LinEpi ep;
+};
+constexpr int ADAPT_MAX_RANK = 128;
+size_t adapters_part_bytes(int64_t T, int rank);
+hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s);
+
 // Integer-only DH / WH layers with integer requantisation.
 constexpr int WH_MAX_BLOCK = 256;       // largest output-side Hadamard order
 constexpr int WH_SHIFT_MAX = 48;        // largest shared requantisation shift

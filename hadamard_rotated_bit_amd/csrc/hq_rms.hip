@@ -1,0 +1,276 @@
+// Root-mean-square norm of the residual stream, with the residual's addition
+// before it and, where asked for, its result as the 8-bit codes of a low-bit
+// layer:
+//
+//   h = x + r,   y = h rstd gamma,   rstd = 1 / sqrt(mean(h^2) + eps),
+//   code_c = rint(y_c / s),   s = max_c |y_c| / 127   (one scale per row).
+//
+// rstd is one factor per row, so the codes do not depend on it: code_c =
+// rint(127 v_c / max |v|) with v = h gamma, and s = rstd max |v| / 127. The sum of
+// squares and max |v| are taken in one pass over the row in registers; bound by
+// memory: x and r are read once, h, y and the codes written once.
+//
+// A code is decided as if v and the quotient were exact. In fp32, q = v rcp(max) 127
+// (one factor 127 / max) carries five roundings of 2^-24: two in v, two in the maximum
+// and one in the factor, an error below 127 x 5 x 2^-24 = 3.8e-5. Where q is further
+// than 1e-4 from a half-integer its rounding is the exact one; the values nearer to one
+// (2 in 10^4) are decided again in fp64 with the row's fp64 maximum, which needs only
+// the values within 2^-21 of the fp32 maximum in fp64. A row with a v that is not a
+// finite float has codes 0 and a NaN scale.
+#include "hq_epilogue.h"
+#include "hq_internal.h"
+
+#include <algorithm>
+
+namespace hq {
+
+namespace {
+
+constexpr float kBorder = 0.5f - 1e-4f;
+// Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats:
+// all their codes are decided in fp64.
+constexpr float kTiny = 0x1p-100f;
+
+// Maximum over the wave of a non-negative double that few lanes have.
+__device__ __forceinline__ double few_max(double v, bool mine) {
+  uint64_t left = __ballot(mine);
+  double m = 0.0;
+  while (left) {
+    const int l = __builtin_ctzll(left);
+    left &= left - 1;
+    const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(bits), l);
+    const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(bits >> 32), l);
+    m = fmax(m, __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo));
+  }
+  return m;
+}
+
+// Maximum over aligned groups of L lanes of the bits of non-negative floats: as
+// integers NaN is above infinity and infinity above every number.
+template <int L>
+__device__ __forceinline__ uint32_t bits_max(uint32_t v) {
+  auto other = [](uint32_t a, float b) { return max(a, __float_as_uint(b)); };
+  if constexpr (L >= 2) v = other(v, lane_xor<1>(__uint_as_float(v)));
+  if constexpr (L >= 4) v = other(v, lane_xor<2>(__uint_as_float(v)));
+  if constexpr (L >= 8) v = other(v, lane_xor<4>(__uint_as_float(v)));
+  if constexpr (L >= 16) v = other(v, lane_xor<8>(__uint_as_float(v)));
+  if constexpr (L >= 32) { float lo, hi; lane_pair<16>(__uint_as_float(v), &lo, &hi); v = other(__float_as_uint(lo), hi); }
+  if constexpr (L >= 64) { float lo, hi; lane_pair<32>(__uint_as_float(v), &lo, &hi); v = other(__float_as_uint(lo), hi); }
+  return v;
+}
+constexpr uint32_t kInf = 0x7f800000u;
+
+}  // namespace
+
+// L lanes per row (64 / L rows per wave) and W waves per row (W > 1: L = 64, a block
+// per row), R pieces of 8 channels per lane. Q: codes are wanted.
+template <typename TE, int L, int W, int R, bool Q>
+__global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
+  static_assert(W == 1 || (W == 4 && L == 64), "a block per row or whole rows per wave");
+  __shared__ float part[W];
+  __shared__ uint32_t part_bits[W];
+  __shared__ double part_top[W];
+  constexpr int RPB = 256 / (L * W);   // rows per block
+  const int VR = k.C / 8;
+  const int sub = W > 1 ? int(threadIdx.x) : int(threadIdx.x) & (L - 1);
+  constexpr int STEP = L * W;          // pieces between a lane's pieces
+  for (int64_t r0 = int64_t(blockIdx.x) * RPB; r0 < k.T; r0 += int64_t(gridDim.x) * RPB) {
+    const int64_t row = W > 1 ? r0 : r0 + int(threadIdx.x) / L;
+    const int nv = row < k.T ? VR : 0;
+    const int64_t base = row * k.C + 8 * sub;
+    Raw8<TE> x[R], r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (sub + STEP * i < nv) x[i] = raw_load(static_cast<const TE*>(k.x) + base + 8 * STEP * i);
+    if (k.r) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (sub + STEP * i < nv) r[i] = raw_load(static_cast<const TE*>(k.r) + base + 8 * STEP * i);
+    }
+    float h[R][8], g[R][8];
+    float s2 = 0.0f;
+    uint32_t tb = 0;   // bits of max |h gamma|
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (sub + STEP * i < nv) {
+        raw_get(x[i], h[i]);
+        if (k.r) {
+          float t[8];
+          raw_get(r[i], t);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[i][e] += t[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = 1.0f;
+        if (k.gamma) load8(k.gamma + 8 * (sub + STEP * i), g[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s2 = fmaf(h[i][e], h[i][e], s2);
+          if constexpr (Q) tb = max(tb, __float_as_uint(h[i][e] * g[i][e]) & 0x7fffffffu);
+        }
+      }
+    }
+    s2 = group_sum<L>(s2);
+    double top64 = 0.0;
+    if constexpr (Q) {
+      // the fp64 maximum of the wave's part of the row (W > 1) or of each row of the wave
+      const uint32_t wb = bits_max<L>(tb);
+      const float near = __uint_as_float(wb) * (1.0f - 0x1p-21f);
+      if (__uint_as_float(tb) >= near && tb > 0 && wb < kInf) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (sub + STEP * i >= nv) continue;
+          float xv[8], rv[8];
+          raw_get(x[i], xv);
+          if (k.r) raw_get(r[i], rv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (fabsf(h[i][e] * g[i][e]) >= near) {
+              const double v = (k.r ? double(xv[e]) + double(rv[e]) : double(xv[e])) * double(g[i][e]);
+              top64 = fmax(top64, fabs(v));
+            }
+          }
+        }
+      }
+      if constexpr (L == 64) {
+        top64 = few_max(top64, top64 > 0.0);
+      } else {
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) top64 = fmax(top64, __shfl_xor(top64, m, 64));
+      }
+      tb = wb;
+    }
+    if constexpr (W > 1) {
+      const int w = int(threadIdx.x) >> 6;
+      __syncthreads();   // the last row's values are read
+      if ((threadIdx.x & 63) == 0) {
+        part[w] = s2;
+        if constexpr (Q) {
+          part_bits[w] = tb;
+          part_top[w] = top64;
+        }
+      }
+      __syncthreads();
+      s2 = (part[0] + part[1]) + (part[2] + part[3]);
+      if constexpr (Q) {
+        tb = max(max(part_bits[0], part_bits[1]), max(part_bits[2], part_bits[3]));
+        top64 = fmax(fmax(part_top[0], part_top[1]), fmax(part_top[2], part_top[3]));
+      }
+    }
+    float rstd = 1.0f / sqrtf(s2 / float(k.C) + k.eps);
+    if (__any(s2 == INFINITY)) {
+      // squares past the largest float: once more, of h 2^-80 (the same branch for a
+      // whole block where a block has one row)
+      float z2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float z = h[i][e] * 0x1p-80f;
+          z2 = fmaf(z, z, z2);
+        }
+      }
+      z2 = group_sum<L>(z2);
+      if constexpr (W > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) part[int(threadIdx.x) >> 6] = z2;
+        __syncthreads();
+        z2 = (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 / float(k.C) + k.eps * 0x1p-80f * 0x1p-80f);
+    }
+    if (k.h) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (sub + STEP * i < nv) store8(static_cast<TE*>(k.h) + base + 8 * STEP * i, h[i]);
+    }
+    if (k.y) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (h[i][e] * rstd) * g[i][e];
+        if (k.y_bf16) store8(static_cast<uint16_t*>(k.y) + base + 8 * STEP * i, y);
+        else store8(static_cast<float*>(k.y) + base + 8 * STEP * i, y);
+      }
+    }
+    if constexpr (Q) {
+      const bool finite = tb < kInf;
+      const float top = __uint_as_float(tb);
+      const float rcp = finite && top >= kTiny ? 127.0f / top : 0.0f;
+      const float border = top < kTiny ? -1.0f : kBorder;   // tiny rows: all of them in fp64
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+        int q[8];
+        float far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = h[i][e] * g[i][e], n = rintf(v * rcp);
+          q[e] = int(n);
+          far = fmaxf(far, fabsf(fmaf(v, rcp, -n)));
+        }
+        if (finite && top > 0.0f && far > border) {
+          float xv[8], rv[8];
+          raw_get(x[i], xv);
+          if (k.r) raw_get(r[i], rv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = h[i][e] * g[i][e];
+            if (fabsf(fmaf(v, rcp, -rintf(v * rcp))) > border) {
+              const double v64 = (k.r ? double(xv[e]) + double(rv[e]) : double(xv[e])) * double(g[i][e]);
+              q[e] = int(rint(v64 / (top64 / 127.0)));
+            }
+          }
+        }
+        uint32_t d[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          d[e] = finite ? (uint32_t(q[4 * e]) & 255u) | (uint32_t(q[4 * e + 1]) & 255u) << 8 |
+                              (uint32_t(q[4 * e + 2]) & 255u) << 16 | uint32_t(q[4 * e + 3]) << 24
+                        : 0u;
+        *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) = make_uint2(d[0], d[1]);
+      }
+      if (sub == 0 && row < k.T) k.scales[row] = finite ? top / 127.0f * rstd : __uint_as_float(0x7fc00000u);
+    }
+  }
+}
+
+namespace {
+
+template <typename TE, int L, int W, int R>
+hipError_t launch_rms_form(const RmsArgs& a, hipStream_t s) {
+  constexpr int RPB = 256 / (L * W);
+  const int64_t blocks = std::min<int64_t>((a.T + RPB - 1) / RPB, 1 << 20);
+  if (a.codes)
+    hipLaunchKernelGGL((rms_kernel<TE, L, W, R, true>), dim3(unsigned(blocks)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((rms_kernel<TE, L, W, R, false>), dim3(unsigned(blocks)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename TE>
+hipError_t launch_rms_typed(const RmsArgs& a, hipStream_t s) {
+  const int v = a.C / 8;
+  if (v <= 8) return launch_rms_form<TE, 8, 1, 1>(a, s);
+  if (v <= 16) return launch_rms_form<TE, 16, 1, 1>(a, s);
+  if (v <= 32) return launch_rms_form<TE, 32, 1, 1>(a, s);
+  if (v <= 64) return launch_rms_form<TE, 64, 1, 1>(a, s);
+  if (v <= 128) return launch_rms_form<TE, 64, 1, 2>(a, s);
+  if (v <= 192) return launch_rms_form<TE, 64, 1, 3>(a, s);
+  if (v <= 256) return launch_rms_form<TE, 64, 1, 4>(a, s);
+  if (v <= 512) return launch_rms_form<TE, 64, 4, 2>(a, s);
+  if (v <= 768) return launch_rms_form<TE, 64, 4, 3>(a, s);
+  return launch_rms_form<TE, 64, 4, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const RmsArgs& a, hipStream_t s) {
+  return a.x_bf16 ? launch_rms_typed<uint16_t>(a, s) : launch_rms_typed<float>(a, s);
+}
+
+}  // namespace hq

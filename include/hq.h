@@ -430,6 +430,122 @@ typedef struct {
 int hq_group_norm_plan(const hq_norm_desc* desc, int64_t samples, int64_t positions,
                        hq_norm_plan* out);
 
+/* RMS norm descriptor: channels a multiple of 8 up to 8192; outputs any of
+ * HQ_RMS_* (at least one); x_dtype (X, residual, H) and y_dtype (Y) any
+ * hq_dtype; eps > 0. */
+typedef enum {
+  HQ_RMS_Y = 1,      /* the norm, in y_dtype                                    */
+  HQ_RMS_SUM = 2,    /* h = X + residual, in x_dtype                            */
+  HQ_RMS_CODES = 4   /* the norm as int8 codes with one scale per row           */
+} hq_rms_outputs;
+typedef struct {
+  int32_t channels, outputs, x_dtype, y_dtype;
+  float eps;
+} hq_rms_desc;
+
+/* Bookkeeping, host-only: check an RMS norm descriptor. */
+int hq_rms_validate(const hq_rms_desc* desc);
+
+/* Root-mean-square norm of the residual stream (Zhang and Sennrich, "Root Mean
+ * Square Layer Normalization", Eq. (4)) with the residual's addition before it,
+ * and its result quantised per row by HaTQ Sec. III-A Eq. (3) at 8 bits:
+ *   h = X + residual,  y = h gamma / sqrt(mean(h^2) + eps),
+ *   s = max_c |y_c| / 127,  code_c = round(y_c / s)   (half to even; s = 0: 0).
+ * The norm of a rotated row is the rotated norm, so in a network whose residual
+ * stream is kept in the Hadamard basis these codes are the ones that a layer of
+ * block = 1 and a_bits = 8 takes (hq_gemm_dequant; gamma may carry 1/sigma).
+ *  X [T, channels] x_dtype; residual the same or NULL (h = X); gamma f32
+ *  [channels] or NULL (ones); T up to 2^26; T = 0 is a no-op.
+ *  H [T, channels] x_dtype, Y [T, channels] y_dtype, codes int8 [T, channels] with
+ *  scales f32 [T]: those in desc->outputs are written, the others ignored.
+ * The norm and the codes are those of the unrounded h; sums are fp32, and codes are
+ * what 64-bit arithmetic gives them (scales are fp32). H may be X or residual, and Y
+ * may be X or residual where the types are the same; otherwise the outputs must not
+ * overlap an input or each other. Rows whose squares pass the largest float are normed
+ * like others; NaN and infinities stay in their row; a row with an h gamma that is not
+ * a finite float has codes of 0 and a NaN scale. */
+int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, const float* gamma,
+                int64_t T, void* H, void* Y, int8_t* codes, float* scales, void* stream);
+
+/* Rotary position descriptor.
+ *  q_heads, k_heads  heads at the start of each row: q_heads >= 0 of queries, then
+ *                    k_heads >= 0 of keys (at least one in all, up to 1024).
+ *  head_dim  channels of a head: a multiple of 8 up to 256.
+ *  axes      1 to 4; pairs[i] >= 0: the rotated pairs of axis i (consecutive pairs),
+ *            in all a multiple of 4, at least 4 and at most head_dim / 2 (channels
+ *            behind them are not rotated).
+ *  layout    HQ_ROPE_PAIRS: pair i is (2i, 2i + 1); HQ_ROPE_HALVES: (i, i + P), P the
+ *            pairs of all axes.
+ *  norm      1: an RMS norm of each head (eps > 0) before its rotation; 0: none.
+ *  inverse   1: the opposite rotation (the transposed map; norm must be 0).
+ *  pos_dtype HQ_POS_I32 or HQ_POS_F32.
+ *  x_dtype, y_dtype  any hq_dtype. */
+typedef enum { HQ_ROPE_PAIRS = 0, HQ_ROPE_HALVES = 1 } hq_rope_layout;
+typedef enum { HQ_POS_I32 = 0, HQ_POS_F32 = 1 } hq_pos_dtype;
+#define HQ_ROPE_MAX_AXES 4
+typedef struct {
+  int32_t q_heads, k_heads, head_dim, axes;
+  int32_t pairs[HQ_ROPE_MAX_AXES];
+  int32_t layout, norm, inverse, pos_dtype, x_dtype, y_dtype;
+  float eps;
+} hq_rope_desc;
+
+/* Bookkeeping, host-only: check a rotary position descriptor. */
+int hq_rope_validate(const hq_rope_desc* desc);
+
+/* Rotary positions (Su et al., "RoFormer: Enhanced Transformer with Rotary Position
+ * Embedding", Eq. (34)) with one position per axis, on the q and k heads of a packed
+ * projection (what a projection layer gives attention), behind an RMS norm of each
+ * head where desc->norm (Zhang and Sennrich, Eq. (4)):
+ *   n = x gamma / sqrt(mean(x^2) + eps)     (or n = x)
+ *   (a', b') = (a cos t - b sin t, b cos t + a sin t),  t = positions[row, axis(i)] freqs[i]
+ * for the channels (a, b) of pair i.
+ *  X [T, >= (q_heads + k_heads) head_dim] x_dtype with a row pitch of ldx elements,
+ *  Y the same in y_dtype with a pitch of ldy: multiples of 8. Only the q and k heads
+ *  are read and written. Y may be X itself (same pitch and type); otherwise the spans
+ *  of their rows must not overlap, nor Y those of the other inputs.
+ *  positions [T, axes] int32 or f32 (4-byte aligned); freqs f64 [pairs of all axes],
+ *  radians per position; gamma_q, gamma_k f32 [head_dim] or NULL (ones; must be NULL
+ *  without norm). T up to 2^26; T = 0 is a no-op.
+ * Angles are reduced to a turn in 64 bits; cos, sin and all else are fp32. A position
+ * that is not finite gives NaN in its row's rotated channels. */
+int hq_rope(const hq_rope_desc* desc, const void* X, int64_t ldx, const void* positions,
+            const double* freqs, const float* gamma_q, const float* gamma_k, int64_t T, void* Y,
+            int64_t ldy, void* stream);
+
+/* Adapter descriptor: d_in and d_out multiples of 8 up to 65536, rank a multiple of 8
+ * up to 128 (adapters of a smaller rank: rows of zeros in A); x_dtype (X) and w_dtype
+ * (A, B) the same hq_dtype; y_dtype (base, Y, residual, gate) any. */
+typedef struct {
+  int32_t d_in, d_out, rank, x_dtype, w_dtype, y_dtype;
+} hq_adapter_desc;
+
+/* Bookkeeping, host-only: check an adapter descriptor. */
+int hq_adapter_validate(const hq_adapter_desc* desc);
+
+/* Bookkeeping, host-only: workspace bytes hq_adapters needs for T rows; 0 if invalid. */
+size_t hq_adapters_workspace_bytes(const hq_adapter_desc* desc, int64_t T);
+
+/* Low-rank adapters of many requests beside a projection that they share (Hu et al.,
+ * "LoRA", Eq. (3), one adapter per row), behind hq_linear, hq_quant_linear or any
+ * other product that gave `base`:
+ *   V[t] = base[t] + scales[a] B_a (A_a X[t]),  a = ids[t],
+ * then the epilogue above: Y = residual + gate phi(V).
+ *  X [T, d_in] x_dtype; A [count, rank, d_in], B [count, d_out, rank] w_dtype (NULL
+ *  with count = 0); ids int32 [T] (4-byte aligned), any value outside 0 .. count - 1:
+ *  no adapter (V = base, and X[t] is not read); scales f32 [count] or NULL (ones);
+ *  base [T, d_out] y_dtype or NULL (zeros), possibly Y itself; Y [T, d_out] y_dtype;
+ *  epilogue NULL or as above; workspace at least hq_adapters_workspace_bytes(desc, T)
+ *  bytes (NULL when that is 0), not shared with a concurrent call. T up to 2^26; T = 0
+ *  is a no-op. Neither Y nor the workspace may overlap another operand or each other,
+ *  but for base and residual, either of which may be Y. The products are summed in
+ *  fp32 and A_a X[t] stays fp32 between them; the same inputs always give the same
+ *  bits. NaN and infinities stay in their row. */
+int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const void* B,
+                int32_t count, const int32_t* ids, const float* scales, const void* base, int64_t T,
+                const hq_epilogue* epilogue, void* Y, void* workspace, size_t workspace_bytes,
+                void* stream);
+
 /* ---- Stage entry points (the same kernels, for testing and profiling) ---- */
 
 /* Per-channel centring statistics (center = 2 only; T >= 1), the per-channel
