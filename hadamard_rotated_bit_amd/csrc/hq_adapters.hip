@@ -122,14 +122,26 @@ __device__ __forceinline__ v4f frag_mfma(const Frag<TE>& a, const Frag<TE>& b, v
     return mfma16(__uint_as_float(a.q.w), __uint_as_float(b.q.w), c);
   }
 }
+// 16 bytes at a uniform base and a lane's 32-bit offset (one address register).
+__device__ __forceinline__ uint4 load16(const void* base, uint32_t off) {
+  return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off);
+}
 template <typename TE>
-__device__ __forceinline__ Frag<TE> frag_load(const TE* p, bool ok) {
-  Frag<TE> f;
-  f.q = ok ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-  return f;
+__device__ __forceinline__ Raw8<TE> raw_at(const void* base, uint32_t off) {
+  Raw8<TE> r;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) r.q[i] = load16(base, off + 16 * i);
+  return r;
 }
 
-// The adapter of lane (lane % rows) of a tile from row r0, -1 where it has none.
+// A barrier that waits for LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The adapter of row r of a tile from row r0, -1 where it has none.
 __device__ __forceinline__ int tile_id(const AdaptArgs& k, int64_t r0, int r) {
   const int id = r0 + r < k.T ? k.ids[r0 + r] : -1;
   return uint32_t(id) < uint32_t(k.count) ? id : -1;
@@ -137,207 +149,330 @@ __device__ __forceinline__ int tile_id(const AdaptArgs& k, int64_t r0, int r) {
 
 }  // namespace
 
-// u of 16 MT rows: NW waves take the 64-k chunks of the rows and of A_a in turn, for each
-// adapter that the rows have; their sums are joined in LDS in wave order. RT: tiles of 16
-// rank indexes (RT 16 >= rank).
+// A_a x of 16 MT rows over one of `splits` parts of K, for each adapter that the rows
+// have, into u [splits, T, rank]. The part's chunks of 128 bytes a row go to NW waves in
+// turn. A wave loads a chunk of its rows of x and of A_a eight lanes a row (a fragment's
+// own order, 16 rows in consecutive lanes, costs the address unit four times as much),
+// passes it through its own part of the LDS (slot c ^ (r / 2) mod 8 of row r: 16 lanes
+// read 16 distinct positions of the 64 banks) and has the next chunk's loads in flight
+// meanwhile. The waves' sums are joined in LDS in wave order.
 template <typename TE, int MT, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
-  constexpr int ROWS = 16 * MT, STEPS = 64 / F::KS;
-  constexpr int RJ = RT < 2 ? RT : 2;   // tiles joined at a time
-  __shared__ float red[NW][ROWS][16 * RJ + 1];
-  const int lane = int(threadIdx.x) & 63, w = int(threadIdx.x) >> 6;
+  constexpr int ROWS = 16 * MT, LROWS = 16 * (MT + RT), UNITS = LROWS / 8;
+  constexpr int CK = 128 / sizeof(TE);   // k of a chunk
+  constexpr int RJ = RT < 2 ? RT : 2;    // rank tiles joined at a time
+  constexpr int RP = 16 * RJ + 1;
+  static_assert(NW * ROWS * RP * 4 <= NW * LROWS * 128, "the sums fit in the chunks' place");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NW * LROWS * 128];
+  const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int i = lane & 15, g = lane >> 4;
-  for (int64_t r0 = int64_t(blockIdx.x) * ROWS; r0 < k.T; r0 += int64_t(gridDim.x) * ROWS) {
-  const int id = lane < ROWS ? tile_id(k, r0, lane) : -1;
-  uint64_t left = __ballot(id >= 0);
-  while (left) {   // the same for every wave
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t match = __ballot(id == a);
-    left &= ~match;
-    const TE* x[MT];
-    const TE* ar[RT];
+  const int64_t tiles = (k.T + ROWS - 1) / ROWS;
+  const int chunks = (k.K + CK - 1) / CK;
+  const uint32_t ldb = uint32_t(k.K) * sizeof(TE);
+  uint8_t* const mine = smem + w * LROWS * 128;
+  const int urow = lane >> 3, piece = lane & 7;
+  for (int64_t job = blockIdx.x; job < tiles * k.splits; job += gridDim.x) {
+    const int64_t r0 = job % tiles * ROWS;
+    const int split = int(job / tiles);
+    const int c1 = int(int64_t(chunks) * (split + 1) / k.splits);
+    const int rows = int(min(k.T - r0, int64_t(ROWS)));
+    const uint8_t* const x = static_cast<const uint8_t*>(k.x) + r0 * ldb;
+    uint32_t off[UNITS];   // of the lane's rows of x and of A_a
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      x[m] = static_cast<const TE*>(k.x) + min(r0 + 16 * m + i, k.T - 1) * k.K + F::PER * g;
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      ar[t] = static_cast<const TE*>(k.a) + (int64_t(a) * k.rank + min(16 * t + i, k.rank - 1)) * k.K +
-              F::PER * g;
-    v4f acc[MT][RT] = {};
-    for (int c = 64 * w; c < k.K; c += 64 * NW) {
-      F fx[STEPS][MT], fa[STEPS][RT];
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int kk = c + F::KS * s;
-        const bool ok = kk + F::PER * g < k.K;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) fx[s][m] = frag_load<TE>(x[m] + kk, ok);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) fa[s][t] = frag_load<TE>(ar[t] + kk, ok);
-      }
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[m][t] = frag_mfma<TE>(fx[s][m], fa[s][t], acc[m][t]);
+    for (int n = 0; n < UNITS; ++n) {
+      const int r = 8 * n + urow;
+      off[n] = uint32_t(r < ROWS ? min(r, rows - 1) : min(r - ROWS, k.rank - 1)) * ldb + 16 * piece;
     }
-    const float scale = k.scales ? k.scales[a] : 1.0f;
+    const int id = lane < ROWS ? tile_id(k, r0, lane) : -1;
+    for (uint64_t left = __ballot(id >= 0); left;) {   // the same for every wave
+      const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      const uint64_t match = __ballot(id == a);
+      left &= ~match;
+      const uint8_t* const A = static_cast<const uint8_t*>(k.a) + int64_t(a) * k.rank * ldb;
+      uint4 st[UNITS];
+      auto load = [&](int c) {   // zeros past the end of a row
+        if (uint32_t(c + 1) * 128 <= ldb) {
 #pragma unroll
-    for (int t0 = 0; t0 < RT; t0 += RJ) {
-      __syncthreads();   // the last sums are read
+          for (int n = 0; n < UNITS; ++n) st[n] = load16((n < 2 * MT ? x : A) + c * 128, off[n]);
+        } else {
+          const bool ok = uint32_t(c) * 128 + 16 * piece < ldb;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < RJ; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) red[w][16 * m + 4 * g + e][16 * t + i] = acc[m][t0 + t][e];
-      __syncthreads();
-      for (int o = int(threadIdx.x); o < ROWS * 16 * RJ; o += 64 * NW) {
-        const int row = o / (16 * RJ), j = o - row * (16 * RJ);
-        float s = red[0][row][j];
-#pragma unroll
-        for (int n = 1; n < NW; ++n) s += red[n][row][j];
-        if (((match >> row) & 1) && 16 * t0 + j < k.rank)
-          k.u[(r0 + row) * k.rank + 16 * t0 + j] = s * scale;
-      }
-    }
-  }
-  }
-}
-
-// Y of 16 MT rows x 256 columns, 64 columns a wave. B_a's rows are the MFMA's rows, so a
-// lane ends with columns n .. n + 7 and n + 32 .. n + 39 of one row: MFMAs 2 p and 2 p + 1
-// take the columns 32 p + 8 (i / 4) + i % 4 and the four behind each. u enters a bf16
-// product as three bf16 parts (24 bits).
-template <typename TE, typename TY, int MT>
-__global__ __launch_bounds__(256) void adapt_up_tile_kernel(AdaptArgs k) {
-  using F = Frag<TE>;
-  constexpr int ROWS = 16 * MT, NP = sizeof(TE) == 2 ? 3 : 1;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int lane = int(threadIdx.x) & 63, w = int(threadIdx.x) >> 6;
-  const int i = lane & 15, g = lane >> 4;
-  const int nb = (k.N + 255) / 256;
-  const int steps = (k.rank + F::KS - 1) / F::KS;
-  const int pitch = steps * F::KS + F::PER;   // elements; 16 bytes past a row
-  TE* const us = reinterpret_cast<TE*>(smem);
-  for (int64_t tile = blockIdx.x; tile < (k.T + ROWS - 1) / ROWS * nb; tile += gridDim.x) {
-  const int64_t r0 = tile / nb * ROWS;
-  const int n0 = int(tile % nb) * 256 + 64 * w;
-  const int id = lane < ROWS ? tile_id(k, r0, lane) : -1;
-  uint64_t left = __ballot(id >= 0);
-  __syncthreads();   // the last tile's u is read
-  if (left) {
-    const int octs = steps * F::KS / 4;
-    for (int o = int(threadIdx.x); o < ROWS * octs; o += 256) {
-      const int row = o / octs, j = 4 * (o - row * octs);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (r0 + row < k.T && j < k.rank)
-        v = *reinterpret_cast<const float4*>(k.u + (r0 + row) * k.rank + j);
-      if constexpr (NP == 1) {
-        *reinterpret_cast<float4*>(us + row * pitch + j) = v;
-      } else {
-        float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const uint32_t a = pack_bf16x2(f[0], f[1]), b = pack_bf16x2(f[2], f[3]);
-          *reinterpret_cast<uint2*>(us + (p * ROWS + row) * pitch + j) = make_uint2(a, b);
-          f[0] -= __uint_as_float(a << 16);
-          f[1] -= __uint_as_float(a & 0xFFFF0000u);
-          f[2] -= __uint_as_float(b << 16);
-          f[3] -= __uint_as_float(b & 0xFFFF0000u);
+          for (int n = 0; n < UNITS; ++n)
+            st[n] = ok ? load16((n < 2 * MT ? x : A) + c * 128, off[n]) : make_uint4(0, 0, 0, 0);
         }
-      }
-    }
-  }
-  __syncthreads();
-  if (n0 >= k.N) continue;
-  // rows without an adapter first, then adapter by adapter
-  uint64_t match = __ballot(id < 0) & ((uint64_t(1) << (ROWS - 1) << 1) - 1);
-  int a = -1;
-  for (;;) {
-    if (match) {
-      v4f acc[MT][4] = {};
-      if (a >= 0) {
-        const TE* br[4];
+      };
+      v4f acc[MT][RT] = {};
+      int c = int(int64_t(chunks) * split / k.splits) + w;
+      if (c < c1) load(c);
+#pragma unroll 1
+      for (; c < c1; c += NW) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          br[t] = static_cast<const TE*>(k.b) +
-                  (int64_t(a) * k.N + min(n0 + 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3), k.N - 1)) * k.rank +
-                  F::PER * g;
-        for (int s = 0; s < steps; ++s) {
-          const bool ok = F::KS * s + F::PER * g < k.rank;
-          F fb[4];
+        for (int n = 0; n < UNITS; ++n) {
+          const int r = 8 * n + urow;
+          *reinterpret_cast<uint4*>(mine + r * 128 + 16 * (piece ^ ((r >> 1) & 7))) = st[n];
+        }
+        if (c + NW < c1) load(c + NW);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) fb[t] = frag_load<TE>(br[t] + F::KS * s, ok);
+        for (int s = 0; s < 2; ++s) {
+          F fx[MT], fa[RT];
+          const int slot = 16 * ((4 * s + g) ^ ((i >> 1) & 7));
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            fx[m].q = *reinterpret_cast<const uint4*>(mine + (16 * m + i) * 128 + slot);
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            fa[t].q = *reinterpret_cast<const uint4*>(mine + (ROWS + 16 * t + i) * 128 + slot);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              F fu;
-              fu.q = *reinterpret_cast<const uint4*>(us + (p * ROWS + 16 * m + i) * pitch + F::KS * s +
-                                                     F::PER * g);
-#pragma unroll
-              for (int t = 0; t < 4; ++t) acc[m][t] = frag_mfma<TE>(fb[t], fu, acc[m][t]);
-            }
+            for (int t = 0; t < RT; ++t) acc[m][t] = frag_mfma<TE>(fx[m], fa[t], acc[m][t]);
         }
       }
+      float* const red = reinterpret_cast<float*>(smem);   // [NW][ROWS][RP]
+      float* const u = k.u + int64_t(split) * k.T * k.rank;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const bool mine = (match >> (16 * m + i)) & 1;
-        const int64_t row = r0 + 16 * m + i;
-        float v[2][8];
-        int64_t mm[2], nn[2];
-        bool ok[2];
+      for (int t0 = 0; t0 < RT; t0 += RJ) {
+        lds_barrier();   // the chunks and the last sums are read
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          mm[p] = row;
-          nn[p] = n0 + 32 * p + 8 * g;
-          ok[p] = mine && row < k.T && nn[p] < k.N;
-          float b[8] = {};
-          if (k.base && ok[p]) load8(static_cast<const TY*>(k.base) + row * k.N + nn[p], b);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[p][e] = b[e] + acc[m][2 * p + (e >> 2)][e & 3];
+          for (int t = 0; t < RJ; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              red[(w * ROWS + 16 * m + 4 * g + e) * RP + 16 * t + i] = acc[m][t0 + t][e];
+        lds_barrier();
+#pragma unroll 1
+        for (int o = int(threadIdx.x); o < ROWS * 16 * RJ; o += 64 * NW) {
+          const int row = o / (16 * RJ), j = o - row * (16 * RJ);
+          float s = red[row * RP + j];
+#pragma unroll
+          for (int n = 1; n < NW; ++n) s += red[(n * ROWS + row) * RP + j];
+          if (((match >> row) & 1) && 16 * t0 + j < k.rank) u[(r0 + row) * k.rank + 16 * t0 + j] = s;
         }
-        finish8<TY, 2>(v, mm, nn, ok, k.N, k.ep);
+      }
+      lds_barrier();   // the sums are read
+    }
+  }
+}
+
+// Y of 64 rows x `slabs` slabs of 128 columns, 16 rows a wave. u of the rows, added over
+// its parts and scaled, goes to LDS (for bf16 products as three bf16 parts, 24 bits), then
+// a slab of B_a after the other through registers and LDS, its loads in flight during the
+// slab before. MFMA t has the columns 8 j + t on its lanes j, so that a lane ends with
+// eight consecutive columns of four rows, and 16 lanes with 256 bytes of a bf16 row: base,
+// residual and Y move in whole lines. SU: k-steps of the product.
+template <typename TE, typename TY, int SU>
+__global__ __launch_bounds__(256) void adapt_up_tile_kernel(AdaptArgs k) {
+  using F = Frag<TE>;
+  constexpr int NP = sizeof(TE) == 2 ? 3 : 1;
+  constexpr uint32_t ES = sizeof(TE), EY = sizeof(TY);
+  constexpr uint32_t PITCH = SU * 64 + 16;   // bytes of a row in LDS
+  constexpr int NB = 2 * SU;                 // 16-byte pieces of a slab per thread
+  __shared__ __attribute__((aligned(16))) uint8_t us[NP * 64 * PITCH];
+  __shared__ __attribute__((aligned(16))) uint8_t bs[128 * PITCH];
+  const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int groups = (k.N + 128 * k.slabs - 1) / (128 * k.slabs);
+  const int64_t tiles = (k.T + 63) / 64;
+  const uint32_t brow = uint32_t(k.rank) * ES;   // bytes of a row of B
+  const uint32_t ppr = brow / 16, npiece = 128 * ppr;
+  // row n of a slab is row (n mod 8) 16 + n / 8 in LDS: the 16 lanes of MFMA t read neighbours
+  uint32_t to[NB];
+#pragma unroll
+  for (int z = 0; z < NB; ++z) {
+    const uint32_t q = threadIdx.x + 256 * z, n = q / ppr;
+    to[z] = ((n & 7) * 16 + (n >> 3)) * PITCH + 16 * (q - n * ppr);
+  }
+  if (brow < SU * 64) {   // rank indexes past the last one
+    for (uint32_t o = threadIdx.x; o < 128 * PITCH / 16; o += 256)
+      reinterpret_cast<uint4*>(bs)[o] = make_uint4(0, 0, 0, 0);
+  }
+  for (int64_t job = blockIdx.x; job < tiles * groups; job += gridDim.x) {
+    const int64_t r0 = job / groups * 64;
+    const int s0 = int(job % groups) * k.slabs, s1 = min(s0 + k.slabs, (k.N + 127) / 128);
+    const int id = tile_id(k, r0, lane);
+    const uint64_t all = __ballot(id >= 0);
+    uint4 bq[NB];
+    auto load_b = [&](int slab, int a) {
+      const uint8_t* const B = static_cast<const uint8_t*>(k.b) + (int64_t(a) * k.N + 128 * slab) * brow;
+      const uint32_t most = min(npiece, uint32_t(k.N - 128 * slab) * ppr);
+#pragma unroll
+      for (int z = 0; z < NB; ++z)
+        if (threadIdx.x + 256 * z < most) bq[z] = load16(B, 16 * (threadIdx.x + 256 * z));
+    };
+    const int first = all ? __builtin_amdgcn_readlane(id, __builtin_ctzll(all)) : -1;
+    if (first >= 0) load_b(s0, first);
+    // the lane's rows 4 g + e of the wave's 16
+    const int64_t w0 = r0 + 16 * w;
+    const int wrows = int(min(k.T - w0, int64_t(16)));
+    const uint8_t* const base = static_cast<const uint8_t*>(k.base) + w0 * k.N * EY;
+    const uint8_t* const residual = static_cast<const uint8_t*>(k.ep.residual) + w0 * k.N * EY;
+    uint8_t* const Y = static_cast<uint8_t*>(k.ep.Y) + w0 * k.N * EY;
+    Raw8<TY> bb[4] = {};
+    auto load_base = [&](int slab) {
+      const uint32_t n = 128 * slab + 8 * i;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k.base && 4 * g + e < wrows && n < uint32_t(k.N))
+          bb[e] = raw_at<TY>(base, (uint32_t(4 * g + e) * k.N + n) * EY);
+    };
+    load_base(s0);
+    lds_barrier();   // the last tile's u is read
+    if (all) {
+      constexpr int Q = SU * F::KS / 4;
+      for (int o = int(threadIdx.x); o < 64 * Q; o += 256) {
+        const int row = o / Q, j = 4 * (o - row * Q);
+        const int a = tile_id(k, r0, row);
+        float f[4] = {};
+        if (a >= 0 && j < k.rank) {
+          const float* p = k.u + (r0 + row) * k.rank + j;
+          for (int n = 0; n < k.splits; ++n, p += k.T * k.rank) {
+            const float4 v = *reinterpret_cast<const float4*>(p);
+            f[0] += v.x; f[1] += v.y; f[2] += v.z; f[3] += v.w;
+          }
+          const float scale = k.scales ? k.scales[a] : 1.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] *= scale;
+        }
+        if constexpr (NP == 1) {
+          *reinterpret_cast<float4*>(us + row * PITCH + 4 * j) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const uint32_t lo = pack_bf16x2(f[0], f[1]), hi = pack_bf16x2(f[2], f[3]);
+            *reinterpret_cast<uint2*>(us + (p * 64 + row) * PITCH + 2 * j) = make_uint2(lo, hi);
+            f[0] -= __uint_as_float(lo << 16);
+            f[1] -= __uint_as_float(lo & 0xFFFF0000u);
+            f[2] -= __uint_as_float(hi << 16);
+            f[3] -= __uint_as_float(hi & 0xFFFF0000u);
+          }
+        }
       }
     }
-    if (!left) break;
-    a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    match = __ballot(id == a);
-    left &= ~match;
-  }
+#pragma unroll 1
+    for (int slab = s0; slab < s1; ++slab) {
+      v4f acc[8] = {};
+      for (uint64_t left = all; left;) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t match = __ballot(id == a);
+        left &= ~match;
+        lds_barrier();   // the last slab is read
+#pragma unroll
+        for (int z = 0; z < NB; ++z)
+          if (threadIdx.x + 256 * z < npiece) *reinterpret_cast<uint4*>(bs + to[z]) = bq[z];
+        lds_barrier();
+        if (left) load_b(slab, __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+        else if (slab + 1 < s1) load_b(slab + 1, first);
+        const uint32_t here = uint32_t(match >> (16 * w)) & 0xFFFFu;   // the wave's rows that have a
+        if (!here) continue;
+        v4f d[8] = {};
+#pragma unroll
+        for (int s = 0; s < SU; ++s) {
+          F fu[NP];
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            fu[p].q = *reinterpret_cast<const uint4*>(us + (p * 64 + 16 * w + i) * PITCH + 64 * s + 16 * g);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            F fb;
+            fb.q = *reinterpret_cast<const uint4*>(bs + (16 * t + i) * PITCH + 64 * s + 16 * g);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) d[t] = frag_mfma<TE>(fu[p], fb, d[t]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool has = (here >> (4 * g + e)) & 1;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) acc[t][e] = has ? d[t][e] : acc[t][e];
+        }
+      }
+      const uint32_t n = 128 * slab + 8 * i;
+      float v[4][8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        raw_get(bb[e], v[e]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[e][t] += acc[t][e];
+      }
+      if (slab + 1 < s1) load_base(slab + 1);
+      if (n >= uint32_t(k.N)) continue;
+      Raw8<TY> r[4], gt[4];
+      if (k.ep.residual) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * g + e < wrows) r[e] = raw_at<TY>(residual, (uint32_t(4 * g + e) * k.N + n) * EY);
+      }
+      if (k.ep.gate) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * g + e < wrows)
+            gt[e] = raw_load(static_cast<const TY*>(k.ep.gate) +
+                             int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld + n);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (4 * g + e >= wrows) continue;
+        float t[8];
+        apply_act<8, EY == 4>(v[e], k.ep.act);
+        if (k.ep.gate) {
+          raw_get(gt[e], t);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[e][x] *= t[x];
+        }
+        if (k.ep.residual) {
+          raw_get(r[e], t);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[e][x] += t[x];
+        }
+        store8(reinterpret_cast<TY*>(Y + (uint32_t(4 * g + e) * k.N + n) * EY), v[e]);
+      }
+    }
   }
 }
 
 namespace {
 
-template <typename TE, int RT>
-hipError_t launch_down_tiles(const AdaptArgs& a, hipStream_t s) {
-  constexpr int MT = 2, NW = 8;
-  const dim3 grid(unsigned(std::min<int64_t>((a.T + 16 * MT - 1) / (16 * MT), 1 << 20)));
-  hipLaunchKernelGGL((adapt_down_tile_kernel<TE, MT, RT, NW>), grid, dim3(64 * NW), 0, s, a);
+int down_splits(int64_t T, int K, int es) {
+  const int64_t tiles = (T + 31) / 32, chunks = (int64_t(K) * es + 127) / 128;
+  return int(std::max<int64_t>(1, std::min(256 / tiles, (chunks + 7) / 8)));
+}
+
+template <typename TE, int MT, int RT, int NW>
+hipError_t launch_down(const AdaptArgs& a, hipStream_t s) {
+  const int64_t jobs = (a.T + 16 * MT - 1) / (16 * MT) * a.splits;
+  hipLaunchKernelGGL((adapt_down_tile_kernel<TE, MT, RT, NW>),
+                     dim3(unsigned(std::min<int64_t>(jobs, 1 << 20))), dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+template <typename TE, typename TY, int SU>
+hipError_t launch_up(AdaptArgs a, hipStream_t s) {
+  const int64_t tiles = (a.T + 63) / 64, slabs = (a.N + 127) / 128;
+  a.slabs = int(std::max<int64_t>(1, std::min<int64_t>(8, tiles * slabs / 1024)));
+  const int64_t jobs = tiles * ((slabs + a.slabs - 1) / a.slabs);
+  hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>),
+                     dim3(unsigned(std::min<int64_t>(jobs, 1 << 20))), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <typename TE, typename TY>
-hipError_t launch_up_tiles(const AdaptArgs& a, hipStream_t s) {
-  constexpr int MT = 4, NP = sizeof(TE) == 2 ? 3 : 1;
-  const int64_t nb = (a.N + 255) / 256, tiles = (a.T + 16 * MT - 1) / (16 * MT);
+hipError_t launch_up_typed(const AdaptArgs& a, hipStream_t s) {
   const int steps = (a.rank + Frag<TE>::KS - 1) / Frag<TE>::KS;
-  const size_t lds = size_t(NP) * 16 * MT * size_t(steps * Frag<TE>::KS + Frag<TE>::PER) * sizeof(TE);
-  hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, MT>), dim3(unsigned(std::min<int64_t>(nb * tiles, 1 << 20))), dim3(256), lds, s, a);
-  return hipGetLastError();
+  if (steps <= 1) return launch_up<TE, TY, 1>(a, s);
+  if (steps <= 2) return launch_up<TE, TY, 2>(a, s);
+  if (steps <= 4) return launch_up<TE, TY, 4>(a, s);
+  if constexpr (sizeof(TE) == 4) return launch_up<TE, TY, 8>(a, s);
+  return hipErrorInvalidValue;
 }
 template <typename TE>
-hipError_t launch_tiles(const AdaptArgs& a, hipStream_t s) {
-  const int rt = (a.rank + 15) / 16;
-  const hipError_t e = rt <= 1   ? launch_down_tiles<TE, 1>(a, s)
-                       : rt <= 2 ? launch_down_tiles<TE, 2>(a, s)
-                       : rt <= 4 ? launch_down_tiles<TE, 4>(a, s)
-                                 : launch_down_tiles<TE, 8>(a, s);
+hipError_t launch_tiles(AdaptArgs a, hipStream_t s) {
+  a.splits = down_splits(a.T, a.K, int(sizeof(TE)));
+  const hipError_t e = a.rank <= 16   ? launch_down<TE, 2, 1, 8>(a, s)
+                       : a.rank <= 32 ? launch_down<TE, 2, 2, 8>(a, s)
+                       : a.rank <= 64 ? launch_down<TE, 2, 4, 8>(a, s)
+                                      : launch_down<TE, 2, 8, 4>(a, s);
   if (e != hipSuccess) return e;
-  return a.ep.y_bf16 ? launch_up_tiles<TE, uint16_t>(a, s) : launch_up_tiles<TE, float>(a, s);
+  return a.ep.y_bf16 ? launch_up_typed<TE, uint16_t>(a, s) : launch_up_typed<TE, float>(a, s);
 }
 
 template <typename TE>
@@ -353,10 +488,17 @@ hipError_t launch_adapters_typed(const AdaptArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t adapters_part_bytes(int64_t T, int rank) { return size_t(T) * size_t(rank) * 4; }
+namespace {
+constexpr int kRowsMost = 64;   // rows that are taken one by one
+}
+
+size_t adapters_part_bytes(int64_t T, int K, int rank, int esize) {
+  const int splits = T > kRowsMost ? down_splits(T, K, esize) : 1;
+  return size_t(splits) * size_t(T) * size_t(rank) * 4;
+}
 
 hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s) {
-  if (a.T > 64) return a.bf16 ? launch_tiles<uint16_t>(a, s) : launch_tiles<float>(a, s);
+  if (a.T > kRowsMost) return a.bf16 ? launch_tiles<uint16_t>(a, s) : launch_tiles<float>(a, s);
   return a.bf16 ? launch_adapters_typed<uint16_t>(a, s) : launch_adapters_typed<float>(a, s);
 }
 

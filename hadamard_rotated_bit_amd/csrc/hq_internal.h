@@ -247,10 +247,11 @@ struct AdaptArgs {
   float* u;
   int64_t T;
   int K, N, rank, count, bf16;
+  int splits, slabs;      // parts of K in u; slabs of columns per block (the launcher's)
   LinEpi ep;
 };
 constexpr int ADAPT_MAX_RANK = 128;
-size_t adapters_part_bytes(int64_t T, int rank);
+size_t adapters_part_bytes(int64_t T, int K, int rank, int esize);
 hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s);
 
 // Integer-only DH / WH layers with integer requantisation.
