@@ -7,6 +7,7 @@
 // Bound by memory: base is read and Y written once, x once, each adapter once per row or
 // tile that uses it (from the caches).
 #include "hq_epilogue.h"
+#include "hq_gemm_kernel.h"
 #include "hq_internal.h"
 
 #include <algorithm>
@@ -134,6 +135,20 @@ __device__ __forceinline__ Raw8<TE> raw_at(const void* base, uint32_t off) {
   return r;
 }
 
+constexpr uint32_t kOutside = 0x80000000u;   // an offset outside every descriptor here
+__device__ __forceinline__ uint4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, int(off), 0, 0));
+#else
+  return make_uint4(0, 0, 0, 0);
+#endif
+}
+__device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint4 v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), r, int(off), 0, 0);
+#endif
+}
+
 // A barrier that waits for LDS alone: loads from memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -167,14 +182,13 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[NW * LROWS * 128];
   const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int64_t tiles = (k.T + ROWS - 1) / ROWS;
   const int chunks = (k.K + CK - 1) / CK;
   const uint32_t ldb = uint32_t(k.K) * sizeof(TE);
   uint8_t* const mine = smem + w * LROWS * 128;
   const int urow = lane >> 3, piece = lane & 7;
-  for (int64_t job = blockIdx.x; job < tiles * k.splits; job += gridDim.x) {
-    const int64_t r0 = job % tiles * ROWS;
-    const int split = int(job / tiles);
+  {
+    const int64_t r0 = int64_t(blockIdx.x) * ROWS;
+    const int split = int(blockIdx.y);
     const int c1 = int(int64_t(chunks) * (split + 1) / k.splits);
     const int rows = int(min(k.T - r0, int64_t(ROWS)));
     const uint8_t* const x = static_cast<const uint8_t*>(k.x) + r0 * ldb;
@@ -203,16 +217,19 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
         }
       };
       v4f acc[MT][RT] = {};
-      int c = int(int64_t(chunks) * split / k.splits) + w;
-      if (c < c1) load(c);
+      const int c0 = int(int64_t(chunks) * split / k.splits) + w;
+      const int nc = c0 < c1 ? (c1 - c0 + NW - 1) / NW : 0;
+      int jc = nc ? int(blockIdx.x % unsigned(nc)) : 0;   // row tiles start apart
+      if (nc) load(c0 + NW * jc);
 #pragma unroll 1
-      for (; c < c1; c += NW) {
+      for (int n = 0; n < nc; ++n) {
+        jc = jc + 1 < nc ? jc + 1 : 0;
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
           const int r = 8 * n + urow;
           *reinterpret_cast<uint4*>(mine + r * 128 + 16 * (piece ^ ((r >> 1) & 7))) = st[n];
         }
-        if (c + NW < c1) load(c + NW);
+        if (n + 1 < nc) load(c0 + NW * jc);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           F fx[MT], fa[RT];
@@ -256,27 +273,69 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   }
 }
 
-// Y of 64 rows x `slabs` slabs of 128 columns, 16 rows a wave. u of the rows, added over
-// its parts and scaled, goes to LDS (for bf16 products as three bf16 parts, 24 bits), then
-// a slab of B_a after the other through registers and LDS, its loads in flight during the
-// slab before. MFMA t has the columns 8 j + t on its lanes j, so that a lane ends with
-// eight consecutive columns of four rows, and 16 lanes with 256 bytes of a bf16 row: base,
-// residual and Y move in whole lines. SU: k-steps of the product.
+// Y of 64 rows (block x) and every gridDim.y-th slab of 128 columns, 16 rows a wave. A wave
+// keeps its rows' u in registers, added over its parts and scaled (for bf16 products as
+// three bf16 parts, 24 bits). B_a goes slab by slab through registers and two buffers in
+// LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
+// lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
+// with 256 bytes of a bf16 row: base, residual and Y move in whole lines. SU: k-steps of
+// the product.
 template <typename TE, typename TY, int SU>
-__global__ __launch_bounds__(256) void adapt_up_tile_kernel(AdaptArgs k) {
+__global__ __launch_bounds__(256, 3) void adapt_up_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
   constexpr int NP = sizeof(TE) == 2 ? 3 : 1;
   constexpr uint32_t ES = sizeof(TE), EY = sizeof(TY);
   constexpr uint32_t PITCH = SU * 64 + 16;   // bytes of a row in LDS
   constexpr int NB = 2 * SU;                 // 16-byte pieces of a slab per thread
-  __shared__ __attribute__((aligned(16))) uint8_t us[NP * 64 * PITCH];
-  __shared__ __attribute__((aligned(16))) uint8_t bs[128 * PITCH];
+  __shared__ __attribute__((aligned(16))) uint8_t bs[2][128 * PITCH];
   const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int groups = (k.N + 128 * k.slabs - 1) / (128 * k.slabs);
-  const int64_t tiles = (k.T + 63) / 64;
+  const int64_t r0 = int64_t(blockIdx.x) * 64;
+  const int s0 = int(blockIdx.y), s1 = (k.N + 127) / 128, sd = int(gridDim.y);
   const uint32_t brow = uint32_t(k.rank) * ES;   // bytes of a row of B
   const uint32_t ppr = brow / 16, npiece = 128 * ppr;
+  const int id = tile_id(k, r0, lane);
+  const uint64_t all = __ballot(id >= 0);
+  // Memory is reached through buffer descriptors: what lies outside reads as zero and is
+  // not written, without a branch, so the waits count the loads and stores that follow.
+  // (slab, left): the next product; left has the tile's rows whose adapters are to come
+  auto next_of = [&](int& slab, uint64_t& left) {
+    left &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+    if (!left) {
+      left = all;
+      slab += sd;
+    }
+  };
+  uint4 bq[NB];
+  auto load_b = [&](int slab, uint64_t left) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const __amdgpu_buffer_rsrc_t B = make_rsrc(static_cast<const uint8_t*>(k.b) + int64_t(a) * k.N * brow,
+                                               slab < s1 ? int(k.N * brow) : 0);
+#pragma unroll
+    for (int z = 0; z < NB; ++z) {
+      const uint32_t q = threadIdx.x + 256 * z;
+      bq[z] = buf_load16(B, q < npiece ? 128 * slab * brow + 16 * q : kOutside);
+    }
+  };
+  // the lane's rows are 4 g + e of the wave's 16
+  const int64_t w0 = r0 + 16 * w;
+  const int wrows = int(max(min(k.T - w0, int64_t(16)), int64_t(0)));
+  const uint32_t inside = (1u << wrows) - 1;
+  const uint32_t rowb = uint32_t(k.N) * EY, at0 = 4 * g * rowb + 8 * i * EY;
+  const int span = int(wrows * rowb);
+  const __amdgpu_buffer_rsrc_t base = make_rsrc(static_cast<const uint8_t*>(k.base) + w0 * k.N * EY, k.base ? span : 0);
+  const __amdgpu_buffer_rsrc_t Y = make_rsrc(static_cast<const uint8_t*>(k.ep.Y) + w0 * k.N * EY, span);
+  constexpr int H = EY / 2;   // 16-byte halves of eight values
+  uint4 bb[4][H];
+  auto load_base = [&](int slab) {
+    const uint32_t at = 128 * slab + 8 * i < k.N ? at0 + 128 * slab * EY : kOutside;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int h = 0; h < H; ++h) bb[e][h] = buf_load16(base, at + e * rowb + 16 * h);
+  };
+  if (all) load_b(s0, all);
+  load_base(s0);
   // row n of a slab is row (n mod 8) 16 + n / 8 in LDS: the 16 lanes of MFMA t read neighbours
   uint32_t to[NB];
 #pragma unroll
@@ -285,150 +344,144 @@ __global__ __launch_bounds__(256) void adapt_up_tile_kernel(AdaptArgs k) {
     to[z] = ((n & 7) * 16 + (n >> 3)) * PITCH + 16 * (q - n * ppr);
   }
   if (brow < SU * 64) {   // rank indexes past the last one
-    for (uint32_t o = threadIdx.x; o < 128 * PITCH / 16; o += 256)
+    for (uint32_t o = threadIdx.x; o < 2 * 128 * PITCH / 16; o += 256)
       reinterpret_cast<uint4*>(bs)[o] = make_uint4(0, 0, 0, 0);
   }
-  for (int64_t job = blockIdx.x; job < tiles * groups; job += gridDim.x) {
-    const int64_t r0 = job / groups * 64;
-    const int s0 = int(job % groups) * k.slabs, s1 = min(s0 + k.slabs, (k.N + 127) / 128);
-    const int id = tile_id(k, r0, lane);
-    const uint64_t all = __ballot(id >= 0);
-    uint4 bq[NB];
-    auto load_b = [&](int slab, int a) {
-      const uint8_t* const B = static_cast<const uint8_t*>(k.b) + (int64_t(a) * k.N + 128 * slab) * brow;
-      const uint32_t most = min(npiece, uint32_t(k.N - 128 * slab) * ppr);
+  F fu[SU][NP] = {};   // row i's u, rank indexes KS s + PER g ..
+  {
+    const int a = __shfl(id, 16 * w + i, 64);
+    const float scale = a >= 0 && k.scales ? k.scales[a] : 1.0f;
+    const float* const p = k.u + (w0 + i) * k.rank + F::PER * g;
 #pragma unroll
-      for (int z = 0; z < NB; ++z)
-        if (threadIdx.x + 256 * z < most) bq[z] = load16(B, 16 * (threadIdx.x + 256 * z));
-    };
-    const int first = all ? __builtin_amdgcn_readlane(id, __builtin_ctzll(all)) : -1;
-    if (first >= 0) load_b(s0, first);
-    // the lane's rows 4 g + e of the wave's 16
-    const int64_t w0 = r0 + 16 * w;
-    const int wrows = int(min(k.T - w0, int64_t(16)));
-    const uint8_t* const base = static_cast<const uint8_t*>(k.base) + w0 * k.N * EY;
-    const uint8_t* const residual = static_cast<const uint8_t*>(k.ep.residual) + w0 * k.N * EY;
-    uint8_t* const Y = static_cast<uint8_t*>(k.ep.Y) + w0 * k.N * EY;
-    Raw8<TY> bb[4] = {};
-    auto load_base = [&](int slab) {
-      const uint32_t n = 128 * slab + 8 * i;
+    for (int s = 0; s < SU; ++s) {
+      if (a < 0 || F::KS * s + F::PER * g >= k.rank) continue;
+      float f[F::PER] = {};
+      for (int n = 0; n < k.splits; ++n) {
+        const float4* const q = reinterpret_cast<const float4*>(p + F::KS * s + n * k.T * k.rank);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (k.base && 4 * g + e < wrows && n < uint32_t(k.N))
-          bb[e] = raw_at<TY>(base, (uint32_t(4 * g + e) * k.N + n) * EY);
-    };
-    load_base(s0);
-    lds_barrier();   // the last tile's u is read
-    if (all) {
-      constexpr int Q = SU * F::KS / 4;
-      for (int o = int(threadIdx.x); o < 64 * Q; o += 256) {
-        const int row = o / Q, j = 4 * (o - row * Q);
-        const int a = tile_id(k, r0, row);
-        float f[4] = {};
-        if (a >= 0 && j < k.rank) {
-          const float* p = k.u + (r0 + row) * k.rank + j;
-          for (int n = 0; n < k.splits; ++n, p += k.T * k.rank) {
-            const float4 v = *reinterpret_cast<const float4*>(p);
-            f[0] += v.x; f[1] += v.y; f[2] += v.z; f[3] += v.w;
-          }
-          const float scale = k.scales ? k.scales[a] : 1.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] *= scale;
+        for (int h = 0; h < F::PER / 4; ++h) {
+          f[4 * h] += q[h].x; f[4 * h + 1] += q[h].y; f[4 * h + 2] += q[h].z; f[4 * h + 3] += q[h].w;
         }
-        if constexpr (NP == 1) {
-          *reinterpret_cast<float4*>(us + row * PITCH + 4 * j) = make_float4(f[0], f[1], f[2], f[3]);
-        } else {
+      }
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const uint32_t lo = pack_bf16x2(f[0], f[1]), hi = pack_bf16x2(f[2], f[3]);
-            *reinterpret_cast<uint2*>(us + (p * 64 + row) * PITCH + 2 * j) = make_uint2(lo, hi);
-            f[0] -= __uint_as_float(lo << 16);
-            f[1] -= __uint_as_float(lo & 0xFFFF0000u);
-            f[2] -= __uint_as_float(hi << 16);
-            f[3] -= __uint_as_float(hi & 0xFFFF0000u);
+      for (int e = 0; e < F::PER; ++e) f[e] *= scale;
+      if constexpr (NP == 1) {
+        fu[s][0].q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      } else {
+#pragma unroll
+        for (int p3 = 0; p3 < NP; ++p3) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            f[2 * e] -= __uint_as_float(h[e] << 16);
+            f[2 * e + 1] -= __uint_as_float(h[e] & 0xFFFF0000u);
           }
+          fu[s][p3].q = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
     }
+  }
+  // Y of row 4 g + e of the wave in a slab, from v = base + what the adapter adds, where ok
+  auto finish = [&](float (&v)[8], int e, int slab, bool ok) {
+    uint32_t at = at0;
+    asm volatile("" : "+v"(at));   // addresses made here, not kept over the slabs
+    at += e * rowb + 128 * slab * EY;
+    ok = ok && 128 * slab + 8 * i < k.N;
+    float t[8];
+    apply_act<8, EY == 4>(v, k.ep.act);
+    if (k.ep.gate) {
+      if (ok) raw_get(raw_load(static_cast<const TY*>(k.ep.gate) + 128 * slab + 8 * i +
+                               int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld), t);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] *= t[x];
+    }
+    if (k.ep.residual) {
+      if (ok) raw_get(raw_at<TY>(static_cast<const uint8_t*>(k.ep.residual) + w0 * k.N * EY, at), t);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] += t[x];
+    }
+    if (!ok) at = kOutside;
+    if constexpr (EY == 2) {
+      buf_store16(Y, at, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        buf_store16(Y, at + 16 * h, make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])));
+    }
+  };
+  auto base_of = [&](int e, float (&v)[8]) {
+    Raw8<TY> r;
+#pragma unroll
+    for (int h = 0; h < H; ++h) r.q[h] = bb[e][h];
+    raw_get(r, v);
+  };
+  const uint32_t none = uint32_t(~all >> (16 * w)) & inside;   // rows without an adapter
+  if (none) {
 #pragma unroll 1
-    for (int slab = s0; slab < s1; ++slab) {
-      v4f acc[8] = {};
-      for (uint64_t left = all; left;) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const uint64_t match = __ballot(id == a);
-        left &= ~match;
-        lds_barrier();   // the last slab is read
-#pragma unroll
-        for (int z = 0; z < NB; ++z)
-          if (threadIdx.x + 256 * z < npiece) *reinterpret_cast<uint4*>(bs + to[z]) = bq[z];
-        lds_barrier();
-        if (left) load_b(slab, __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
-        else if (slab + 1 < s1) load_b(slab + 1, first);
-        const uint32_t here = uint32_t(match >> (16 * w)) & 0xFFFFu;   // the wave's rows that have a
-        if (!here) continue;
-        v4f d[8] = {};
-#pragma unroll
-        for (int s = 0; s < SU; ++s) {
-          F fu[NP];
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            fu[p].q = *reinterpret_cast<const uint4*>(us + (p * 64 + 16 * w + i) * PITCH + 64 * s + 16 * g);
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            F fb;
-            fb.q = *reinterpret_cast<const uint4*>(bs + (16 * t + i) * PITCH + 64 * s + 16 * g);
-#pragma unroll
-            for (int p = 0; p < NP; ++p) d[t] = frag_mfma<TE>(fu[p], fb, d[t]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool has = (here >> (4 * g + e)) & 1;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) acc[t][e] = has ? d[t][e] : acc[t][e];
-        }
-      }
-      const uint32_t n = 128 * slab + 8 * i;
-      float v[4][8];
+    for (int slab = s0; slab < s1; slab += sd) {
+      if (slab > s0) load_base(slab);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        raw_get(bb[e], v[e]);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[e][t] += acc[t][e];
-      }
-      if (slab + 1 < s1) load_base(slab + 1);
-      if (n >= uint32_t(k.N)) continue;
-      Raw8<TY> r[4], gt[4];
-      if (k.ep.residual) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (4 * g + e < wrows) r[e] = raw_at<TY>(residual, (uint32_t(4 * g + e) * k.N + n) * EY);
-      }
-      if (k.ep.gate) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (4 * g + e < wrows)
-            gt[e] = raw_load(static_cast<const TY*>(k.ep.gate) +
-                             int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld + n);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (4 * g + e >= wrows) continue;
-        float t[8];
-        apply_act<8, EY == 4>(v[e], k.ep.act);
-        if (k.ep.gate) {
-          raw_get(gt[e], t);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[e][x] *= t[x];
-        }
-        if (k.ep.residual) {
-          raw_get(r[e], t);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[e][x] += t[x];
-        }
-        store8(reinterpret_cast<TY*>(Y + (uint32_t(4 * g + e) * k.N + n) * EY), v[e]);
+        float v[8];
+        base_of(e, v);
+        finish(v, e, slab, (none >> (4 * g + e)) & 1);
       }
     }
+    if (all) load_base(s0);
+  }
+  if (!all) return;
+  auto store_b = [&](int buf) {
+#pragma unroll
+    for (int z = 0; z < NB; ++z)
+      if (threadIdx.x + 256 * z < npiece) *reinterpret_cast<uint4*>(bs[buf] + to[z]) = bq[z];
+  };
+  if (brow < SU * 64) lds_barrier();
+  store_b(0);
+  int slab = s0, bslab = s0, buf = 0;
+  uint64_t left = all, bleft = all;   // the product that is computed, the one that is loaded
+  next_of(bslab, bleft);
+  load_b(bslab, bleft);
+  lds_barrier();
+#pragma unroll 1
+  while (slab < s1) {
+    store_b(buf ^ 1);
+    next_of(bslab, bleft);
+    load_b(bslab, bleft);
+    const uint64_t match = __ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+    const uint32_t here = uint32_t(match >> (16 * w)) & inside;   // the wave's rows that have it
+    v4f d[8] = {};
+#pragma unroll
+    for (int s = 0; s < SU; ++s) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        F fb;
+        fb.q = *reinterpret_cast<const uint4*>(bs[buf] + (16 * t + i) * PITCH + 64 * s + 16 * g);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) d[t] = frag_mfma<TE>(fu[s][p], fb, d[t]);
+        if ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // four reads ahead, no more registers
+      }
+    }
+    float v[4][8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      base_of(e, v[e]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        v[e][x] += d[x][e];
+        asm volatile("" : "+v"(v[e][x]));   // single registers from here, not the MFMA's fours
+      }
+    }
+    const int was = slab;
+    next_of(slab, left);
+    load_base(slab);   // past the last slab nothing is read
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      finish(v[e], e, was, (here >> (4 * g + e)) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    lds_barrier();   // this product is read, the next one written
+    buf ^= 1;
   }
 }
 
@@ -441,18 +494,16 @@ int down_splits(int64_t T, int K, int es) {
 
 template <typename TE, int MT, int RT, int NW>
 hipError_t launch_down(const AdaptArgs& a, hipStream_t s) {
-  const int64_t jobs = (a.T + 16 * MT - 1) / (16 * MT) * a.splits;
-  hipLaunchKernelGGL((adapt_down_tile_kernel<TE, MT, RT, NW>),
-                     dim3(unsigned(std::min<int64_t>(jobs, 1 << 20))), dim3(64 * NW), 0, s, a);
+  const dim3 grid(unsigned((a.T + 16 * MT - 1) / (16 * MT)), unsigned(a.splits));
+  hipLaunchKernelGGL((adapt_down_tile_kernel<TE, MT, RT, NW>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 template <typename TE, typename TY, int SU>
 hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t tiles = (a.T + 63) / 64, slabs = (a.N + 127) / 128;
   a.slabs = int(std::max<int64_t>(1, std::min<int64_t>(8, tiles * slabs / 1024)));
-  const int64_t jobs = tiles * ((slabs + a.slabs - 1) / a.slabs);
-  hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>),
-                     dim3(unsigned(std::min<int64_t>(jobs, 1 << 20))), dim3(256), 0, s, a);
+  const dim3 grid(unsigned(tiles), unsigned((slabs + a.slabs - 1) / a.slabs));
+  hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <typename TE, typename TY>
