@@ -156,6 +156,12 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// The row tile of block x: block b runs on XCD b mod 8, and the tiles of one XCD are
+// neighbours, which share an adapter where rows come in runs (grid: a multiple of 8).
+__device__ __forceinline__ int64_t tile_of_block() {
+  return int64_t(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+}
+
 // The adapter of row r of a tile from row r0, -1 where it has none.
 __device__ __forceinline__ int tile_id(const AdaptArgs& k, int64_t r0, int r) {
   const int id = r0 + r < k.T ? k.ids[r0 + r] : -1;
@@ -187,7 +193,8 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   uint8_t* const mine = smem + w * LROWS * 128;
   const int urow = lane >> 3, piece = lane & 7;
   {
-    const int64_t r0 = int64_t(blockIdx.x) * ROWS;
+    const int64_t r0 = tile_of_block() * ROWS;
+    if (r0 >= k.T) return;
     const int split = int(blockIdx.y);
     const int c1 = int(int64_t(chunks) * (split + 1) / k.splits);
     const int rows = int(min(k.T - r0, int64_t(ROWS)));
@@ -290,7 +297,8 @@ __global__ __launch_bounds__(256, 3) void adapt_up_tile_kernel(AdaptArgs k) {
   __shared__ __attribute__((aligned(16))) uint8_t bs[2][128 * PITCH];
   const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int64_t r0 = int64_t(blockIdx.x) * 64;
+  const int64_t r0 = tile_of_block() * 64;
+  if (r0 >= k.T) return;
   const int s0 = int(blockIdx.y), s1 = (k.N + 127) / 128, sd = int(gridDim.y);
   const uint32_t brow = uint32_t(k.rank) * ES;   // bytes of a row of B
   const uint32_t ppr = brow / 16, npiece = 128 * ppr;
@@ -494,7 +502,7 @@ int down_splits(int64_t T, int K, int es) {
 
 template <typename TE, int MT, int RT, int NW>
 hipError_t launch_down(const AdaptArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned((a.T + 16 * MT - 1) / (16 * MT)), unsigned(a.splits));
+  const dim3 grid(unsigned((a.T + 16 * MT - 1) / (16 * MT) + 7) / 8 * 8, unsigned(a.splits));
   hipLaunchKernelGGL((adapt_down_tile_kernel<TE, MT, RT, NW>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
@@ -502,7 +510,7 @@ template <typename TE, typename TY, int SU>
 hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t tiles = (a.T + 63) / 64, slabs = (a.N + 127) / 128;
   a.slabs = int(std::max<int64_t>(1, std::min<int64_t>(8, tiles * slabs / 1024)));
-  const dim3 grid(unsigned(tiles), unsigned((slabs + a.slabs - 1) / a.slabs));
+  const dim3 grid(unsigned(tiles + 7) / 8 * 8, unsigned((slabs + a.slabs - 1) / a.slabs));
   hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
