@@ -1296,7 +1296,8 @@ int hq_adapter_validate(const hq_adapter_desc* desc) {
 size_t hq_adapters_workspace_bytes(const hq_adapter_desc* desc, int64_t T) {
   g_err.clear();
   if (check_adapter_desc(desc) != HQ_OK || check_rows(T) != HQ_OK) return 0;
-  return align256(hq::adapters_part_bytes(T, desc->d_in, desc->rank, int(dtype_size(desc->x_dtype))));
+  return align256(hq::adapters_part_bytes(T, desc->d_in, desc->d_out, desc->rank,
+                                             int(dtype_size(desc->x_dtype))));
 }
 
 int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const void* B,
@@ -1328,7 +1329,7 @@ int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const
   hq::AdaptArgs k = {};
   st = check_epilogue(epilogue, T, desc->d_out, desc->y_dtype, Y, &k.ep);
   if (st != HQ_OK) return st;
-  const size_t need = align256(hq::adapters_part_bytes(T, desc->d_in, desc->rank, int(es)));
+  const size_t need = align256(hq::adapters_part_bytes(T, desc->d_in, desc->d_out, desc->rank, int(es)));
   if (need && (!workspace || workspace_bytes < need))
     return fail(HQ_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
                 workspace ? workspace_bytes : size_t(0), need);

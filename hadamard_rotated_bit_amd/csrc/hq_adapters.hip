@@ -14,66 +14,143 @@
 
 namespace hq {
 
-// ---- row by row ---------------------------------------------------------------
+namespace {
 
-// u[t, j] = s_a sum_k x[t, k] A_a[j, k]: a wave per row and rank index.
+// 16 bytes at a uniform base and a lane's 32-bit offset (one address register).
+__device__ __forceinline__ uint4 load16(const void* base, uint32_t off) {
+  return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off);
+}
 template <typename TE>
-__global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs k) {
-  const int lane = int(threadIdx.x) & 63;
-  for (int64_t job = int64_t(blockIdx.x) * 4 + (int(threadIdx.x) >> 6); job < k.T * k.rank;
-       job += int64_t(gridDim.x) * 4) {
-  const int64_t t = job / k.rank;
-  const int j = int(job - t * k.rank);
-  const int id = k.ids[t];
-  if (uint32_t(id) >= uint32_t(k.count)) continue;
-  const TE* const x = static_cast<const TE*>(k.x) + t * k.K;
-  const TE* const a = static_cast<const TE*>(k.a) + (int64_t(id) * k.rank + j) * k.K;
-  float s = 0.0f;
-  for (int c = 8 * lane; c < k.K; c += 512) {
-    float p[8], q[8];
-    load8(x + c, p);
-    load8(a + c, q);
+__device__ __forceinline__ Raw8<TE> raw_at(const void* base, uint32_t off) {
+  Raw8<TE> r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
-  }
-  s = group_sum<64>(s);
-  if (lane == 0) k.u[t * k.rank + j] = k.scales ? s * k.scales[id] : s;
+  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) r.q[i] = load16(base, off + 16 * i);
+  return r;
+}
+
+// The elements of 16 bytes as floats.
+template <typename TE>
+__device__ __forceinline__ void get16(const uint4& q, float* v) {
+  if constexpr (sizeof(TE) == 2) {
+    load8(reinterpret_cast<const uint16_t*>(&q), v);
+  } else {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
   }
 }
 
-// Y[t, n .. n + 7] from base and u: a lane per 8 columns of a row.
-template <typename TE>
-__global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs k) {
-  const int per = k.N / 8;
-  for (int64_t job = int64_t(blockIdx.x) * 256 + threadIdx.x; job < k.T * per;
-       job += int64_t(gridDim.x) * 256) {
-  const int64_t t = job / per;
-  const int n = 8 * int(job - t * per);
-  float v[8] = {};
-  if (k.base) {
-    if (k.ep.y_bf16) load8(static_cast<const uint16_t*>(k.base) + t * k.N + n, v);
-    else load8(static_cast<const float*>(k.base) + t * k.N + n, v);
+}  // namespace
+
+// ---- row by row ---------------------------------------------------------------
+
+
+// Y of one row (block x) and a part of its columns (block y; each part takes the row's u
+// for itself: one launch). Eight waves share the rank indexes of u, JW each, all their
+// loads of U strips of K in flight; then 64 columns a wave at a time: B_a's rows pass
+// through the wave's own LDS, read in whole lines, so that each lane has a column.
+// 24 rows of 4096 -> 4096 rank 16: see the launcher.
+template <typename TE, int JW, int U>
+__global__ __launch_bounds__(512) void adapt_rows_kernel(AdaptArgs k) {
+  constexpr int PER = 16 / sizeof(TE);             // elements of 16 bytes
+  constexpr int SP = JW * int(sizeof(TE)) / 2 < 8 ? JW * int(sizeof(TE)) / 2 : 8;
+  constexpr int PITCH = 16 * SP + 16;              // SP pieces of a column's row in LDS
+  __shared__ __attribute__((aligned(16))) float u[8 * JW];
+  __shared__ __attribute__((aligned(16))) uint8_t bs[8][64 * PITCH];
+  const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int64_t t = blockIdx.x;
+  const int id = __builtin_amdgcn_readfirstlane(k.ids[t]);
+  const bool has = uint32_t(id) < uint32_t(k.count);
+  // the wave's first columns are on their way while u is made, the next ones while they are
+  // multiplied
+  const uint32_t brow = uint32_t(k.rank) * sizeof(TE), ppr = brow / 16;
+  const int units = (k.N + 63) / 64;
+  const int u1 = int(int64_t(units) * (blockIdx.y + 1) / gridDim.y);
+  int n0 = int(int64_t(units) * blockIdx.y / gridDim.y) + w;
+  uint4 q[SP];
+  auto load_b = [&](int unit, uint32_t z0) {   // SP pieces from z0 of 64 columns' rows
+    const uint8_t* const B = static_cast<const uint8_t*>(k.b) + (int64_t(id) * k.N + 64 * unit) * brow;
+    const uint32_t sp = min(ppr - z0, uint32_t(SP)), most = uint32_t(min(64, k.N - 64 * unit)) * sp;
+#pragma unroll
+    for (int z = 0; z < SP; ++z) {
+      const uint32_t o = lane + 64 * z, r = o / sp;
+      if (o < most) q[z] = load16(B, r * brow + 16 * (z0 + o - r * sp));
+    }
+  };
+  auto load_base = [&](int unit) {
+    const int n = 64 * unit + lane;
+    if (!k.base || n >= k.N) return 0.0f;
+    return k.ep.y_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(k.base)[t * k.N + n])
+                       : static_cast<const float*>(k.base)[t * k.N + n];
+  };
+  float base = 0.0f;
+  if (n0 < u1) {
+    base = load_base(n0);
+    if (has) load_b(n0, 0);
   }
-  const int id = k.ids[t];
-  if (uint32_t(id) < uint32_t(k.count)) {
-    const TE* const b = static_cast<const TE*>(k.b) + (int64_t(id) * k.N + n) * k.rank;
-    const float* const u = k.u + t * k.rank;
-    float d[8] = {};
-    for (int j = 0; j < k.rank; j += 8) {
-      float p[8];
-      load8(u + j, p);
+  if (has) {
+    const TE* const x = static_cast<const TE*>(k.x) + t * k.K;
+    const TE* const A = static_cast<const TE*>(k.a) + int64_t(id) * k.rank * k.K;
+    float s[JW] = {};
+    uint32_t row[JW];   // rank indexes w, w + 8, ...; past the last one it again
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float q[8];
-        load8(b + e * k.rank + j, q);
+    for (int j = 0; j < JW; ++j) row[j] = uint32_t(min(w + 8 * j, k.rank - 1)) * uint32_t(k.K);
+#pragma unroll 1
+    for (int c = PER * lane; c < k.K; c += 64 * PER * U) {
+      uint4 xq[U], aq[U][JW];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[e] = fmaf(p[i], q[i], d[e]);
+      for (int n = 0; n < U; ++n) {
+        const int cc = c + 64 * PER * n;
+        if (cc >= k.K) continue;
+        xq[n] = load16(x, uint32_t(cc) * sizeof(TE));
+#pragma unroll
+        for (int j = 0; j < JW; ++j) aq[n][j] = load16(A, (row[j] + cc) * uint32_t(sizeof(TE)));
+      }
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        if (c + 64 * PER * n >= k.K) continue;
+        float p[PER], q[PER];
+        get16<TE>(xq[n], p);
+#pragma unroll
+        for (int j = 0; j < JW; ++j) {
+          get16<TE>(aq[n][j], q);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) s[j] = fmaf(p[e], q[e], s[j]);
+        }
       }
     }
+    const float scale = k.scales ? k.scales[id] : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += d[e];
+    for (int j = 0; j < JW; ++j) {
+      const float v = group_sum<64>(s[j]) * scale;
+      if (lane == 0 && w + 8 * j < k.rank) u[w + 8 * j] = v;
+    }
   }
-  finish_piece(v, t, n, k.N, k.ep);
+  __syncthreads();
+  for (; n0 < u1; n0 += 8) {
+    const int n = 64 * n0 + lane;
+    const float b0 = base;
+    float d = 0.0f;
+    if (n0 + 8 < u1) base = load_base(n0 + 8);
+    if (has) {
+#pragma unroll 1
+      for (uint32_t z0 = 0; z0 < ppr; z0 += SP) {
+        const uint32_t sp = min(ppr - z0, uint32_t(SP));
+#pragma unroll
+        for (int z = 0; z < SP; ++z) {
+          const uint32_t o = lane + 64 * z, r = o / sp;
+          if (o < 64 * sp) *reinterpret_cast<uint4*>(bs[w] + r * PITCH + 16 * (o - r * sp)) = q[z];
+        }
+        if (z0 + SP < ppr) load_b(n0, z0 + SP);
+        else if (n0 + 8 < u1) load_b(n0 + 8, 0);
+        for (uint32_t z = 0; z < sp; ++z) {
+          float b[PER];
+          get16<TE>(*reinterpret_cast<const uint4*>(bs[w] + lane * PITCH + 16 * z), b);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) d = fmaf(b[e], u[PER * (z0 + z) + e], d);
+        }
+      }
+    }
+    if (n < k.N) finish1(b0 + d, t, n, k.N, k.ep);
   }
 }
 
@@ -123,18 +200,6 @@ __device__ __forceinline__ v4f frag_mfma(const Frag<TE>& a, const Frag<TE>& b, v
     return mfma16(__uint_as_float(a.q.w), __uint_as_float(b.q.w), c);
   }
 }
-// 16 bytes at a uniform base and a lane's 32-bit offset (one address register).
-__device__ __forceinline__ uint4 load16(const void* base, uint32_t off) {
-  return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off);
-}
-template <typename TE>
-__device__ __forceinline__ Raw8<TE> raw_at(const void* base, uint32_t off) {
-  Raw8<TE> r;
-#pragma unroll
-  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) r.q[i] = load16(base, off + 16 * i);
-  return r;
-}
-
 constexpr uint32_t kOutside = 0x80000000u;   // an offset outside every descriptor here
 __device__ __forceinline__ uint4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -534,31 +599,48 @@ hipError_t launch_tiles(AdaptArgs a, hipStream_t s) {
   return a.ep.y_bf16 ? launch_up_typed<TE, uint16_t>(a, s) : launch_up_typed<TE, float>(a, s);
 }
 
-template <typename TE>
-hipError_t launch_adapters_typed(const AdaptArgs& a, hipStream_t s) {
-  const int64_t down = std::min<int64_t>((a.T * a.rank + 3) / 4, 1 << 20);
-  const int64_t up = std::min<int64_t>((a.T * (a.N / 8) + 255) / 256, 1 << 20);
-  hipLaunchKernelGGL(adapt_down_kernel<TE>, dim3(unsigned(down)), dim3(256), 0, s, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(adapt_up_kernel<TE>, dim3(unsigned(up)), dim3(256), 0, s, a);
+template <typename TE, int JW, int U>
+hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
+  // parts of the columns: a unit of 64 per wave at best, and no more blocks than run at
+  // once, two to a CU up to rank 32 (24 rows of 4096 -> 4096 rank 16: 1 part 12.2 us, 2 8.6,
+  // 4 6.8, 8 5.9; 64 rows, rank 64: 2 parts 19.9, 4 15.6, 6 24)
+  const int64_t most = (JW > 4 ? 256 : 512) / a.T;
+  const int64_t parts = std::min<int64_t>((a.N + 511) / 512, std::max<int64_t>(1, most));
+  hipLaunchKernelGGL((adapt_rows_kernel<TE, JW, U>), dim3(unsigned(a.T), unsigned(parts)), dim3(512), 0, s, a);
   return hipGetLastError();
+}
+template <typename TE>
+hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
+  if (a.rank <= 8) return launch_rows<TE, 1, 8>(a, s);
+  if (a.rank <= 16) return launch_rows<TE, 2, 4>(a, s);
+  if (a.rank <= 32) return launch_rows<TE, 4, 2>(a, s);
+  if (a.rank <= 64) return launch_rows<TE, 8, 2>(a, s);
+  return launch_rows<TE, 16, 1>(a, s);
+}
+
+// One row after the other or tiles of rows? Row by row each row fetches its adapter's
+// factors (from the caches), in tiles each adapter of a tile is fetched once. With an
+// adapter per row (256 rows of 2048 -> 2048, rank 32, 64 adapters: 17.7 us by rows, 105 in
+// tiles) rows win by far, with runs of rows tiles by what the factors weigh (300 rows of
+// 4096 -> 1152, rank 32, 100 MB: 14.6 us either way; 1000 of 1160 -> 2312, 222 MB: 28
+// against 16.4). The ids are on the device: batches of a decoding step's size count as
+// mixed up to 256 MB, larger ones are taken by rows only where that costs nothing.
+bool by_rows(int64_t T, int K, int N, int rank, int esize) {
+  const double mb = double(T) * rank * (double(K) + N) * esize / 1e6;
+  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 512 && mb <= 100.0);
 }
 
 }  // namespace
 
-namespace {
-constexpr int kRowsMost = 64;   // rows that are taken one by one
-}
-
-size_t adapters_part_bytes(int64_t T, int K, int rank, int esize) {
-  const int splits = T > kRowsMost ? down_splits(T, K, esize) : 1;
-  return size_t(splits) * size_t(T) * size_t(rank) * 4;
+size_t adapters_part_bytes(int64_t T, int K, int N, int rank, int esize) {
+  if (by_rows(T, K, N, rank, esize)) return 0;
+  return size_t(down_splits(T, K, esize)) * size_t(T) * size_t(rank) * 4;
 }
 
 hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s) {
-  if (a.T > kRowsMost) return a.bf16 ? launch_tiles<uint16_t>(a, s) : launch_tiles<float>(a, s);
-  return a.bf16 ? launch_adapters_typed<uint16_t>(a, s) : launch_adapters_typed<float>(a, s);
+  if (by_rows(a.T, a.K, a.N, a.rank, a.bf16 ? 2 : 4))
+    return a.bf16 ? launch_rows<uint16_t>(a, s) : launch_rows<float>(a, s);
+  return a.bf16 ? launch_tiles<uint16_t>(a, s) : launch_tiles<float>(a, s);
 }
 
 }  // namespace hq

@@ -251,7 +251,7 @@ struct AdaptArgs {
   LinEpi ep;
 };
 constexpr int ADAPT_MAX_RANK = 128;
-size_t adapters_part_bytes(int64_t T, int K, int rank, int esize);
+size_t adapters_part_bytes(int64_t T, int K, int N, int rank, int esize);
 hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s);
 
 // Integer-only DH / WH layers with integer requantisation.
