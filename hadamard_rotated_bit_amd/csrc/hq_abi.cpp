@@ -1216,6 +1216,7 @@ int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, co
   a.T = T;
   a.C = desc->channels;
   a.eps = desc->eps;
+  a.inv_c = 1.0f / float(desc->channels);
   a.x_bf16 = desc->x_dtype == HQ_BF16;
   a.y_bf16 = desc->y_dtype == HQ_BF16;
   const hipError_t e = hq::launch_rms_norm(a, static_cast<hipStream_t>(stream));

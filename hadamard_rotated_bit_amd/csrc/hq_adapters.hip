@@ -619,15 +619,17 @@ hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
 }
 
 // One row after the other or tiles of rows? Row by row each row fetches its adapter's
-// factors (from the caches), in tiles each adapter of a tile is fetched once. With an
-// adapter per row (256 rows of 2048 -> 2048, rank 32, 64 adapters: 17.7 us by rows, 105 in
-// tiles) rows win by far, with runs of rows tiles by what the factors weigh (300 rows of
-// 4096 -> 1152, rank 32, 100 MB: 14.6 us either way; 1000 of 1160 -> 2312, 222 MB: 28
-// against 16.4). The ids are on the device: batches of a decoding step's size count as
-// mixed up to 256 MB, larger ones are taken by rows only where that costs nothing.
+// factors (from the caches), in tiles each adapter of a tile is fetched once, but there
+// are two launches and a chain of waits in each. With runs of rows the two cross where the
+// rows fetch 100 MB (us, rows / tiles: 700 rows of 1024 -> 1024 rank 8, 23 MB, 9.3 / 13.9;
+// 600 of 2048 -> 2048 rank 16, 79 MB, 11.3 / 13.4; 300 of 4096 -> 1152 rank 32, 101 MB,
+// 14.3 / 15.0; 1000 of 1160 -> 2312 rank 32, 222 MB, 28 / 16.4) or where they are many
+// (4000 of 256 -> 512 rank 16, 98 MB, 19.5 / 13.3). With an adapter per row rows win by far
+// (256 rows of 2048 -> 2048, rank 32, 64 adapters: 14.4 / 105): the ids are on the device,
+// so batches of a decoding step's size count as mixed.
 bool by_rows(int64_t T, int K, int N, int rank, int esize) {
   const double mb = double(T) * rank * (double(K) + N) * esize / 1e6;
-  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 512 && mb <= 100.0);
+  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 2048 && mb <= 100.0);
 }
 
 }  // namespace

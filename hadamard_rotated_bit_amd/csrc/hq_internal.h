@@ -209,7 +209,7 @@ struct RmsArgs {
   float* scales;
   int64_t T;
   int C;
-  float eps;
+  float eps, inv_c;     // inv_c: 1 / C
   int x_bf16, y_bf16;   // h has x's type
 };
 hipError_t launch_rms_norm(const RmsArgs& a, hipStream_t s);

@@ -11,8 +11,8 @@
 // memory: x and r are read once, h, y and the codes written once.
 //
 // A code is decided as if v and the quotient were exact. In fp32, q = v rcp(max) 127
-// (one factor 127 / max) carries five roundings of 2^-24: two in v, two in the maximum
-// and one in the factor, an error below 127 x 5 x 2^-24 = 3.8e-5. Where q is further
+// carries two roundings of 2^-24 in v, two in the maximum, and 2^-23 + 2^-24 in 127
+// rcp(max): an error below 127 x 7 x 2^-24 = 5.3e-5. Where q is further
 // than 1e-4 from a half-integer its rounding is the exact one; the values nearer to one
 // (2 in 10^4) are decided again in fp64 with the row's fp64 maximum, which needs only
 // the values within 2^-21 of the fp32 maximum in fp64. A row with a v that is not a
@@ -27,9 +27,11 @@ namespace hq {
 namespace {
 
 constexpr float kBorder = 0.5f - 1e-4f;
-// Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats:
-// all their codes are decided in fp64.
-constexpr float kTiny = 0x1p-100f;
+// Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats, and
+// above 2^125 the reciprocal does: all their codes are decided in fp64.
+constexpr float kTiny = 0x1p-100f, kHuge = 0x1p125f;
+// Values that can be a row's largest in fp64: each carries 2^-23, the fp32 maximum too.
+constexpr float kNear = 1.0f - 0x1p-21f;
 
 // Maximum over the wave of a non-negative double that few lanes have.
 __device__ __forceinline__ double few_max(double v, bool mine) {
@@ -112,12 +114,15 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       }
     }
     s2 = group_sum<L>(s2);
+    const float mine = __uint_as_float(tb);   // the lane's largest |h gamma|
     double top64 = 0.0;
-    if constexpr (Q) {
-      // the fp64 maximum of the wave's part of the row (W > 1) or of each row of the wave
-      const uint32_t wb = bits_max<L>(tb);
-      const float near = __uint_as_float(wb) * (1.0f - 0x1p-21f);
-      if (__uint_as_float(tb) >= near && tb > 0 && wb < kInf) {
+    if constexpr (Q) tb = bits_max<L>(tb);
+    // The fp64 maximum of a row's values that are at least `near`: of the wave's part of the
+    // row (W > 1) or of each row of the wave, for every lane.
+    auto max64 = [&](float near) {
+      double m = 0.0;
+      const bool any = mine >= near && mine > 0.0f && mine < INFINITY;
+      if (any) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           if (sub + STEP * i >= nv) continue;
@@ -128,19 +133,20 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
           for (int e = 0; e < 8; ++e) {
             if (fabsf(h[i][e] * g[i][e]) >= near) {
               const double v = (k.r ? double(xv[e]) + double(rv[e]) : double(xv[e])) * double(g[i][e]);
-              top64 = fmax(top64, fabs(v));
+              m = fmax(m, fabs(v));
             }
           }
         }
       }
       if constexpr (L == 64) {
-        top64 = few_max(top64, top64 > 0.0);
+        m = few_max(m, any);
       } else {
 #pragma unroll
-        for (int m = 1; m < L; m <<= 1) top64 = fmax(top64, __shfl_xor(top64, m, 64));
+        for (int d = 1; d < L; d <<= 1) m = fmax(m, __shfl_xor(m, d, 64));
       }
-      tb = wb;
-    }
+      return m;
+    };
+    if constexpr (Q && W > 1) top64 = max64(__uint_as_float(tb) * kNear);
     if constexpr (W > 1) {
       const int w = int(threadIdx.x) >> 6;
       __syncthreads();   // the last row's values are read
@@ -158,7 +164,9 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
         top64 = fmax(fmax(part_top[0], part_top[1]), fmax(part_top[2], part_top[3]));
       }
     }
-    float rstd = 1.0f / sqrtf(s2 / float(k.C) + k.eps);
+    const float ms = fmaf(s2, k.inv_c, k.eps);
+    // rsq (one unit) takes no squares below the smallest normal floats
+    float rstd = ms >= 0x1p-100f ? __builtin_amdgcn_rsqf(ms) : 1.0f / sqrtf(ms);
     if (__any(s2 == INFINITY)) {
       // squares past the largest float: once more, of h 2^-80 (the same branch for a
       // whole block where a block has one row)
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
         __syncthreads();
         z2 = (part[0] + part[1]) + (part[2] + part[3]);
       }
-      if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 / float(k.C) + k.eps * 0x1p-80f * 0x1p-80f);
+      if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 * k.inv_c + k.eps * 0x1p-80f * 0x1p-80f);
     }
     if (k.h) {
 #pragma unroll
@@ -200,20 +208,30 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
     if constexpr (Q) {
       const bool finite = tb < kInf;
       const float top = __uint_as_float(tb);
-      const float rcp = finite && top >= kTiny ? 127.0f / top : 0.0f;
-      const float border = top < kTiny ? -1.0f : kBorder;   // tiny rows: all of them in fp64
+      const bool plain = top >= kTiny && top <= kHuge;
+      const float rcp = plain ? 127.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
+      const float border = plain || !finite || top == 0.0f ? kBorder : -1.0f;
+      float far = -0.5f;   // the lane's nearest value to a half-integer
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = h[i][e] * g[i][e];
+          far = fmaxf(far, fabsf(fmaf(v, rcp, -rintf(v * rcp))));
+        }
+      }
+      const bool again = far > border;
+      if constexpr (W == 1) {
+        if (__any(again)) top64 = max64(top * kNear);
+      }
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (sub + STEP * i >= nv) continue;
         int q[8];
-        float far = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = h[i][e] * g[i][e], n = rintf(v * rcp);
-          q[e] = int(n);
-          far = fmaxf(far, fabsf(fmaf(v, rcp, -n)));
-        }
-        if (finite && top > 0.0f && far > border) {
+        for (int e = 0; e < 8; ++e) q[e] = int(rintf(h[i][e] * g[i][e] * rcp));
+        if (again) {
           float xv[8], rv[8];
           raw_get(x[i], xv);
           if (k.r) raw_get(r[i], rv);
@@ -234,7 +252,7 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
                         : 0u;
         *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) = make_uint2(d[0], d[1]);
       }
-      if (sub == 0 && row < k.T) k.scales[row] = finite ? top / 127.0f * rstd : __uint_as_float(0x7fc00000u);
+      if (sub == 0 && row < k.T) k.scales[row] = finite ? top * (1.0f / 127.0f) * rstd : __uint_as_float(0x7fc00000u);
     }
   }
 }

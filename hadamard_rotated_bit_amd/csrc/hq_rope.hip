@@ -63,10 +63,18 @@ __device__ __forceinline__ void store4(uint16_t* p, const float v[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// Sum over the n lanes from `first` (n uniform, up to 32; lanes of other runs do the
-// same): every lane gets the sum, in one fixed order.
+// Sum over the runs of n lanes (n uniform, up to 32) that a wave's heads take, in one
+// fixed order; pos is the lane's place in its run, first the run's first lane.
 __device__ __forceinline__ float run_sum(float v, int first, int n, int pos) {
-  for (int d = 32; d >= 1; d >>= 1) {
+  switch (n) {
+    case 1: return v;
+    case 2: return group_sum<2>(v);
+    case 4: return group_sum<4>(v);
+    case 8: return group_sum<8>(v);
+    case 16: return group_sum<16>(v);
+    case 32: return group_sum<32>(v);
+  }
+  for (int d = 16; d >= 1; d >>= 1) {
     if (d >= n) continue;
     const float o = __shfl(v, first + pos + d, 64);
     if (pos + d < n && pos < d) v += o;
@@ -74,87 +82,118 @@ __device__ __forceinline__ float run_sum(float v, int first, int n, int pos) {
   return __shfl(v, first, 64);
 }
 
+// A unit's eight channels as loaded: neighbours, or four of each half.
+template <typename TE, bool SPLIT>
+__device__ __forceinline__ Raw8<TE> unit_load(const TE* p, uint32_t o0, uint32_t o1) {
+  if constexpr (!SPLIT) {
+    return raw_load(p + o0);
+  } else if constexpr (sizeof(TE) == 2) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p + o0), b = *reinterpret_cast<const uint2*>(p + o1);
+    Raw8<TE> r;
+    r.q[0] = make_uint4(a.x, a.y, b.x, b.y);
+    return r;
+  } else {
+    Raw8<TE> r;
+    r.q[0] = *reinterpret_cast<const uint4*>(p + o0);
+    r.q[1] = *reinterpret_cast<const uint4*>(p + o1);
+    return r;
+  }
+}
+
 }  // namespace
 
-// A wave per token and part of its heads (parts per token: `split`); a head's D / 8
-// units of 8 channels go to D / 8 lanes, 64 / (D / 8) heads at a time.
-template <typename TE, typename TY, bool HALVES>
+// A wave per token and part of its heads (`split` parts per token); a head's D / 8 units
+// of 8 channels go to D / 8 lanes, 64 / (D / 8) heads at a time, the next ones' loads in
+// flight meanwhile (and the first ones' during the angles).
+template <typename TE, typename TY, bool HALVES, bool NORM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
-  __shared__ float cs[4][2][ROPE_MAX_PAIRS];
-  const int lane = int(threadIdx.x) & 63, w = int(threadIdx.x) >> 6;
+  __shared__ __attribute__((aligned(16))) float cs[4][2][ROPE_MAX_PAIRS];
+  const int lane = int(threadIdx.x) & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int U = k.D / 8, slots = 64 / U;
   const int slot = lane / U, u = lane - slot * U;
   const int P = k.pairs;
-  // no barrier below: waves are on their own
-  for (int64_t job = int64_t(blockIdx.x) * 4 + w; job < k.T * k.split; job += int64_t(gridDim.x) * 4) {
-  const int64_t tok = job / k.split;
-  const int part = int(job - tok * k.split);
-  for (int i = lane; i < P; i += 64) {
-    int ax = 0;
-    while (ax < k.axes - 1 && i >= k.end[ax]) ++ax;
-    const double pos = k.pos_f32 ? double(static_cast<const float*>(k.pos)[tok * k.axes + ax])
-                                 : double(static_cast<const int32_t*>(k.pos)[tok * k.axes + ax]);
-    float s, c;
-    turn_sincos(pos, k.freqs[i], &s, &c);
-    cs[w][0][i] = c;
-    cs[w][1][i] = k.inverse ? -s : s;
-  }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  // the unit's channels: 8 neighbours, or 4 of each half and, behind them, 8 that pass
   const int NU = P / 4;               // units with pairs
   const bool turns = u < NU;
+  // the unit's channels: 8 neighbours, or 4 of each half and, behind them, 8 that pass
   const int o0 = HALVES && turns ? 4 * u : 8 * u;
   const int o1 = HALVES && turns ? P + 4 * u : 8 * u + 4;
-  float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (turns) {
-    load4(&cs[w][0][4 * u], c);
-    load4(&cs[w][1][4 * u], s);
-  }
   const int heads = k.Hq + k.Hk;
   const int per = (heads + slots * k.split - 1) / (slots * k.split);   // turns of each part
-  const TE* const x = static_cast<const TE*>(k.x) + tok * k.ldx;
-  TY* const y = static_cast<TY*>(k.y) + tok * k.ldy;
   const float inv = 1.0f / float(k.D);
-  for (int it = 0; it < per; ++it) {
-    const int head = (part * per + it) * slots + slot;
-    const bool live = slot < slots && head < heads;
-    float v[8] = {};
-    if (live) {
-      load4(x + head * k.D + o0, v);
-      load4(x + head * k.D + o1, v + 4);
-    }
-    if (k.norm) {
-      float q = 0.0f;
+  float gq[8], gk[8];
+  if constexpr (NORM) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-      q = run_sum(q, slot * U, U, u);
-      const float rstd = 1.0f / sqrtf(q * inv + k.eps);
-      if (live) {
-        const float* const ga = head < k.Hq ? k.gamma_q : k.gamma_k;
-        float g[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-        if (ga) {
-          load4(ga + o0, g);
-          load4(ga + o1, g + 4);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * g[e];
-      }
+    for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 1.0f;
+    if (k.gamma_q && slot < slots) {
+      load4(k.gamma_q + o0, gq);
+      load4(k.gamma_q + o1, gq + 4);
     }
-    if (!live) continue;
-    if (turns) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ia = HALVES ? e : 2 * e, ib = HALVES ? 4 + e : 2 * e + 1;
-        const float a = v[ia], b = v[ib];
-        v[ia] = a * c[e] - b * s[e];
-        v[ib] = b * c[e] + a * s[e];
-      }
+    if (k.gamma_k && slot < slots) {
+      load4(k.gamma_k + o0, gk);
+      load4(k.gamma_k + o1, gk + 4);
     }
-    store4(y + head * k.D + o0, v);
-    store4(y + head * k.D + o1, v + 4);
   }
+  // no barrier: waves are on their own
+  for (int64_t job = int64_t(blockIdx.x) * 4 + w; job < k.T * k.split; job += int64_t(gridDim.x) * 4) {
+    const int64_t tok = k.split == 1 ? job : job / k.split;
+    const int h0 = int(job - tok * k.split) * per * slots, h1 = min(h0 + per * slots, heads);
+    const TE* const x = static_cast<const TE*>(k.x) + tok * k.ldx;
+    TY* const y = static_cast<TY*>(k.y) + tok * k.ldy;
+    Raw8<TE> next = {};
+    int head = slot < slots ? h0 + slot : h1;
+    if (head < h1) next = unit_load<TE, HALVES>(x + head * k.D, o0, o1);
+    for (int i = lane; i < P; i += 64) {
+      int ax = 0;
+      while (ax < k.axes - 1 && i >= k.end[ax]) ++ax;
+      const double pos = k.pos_f32 ? double(static_cast<const float*>(k.pos)[tok * k.axes + ax])
+                                   : double(static_cast<const int32_t*>(k.pos)[tok * k.axes + ax]);
+      float s, c;
+      turn_sincos(pos, k.freqs[i], &s, &c);
+      cs[w][0][i] = c;
+      cs[w][1][i] = k.inverse ? -s : s;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (turns) {
+      load4(&cs[w][0][4 * u], c);
+      load4(&cs[w][1][4 * u], s);
+    }
+#pragma unroll 1
+    for (int it = h0; it < h1; it += slots, head += slots) {
+      float v[8];
+      raw_get(next, v);
+      if (head + slots < h1) next = unit_load<TE, HALVES>(x + (head + slots) * k.D, o0, o1);
+      if constexpr (NORM) {
+        float q = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+        q = fmaf(run_sum(q, slot * U, U, u), inv, k.eps);
+        // rsq takes no squares below the smallest normal floats
+        const float rstd = q >= 0x1p-100f ? __builtin_amdgcn_rsqf(q) : 1.0f / sqrtf(q);
+        const bool isq = head < k.Hq;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * (isq ? gq[e] : gk[e]);
+      }
+      if (head >= h1) continue;
+      if (turns) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ia = HALVES ? e : 2 * e, ib = HALVES ? 4 + e : 2 * e + 1;
+          const float a = v[ia], b = v[ib];
+          v[ia] = a * c[e] - b * s[e];
+          v[ib] = b * c[e] + a * s[e];
+        }
+      }
+      TY* const out = y + head * k.D;
+      if constexpr (HALVES) {
+        store4(out + o0, v);
+        store4(out + o1, v + 4);
+      } else {
+        store8(out + o0, v);
+      }
+    }
   }
 }
 
@@ -167,8 +206,13 @@ hipError_t launch_rope_typed(RopeArgs a, hipStream_t s) {
   a.split = int(std::max<int64_t>(1, std::min<int64_t>(std::min(turns, 8), 2048 / a.T)));
   const int64_t waves = a.T * a.split;
   const dim3 grid(unsigned(std::min<int64_t>((waves + 3) / 4, 1 << 20)));
-  if (a.halves) hipLaunchKernelGGL((rope_kernel<TE, TY, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rope_kernel<TE, TY, false>), grid, dim3(256), 0, s, a);
+  if (a.halves) {
+    if (a.norm) hipLaunchKernelGGL((rope_kernel<TE, TY, true, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((rope_kernel<TE, TY, true, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (a.norm) hipLaunchKernelGGL((rope_kernel<TE, TY, false, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((rope_kernel<TE, TY, false, false>), grid, dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
