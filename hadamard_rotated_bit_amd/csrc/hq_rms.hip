@@ -30,8 +30,11 @@ constexpr float kBorder = 0.5f - 1e-4f;
 // Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats, and
 // above 2^125 the reciprocal does: all their codes are decided in fp64.
 constexpr float kTiny = 0x1p-100f, kHuge = 0x1p125f;
-// Values that can be a row's largest in fp64: each carries 2^-23, the fp32 maximum too.
-constexpr float kNear = 1.0f - 0x1p-21f;
+// The least fp32 value that can be a row's largest in fp64: each carries 2^-23 of itself
+// (or half the smallest float), the fp32 maximum too.
+__device__ __forceinline__ float near_of(float top) {
+  return fmaxf(0.0f, fminf(top * (1.0f - 0x1p-21f), top - 0x1p-147f));
+}
 
 // Maximum over the wave of a non-negative double that few lanes have.
 __device__ __forceinline__ double few_max(double v, bool mine) {
@@ -90,26 +93,42 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       for (int i = 0; i < R; ++i)
         if (sub + STEP * i < nv) r[i] = raw_load(static_cast<const TE*>(k.r) + base + 8 * STEP * i);
     }
-    float h[R][8], g[R][8];
+    // h of piece i, in fp32: x and r stay as they were loaded, beside v = h gamma
+    auto sum_of = [&](int i, float (&h)[8]) {
+      raw_get(x[i], h);
+      if (k.r) {
+        float t[8];
+        raw_get(r[i], t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] += t[e];
+      }
+    };
+    // h gamma of value n = 8 i + e of the lane in fp64, from memory (nothing of the row is
+    // written before the codes are decided; few values come here, and indexes that are not
+    // known beforehand keep registers free)
+    auto exact = [&](int n) {
+      const int64_t c = 8 * (sub + STEP * (n >> 3)) + (n & 7);
+      auto at = [&](const void* p) {
+        if constexpr (sizeof(TE) == 2) return double(bf16_to_f32(static_cast<const uint16_t*>(p)[row * k.C + c]));
+        else return double(static_cast<const float*>(p)[row * k.C + c]);
+      };
+      const double h = k.r ? at(k.x) + at(k.r) : at(k.x);
+      return k.gamma ? h * double(k.gamma[c]) : h;
+    };
+    float v[R][8];
     float s2 = 0.0f;
     uint32_t tb = 0;   // bits of max |h gamma|
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (sub + STEP * i < nv) {
-        raw_get(x[i], h[i]);
-        if (k.r) {
-          float t[8];
-          raw_get(r[i], t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[i][e] += t[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] = 1.0f;
-        if (k.gamma) load8(k.gamma + 8 * (sub + STEP * i), g[i]);
+        float h[8], g[8];
+        if (k.gamma) load8(k.gamma + 8 * (sub + STEP * i), g);
+        sum_of(i, h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s2 = fmaf(h[i][e], h[i][e], s2);
-          if constexpr (Q) tb = max(tb, __float_as_uint(h[i][e] * g[i][e]) & 0x7fffffffu);
+          s2 = fmaf(h[e], h[e], s2);
+          v[i][e] = k.gamma ? h[e] * g[e] : h[e];
+          if constexpr (Q) tb = max(tb, __float_as_uint(v[i][e]) & 0x7fffffffu);
         }
       }
     }
@@ -123,20 +142,14 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       double m = 0.0;
       const bool any = mine >= near && mine > 0.0f && mine < INFINITY;
       if (any) {
+        uint32_t which = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           if (sub + STEP * i >= nv) continue;
-          float xv[8], rv[8];
-          raw_get(x[i], xv);
-          if (k.r) raw_get(r[i], rv);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (fabsf(h[i][e] * g[i][e]) >= near) {
-              const double v = (k.r ? double(xv[e]) + double(rv[e]) : double(xv[e])) * double(g[i][e]);
-              m = fmax(m, fabs(v));
-            }
-          }
+          for (int e = 0; e < 8; ++e) which |= fabsf(v[i][e]) >= near ? 1u << (8 * i + e) : 0u;
         }
+        for (; which; which &= which - 1) m = fmax(m, fabs(exact(__builtin_ctz(which))));
       }
       if constexpr (L == 64) {
         m = few_max(m, any);
@@ -146,7 +159,7 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       }
       return m;
     };
-    if constexpr (Q && W > 1) top64 = max64(__uint_as_float(tb) * kNear);
+    if constexpr (Q && W > 1) top64 = max64(near_of(__uint_as_float(tb)));
     if constexpr (W > 1) {
       const int w = int(threadIdx.x) >> 6;
       __syncthreads();   // the last row's values are read
@@ -174,9 +187,11 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (sub + STEP * i >= nv) continue;
+        float h[8];
+        sum_of(i, h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float z = h[i][e] * 0x1p-80f;
+          const float z = h[e] * 0x1p-80f;
           z2 = fmaf(z, z, z2);
         }
       }
@@ -189,10 +204,49 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       }
       if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 * k.inv_c + k.eps * 0x1p-80f * 0x1p-80f);
     }
+    if constexpr (Q) {
+      const bool finite = tb < kInf;
+      const float top = __uint_as_float(tb);
+      const bool plain = top >= kTiny && top <= kHuge;
+      const float rcp = plain ? 127.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
+      const float border = plain || !finite || top == 0.0f ? kBorder : -1.0f;
+      uint32_t again = 0;   // values next to a half-integer
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+        uint32_t d[2] = {};
+        float far = -0.5f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = rintf(v[i][e] * rcp);
+          far = fmaxf(far, fabsf(fmaf(v[i][e], rcp, -n)));
+          d[e >> 2] |= (uint32_t(int(n)) & 255u) << (8 * (e & 3));
+        }
+        if (far > border) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            again |= fabsf(fmaf(v[i][e], rcp, -rintf(v[i][e] * rcp))) > border ? 1u << (8 * i + e) : 0u;
+        }
+        *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) =
+            finite ? make_uint2(d[0], d[1]) : make_uint2(0, 0);
+      }
+      if constexpr (W == 1) {
+        if (__any(again)) top64 = max64(near_of(top));
+      }
+      for (; again; again &= again - 1) {
+        const int n = __builtin_ctz(again);
+        k.codes[base + 8 * STEP * (n >> 3) + (n & 7)] = uint8_t(int8_t(int(rint(exact(n) / (top64 / 127.0)))));
+      }
+      if (sub == 0 && row < k.T) k.scales[row] = finite ? top * (1.0f / 127.0f) * rstd : __uint_as_float(0x7fc00000u);
+    }
     if (k.h) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (sub + STEP * i < nv) store8(static_cast<TE*>(k.h) + base + 8 * STEP * i, h[i]);
+      for (int i = 0; i < R; ++i) {
+        if (sub + STEP * i >= nv) continue;
+        float h[8];
+        sum_of(i, h);
+        store8(static_cast<TE*>(k.h) + base + 8 * STEP * i, h);
+      }
     }
     if (k.y) {
 #pragma unroll
@@ -200,59 +254,10 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
         if (sub + STEP * i >= nv) continue;
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (h[i][e] * rstd) * g[i][e];
+        for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd;
         if (k.y_bf16) store8(static_cast<uint16_t*>(k.y) + base + 8 * STEP * i, y);
         else store8(static_cast<float*>(k.y) + base + 8 * STEP * i, y);
       }
-    }
-    if constexpr (Q) {
-      const bool finite = tb < kInf;
-      const float top = __uint_as_float(tb);
-      const bool plain = top >= kTiny && top <= kHuge;
-      const float rcp = plain ? 127.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
-      const float border = plain || !finite || top == 0.0f ? kBorder : -1.0f;
-      float far = -0.5f;   // the lane's nearest value to a half-integer
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (sub + STEP * i >= nv) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = h[i][e] * g[i][e];
-          far = fmaxf(far, fabsf(fmaf(v, rcp, -rintf(v * rcp))));
-        }
-      }
-      const bool again = far > border;
-      if constexpr (W == 1) {
-        if (__any(again)) top64 = max64(top * kNear);
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (sub + STEP * i >= nv) continue;
-        int q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = int(rintf(h[i][e] * g[i][e] * rcp));
-        if (again) {
-          float xv[8], rv[8];
-          raw_get(x[i], xv);
-          if (k.r) raw_get(r[i], rv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = h[i][e] * g[i][e];
-            if (fabsf(fmaf(v, rcp, -rintf(v * rcp))) > border) {
-              const double v64 = (k.r ? double(xv[e]) + double(rv[e]) : double(xv[e])) * double(g[i][e]);
-              q[e] = int(rint(v64 / (top64 / 127.0)));
-            }
-          }
-        }
-        uint32_t d[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          d[e] = finite ? (uint32_t(q[4 * e]) & 255u) | (uint32_t(q[4 * e + 1]) & 255u) << 8 |
-                              (uint32_t(q[4 * e + 2]) & 255u) << 16 | uint32_t(q[4 * e + 3]) << 24
-                        : 0u;
-        *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) = make_uint2(d[0], d[1]);
-      }
-      if (sub == 0 && row < k.T) k.scales[row] = finite ? top * (1.0f / 127.0f) * rstd : __uint_as_float(0x7fc00000u);
     }
   }
 }
