@@ -493,12 +493,18 @@ __global__ __launch_bounds__(256, 3) void adapt_up_tile_kernel(AdaptArgs k) {
   if (none) {
 #pragma unroll 1
     for (int slab = s0; slab < s1; slab += sd) {
-      if (slab > s0) load_base(slab);
+      float v[4][8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v[8];
-        base_of(e, v);
-        finish(v, e, slab, (none >> (4 * g + e)) & 1);
+        base_of(e, v[e]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) asm volatile("" : "+v"(v[e][x]));   // bb is free
+      }
+      load_base(slab + sd);   // past the last slab nothing is read
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        finish(v[e], e, slab, (none >> (4 * g + e)) & 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (all) load_base(s0);
@@ -574,7 +580,11 @@ hipError_t launch_down(const AdaptArgs& a, hipStream_t s) {
 template <typename TE, typename TY, int SU>
 hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t tiles = (a.T + 63) / 64, slabs = (a.N + 127) / 128;
-  a.slabs = int(std::max<int64_t>(1, std::min<int64_t>(8, tiles * slabs / 1024)));
+  // column groups: up to 12 per row tile, more where that leaves CUs without a block, whole
+  // slabs each (8192 rows, 36 slabs: 4 groups 62 us, 8 49, 12 43.6; 32 slabs rank 64: 4 43,
+  // 11 39, 16 41; 1000 rows, 19 slabs: 8 15.1, 12 11.1, 19 9.6)
+  const int64_t groups = std::max<int64_t>(12, 512 / tiles);
+  a.slabs = int((slabs + groups - 1) / groups);
   const dim3 grid(unsigned(tiles + 7) / 8 * 8, unsigned((slabs + a.slabs - 1) / a.slabs));
   hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
@@ -621,15 +631,15 @@ hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
 // One row after the other or tiles of rows? Row by row each row fetches its adapter's
 // factors (from the caches), in tiles each adapter of a tile is fetched once, but there
 // are two launches and a chain of waits in each. With runs of rows the two cross where the
-// rows fetch 100 MB (us, rows / tiles: 700 rows of 1024 -> 1024 rank 8, 23 MB, 9.3 / 13.9;
+// rows fetch 120 MB (us, rows / tiles: 700 rows of 1024 -> 1024 rank 8, 23 MB, 9.3 / 13.9;
 // 600 of 2048 -> 2048 rank 16, 79 MB, 11.3 / 13.4; 300 of 4096 -> 1152 rank 32, 101 MB,
-// 14.3 / 15.0; 1000 of 1160 -> 2312 rank 32, 222 MB, 28 / 16.4) or where they are many
+// 14.3 / 15.0; 1037 of 1160 -> 2312 rank 8 fp32, 115 MB, 19.1 / 20.5; 1000 of 1160 -> 2312 rank 32, 222 MB, 28 / 16.4) or where they are many
 // (4000 of 256 -> 512 rank 16, 98 MB, 19.5 / 13.3). With an adapter per row rows win by far
 // (256 rows of 2048 -> 2048, rank 32, 64 adapters: 14.4 / 105): the ids are on the device,
 // so batches of a decoding step's size count as mixed.
 bool by_rows(int64_t T, int K, int N, int rank, int esize) {
   const double mb = double(T) * rank * (double(K) + N) * esize / 1e6;
-  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 2048 && mb <= 100.0);
+  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 2048 && mb <= 120.0);
 }
 
 }  // namespace
