@@ -677,23 +677,31 @@ def rms_norm(desc: RmsNormDesc, X: torch.Tensor, gamma: Optional[torch.Tensor] =
         _fits(gamma, "gamma", torch.float32, (desc.channels,), device)
     ydt, want = _TORCH[desc.y_dtype], desc.outputs
     # outputs of X's type and shape are allocated like X: half a microsecond less each
-    for t, name, dtype, size, flag in ((out, "out", ydt, shape, HQ_RMS_Y),
-                                       (sum_out, "sum_out", xdt, shape, HQ_RMS_SUM),
-                                       (codes, "codes", torch.int8, shape, HQ_RMS_CODES),
-                                       (scales, "scales", torch.float32, shape[:1], HQ_RMS_CODES)):
-        if t is not None:
-            if not want & flag:
-                raise ValueError(f"{name} is not among the descriptor's outputs")
-            _fits(t, name, dtype, size, device)
-    if want & HQ_RMS_Y and out is None:
-        out = torch.empty_like(X) if ydt is xdt else X.new_empty(shape, dtype=ydt)
-    if want & HQ_RMS_SUM and sum_out is None:
-        sum_out = torch.empty_like(X)
+    if want & HQ_RMS_Y:
+        if out is None:
+            out = torch.empty_like(X) if ydt is xdt else X.new_empty(shape, dtype=ydt)
+        else:
+            _fits(out, "out", ydt, shape, device)
+    elif out is not None:
+        raise ValueError("out is not among the descriptor's outputs")
+    if want & HQ_RMS_SUM:
+        if sum_out is None:
+            sum_out = torch.empty_like(X)
+        else:
+            _fits(sum_out, "sum_out", xdt, shape, device)
+    elif sum_out is not None:
+        raise ValueError("sum_out is not among the descriptor's outputs")
     if want & HQ_RMS_CODES:
         if codes is None:
             codes = X.new_empty(shape, dtype=torch.int8)
+        else:
+            _fits(codes, "codes", torch.int8, shape, device)
         if scales is None:
             scales = X.new_empty(shape[:1], dtype=torch.float32)
+        else:
+            _fits(scales, "scales", torch.float32, shape[:1], device)
+    elif codes is not None or scales is not None:
+        raise ValueError("codes are not among the descriptor's outputs")
     check(load().hq_rms_norm(desc._ref, X.data_ptr(), _addr(residual), _addr(gamma), shape[0],
                              _addr(sum_out), _addr(out), _addr(codes), _addr(scales),
                              _stream_of(device)))

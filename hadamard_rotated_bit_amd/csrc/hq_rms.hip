@@ -70,12 +70,15 @@ constexpr uint32_t kInf = 0x7f800000u;
 
 // L lanes per row (64 / L rows per wave) and W waves per row (W > 1: L = 64, a block
 // per row), R pieces of 8 channels per lane. Q: codes are wanted.
+// The least waves per SIMD keep the registers of the codes' rare path down (12288 x 256
+// fp32 9.9 -> 9.6 us, 8192 x 4096 bf16 61.6 -> 59.5; one more wave spills: 13.1, 70.9).
 template <typename TE, int L, int W, int R, bool Q>
-__global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
+__global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(RmsArgs k) {
   static_assert(W == 1 || (W == 4 && L == 64), "a block per row or whole rows per wave");
-  __shared__ float part[W];
-  __shared__ uint32_t part_bits[W];
+  __shared__ float part[2][W], part_z[W];   // of rows in turn: one barrier for each
+  __shared__ uint32_t part_bits[2][W];
   __shared__ double part_top[W];
+  int turn = 0;
   constexpr int RPB = 256 / (L * W);   // rows per block
   const int VR = k.C / 8;
   const int sub = W > 1 ? int(threadIdx.x) : int(threadIdx.x) & (L - 1);
@@ -136,8 +139,8 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
     const float mine = __uint_as_float(tb);   // the lane's largest |h gamma|
     double top64 = 0.0;
     if constexpr (Q) tb = bits_max<L>(tb);
-    // The fp64 maximum of a row's values that are at least `near`: of the wave's part of the
-    // row (W > 1) or of each row of the wave, for every lane.
+    // The fp64 maximum of the values that are at least `near`, for every lane: of the wave's
+    // part of a row (W > 1) or of each row of the wave.
     auto max64 = [&](float near) {
       double m = 0.0;
       const bool any = mine >= near && mine > 0.0f && mine < INFINITY;
@@ -159,23 +162,20 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       }
       return m;
     };
-    if constexpr (Q && W > 1) top64 = max64(near_of(__uint_as_float(tb)));
     if constexpr (W > 1) {
       const int w = int(threadIdx.x) >> 6;
-      __syncthreads();   // the last row's values are read
       if ((threadIdx.x & 63) == 0) {
-        part[w] = s2;
-        if constexpr (Q) {
-          part_bits[w] = tb;
-          part_top[w] = top64;
-        }
+        part[turn][w] = s2;
+        if constexpr (Q) part_bits[turn][w] = tb;
       }
       __syncthreads();
-      s2 = (part[0] + part[1]) + (part[2] + part[3]);
+      const float* const p = part[turn];
+      s2 = (p[0] + p[1]) + (p[2] + p[3]);
       if constexpr (Q) {
-        tb = max(max(part_bits[0], part_bits[1]), max(part_bits[2], part_bits[3]));
-        top64 = fmax(fmax(part_top[0], part_top[1]), fmax(part_top[2], part_top[3]));
+        const uint32_t* const b = part_bits[turn];
+        tb = max(max(b[0], b[1]), max(b[2], b[3]));
       }
+      turn ^= 1;
     }
     const float ms = fmaf(s2, k.inv_c, k.eps);
     // rsq (one unit) takes no squares below the smallest normal floats
@@ -197,10 +197,9 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
       }
       z2 = group_sum<L>(z2);
       if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0) part_z[int(threadIdx.x) >> 6] = z2;
         __syncthreads();
-        if ((threadIdx.x & 63) == 0) part[int(threadIdx.x) >> 6] = z2;
-        __syncthreads();
-        z2 = (part[0] + part[1]) + (part[2] + part[3]);
+        z2 = (part_z[0] + part_z[1]) + (part_z[2] + part_z[3]);
       }
       if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 * k.inv_c + k.eps * 0x1p-80f * 0x1p-80f);
     }
@@ -230,8 +229,14 @@ __global__ __launch_bounds__(256) void rms_kernel(RmsArgs k) {
         *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) =
             finite ? make_uint2(d[0], d[1]) : make_uint2(0, 0);
       }
+      // every wave of the row has to help where one needs the fp64 maximum
       if constexpr (W == 1) {
         if (__any(again)) top64 = max64(near_of(top));
+      } else if (__syncthreads_or(again != 0)) {
+        top64 = max64(near_of(top));
+        if ((threadIdx.x & 63) == 0) part_top[int(threadIdx.x) >> 6] = top64;
+        __syncthreads();
+        top64 = fmax(fmax(part_top[0], part_top[1]), fmax(part_top[2], part_top[3]));
       }
       for (; again; again &= again - 1) {
         const int n = __builtin_ctz(again);
