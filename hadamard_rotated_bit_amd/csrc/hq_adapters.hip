@@ -351,9 +351,10 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
 // LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
 // with 256 bytes of a bf16 row: base, residual and Y move in whole lines. SU: k-steps of
-// the product.
-template <typename TE, typename TY, int SU>
-__global__ __launch_bounds__(256, 3) void adapt_up_tile_kernel(AdaptArgs k) {
+// the product. EXT: an activation, a gate or a residual (without them the kernel is a third
+// of the code, which a short launch has to fetch first).
+template <typename TE, typename TY, int SU, bool EXT>
+__global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
   constexpr int NP = sizeof(TE) == 2 ? 3 : 1;
   constexpr uint32_t ES = sizeof(TE), EY = sizeof(TY);
@@ -461,18 +462,20 @@ __global__ __launch_bounds__(256, 3) void adapt_up_tile_kernel(AdaptArgs k) {
     asm volatile("" : "+v"(at));   // addresses made here, not kept over the slabs
     at += e * rowb + 128 * slab * EY;
     ok = ok && 128 * slab + 8 * i < k.N;
-    float t[8];
-    apply_act<8, EY == 4>(v, k.ep.act);
-    if (k.ep.gate) {
-      if (ok) raw_get(raw_load(static_cast<const TY*>(k.ep.gate) + 128 * slab + 8 * i +
-                               int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld), t);
+    if constexpr (EXT) {
+      float t[8];
+      apply_act<8, EY == 4>(v, k.ep.act);
+      if (k.ep.gate) {
+        if (ok) raw_get(raw_load(static_cast<const TY*>(k.ep.gate) + 128 * slab + 8 * i +
+                                 int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld), t);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] *= t[x];
-    }
-    if (k.ep.residual) {
-      if (ok) raw_get(raw_at<TY>(static_cast<const uint8_t*>(k.ep.residual) + w0 * k.N * EY, at), t);
+        for (int x = 0; x < 8; ++x) v[x] *= t[x];
+      }
+      if (k.ep.residual) {
+        if (ok) raw_get(raw_at<TY>(static_cast<const uint8_t*>(k.ep.residual) + w0 * k.N * EY, at), t);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] += t[x];
+        for (int x = 0; x < 8; ++x) v[x] += t[x];
+      }
     }
     if (!ok) at = kOutside;
     if constexpr (EY == 2) {
@@ -586,7 +589,10 @@ hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t groups = std::max<int64_t>(12, 512 / tiles);
   a.slabs = int((slabs + groups - 1) / groups);
   const dim3 grid(unsigned(tiles + 7) / 8 * 8, unsigned((slabs + a.slabs - 1) / a.slabs));
-  hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU>), grid, dim3(256), 0, s, a);
+  if (a.ep.act.act != ACT_NONE || a.ep.gate || a.ep.residual)
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <typename TE, typename TY>
