@@ -62,15 +62,27 @@ def test_call_refusals(kw, status, word):
 
 
 def test_workspace():
-    n = lib.hq_adapters_workspace_bytes(ref(), 100)
-    assert n >= 100 * 16 * 4
+    # rows one by one need none, tiles of rows a row's products with A for each part of K
+    assert lib.hq_adapters_workspace_bytes(ref(), 100) == 0
+    n = lib.hq_adapters_workspace_bytes(ref(), 5000)
+    assert n >= 5000 * 16 * 4
     assert lib.hq_adapters_workspace_bytes(ref(), 0) == 0 and lib.hq_adapters_workspace_bytes(ref(), -1) == 0
-    assert call(ws=None, n=0) == -3
-    assert call(n=n - 1) == -3
+    assert call(T=5000, ws=None, n=0) == -3
+    assert call(T=5000, n=n - 1) == -3
     assert b"workspace" in lib.hq_last_error()
     for at in (0x10000000, 0x20000000, 0x30000010, 0x1000, 0x8000, 0x40000000, 0x50000000 - 16):
-        assert call(ws=at, n=n) == -1
+        assert call(T=5000, ws=at, n=n) == -1
         assert b"workspace overlaps" in lib.hq_last_error()
+
+
+def test_workspace_over_the_range():
+    # from one row to the most, every rank: never negative, never more than 256 parts
+    for T in (1, 4, 5, 64, 256, 257, 2048, 2049, 8192, 100_000, 1 << 26):
+        for d_in, d_out, rank in ((8, 8, 8), (65536, 8, 128), (8, 65536, 64), (65536, 65536, 128), (4096, 4096, 16)):
+            for dt in (0, 1):
+                n = lib.hq_adapters_workspace_bytes(ref(d_in, d_out, rank, dt, dt, dt), T)
+                assert n == 0 or T * rank * 4 <= n <= 256 * T * rank * 4 + 256
+                assert n > 0 or T <= 2048
 
 
 def test_empty_call_is_a_no_op():

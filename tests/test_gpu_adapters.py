@@ -1,6 +1,7 @@
 """hq_adapters against float64: one row to many, ragged widths, every rank, rows of
 mixed adapters, of runs and of none, ids outside the range, the epilogue's parts, base
-in place or absent, non-finite rows, neighbours, streams and graph replays.
+in place or absent, non-finite rows, neighbours, streams and graph replays, row by row
+(no workspace) and in tiles of rows (with one).
 
 Tolerance. u = A x sums K products in fp32 in some order: K + 1 roundings of the
 absolute products, one more for the scale. B u sums `rank` products: rank + 4 roundings
@@ -71,6 +72,10 @@ def run(T, K, N, r, count=3, dt=hq.BF16, ydt=None, kind="runs", act="none", resi
     return Y
 
 
+def in_tiles(T, K, N, r, dt):
+    return hq.adapters_workspace_bytes(hq.AdapterDesc(K, N, r, dt, dt, dt), T) > 0
+
+
 ROWS = [1, 2, 3, 5, 15, 16, 17, 31, 33, 63, 64, 65, 130, 257, 300]
 
 
@@ -83,10 +88,29 @@ def test_rows_and_widths(kind, K, N, dt):
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("K,N", [(8, 8), (16, 24), (72, 136), (136, 128), (264, 392)])
+@pytest.mark.parametrize("kind", ["runs", "mixed", "one"])
+def test_tiles_and_widths(kind, K, N, dt):
+    for T in (2049, 2063, 2064, 2065, 2079, 2081, 2111, 2112, 2113, 2300):
+        assert in_tiles(T, K, N, 16, dt)
+        run(T, K, N, 16, dt=dt, kind=kind)
+
+
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 @pytest.mark.parametrize("r", list(range(8, 129, 8)))
 def test_ranks(r, dt):
-    for T, kind in ((1, "one"), (24, "mixed"), (200, "runs"), (700, "runs"), (1100, "mixed")):
+    for T, kind in ((1, "one"), (24, "mixed"), (200, "runs"), (2049, "runs"), (2100, "mixed")):
+        assert in_tiles(T, 328, 456, r, dt) == (T > 2000)
         run(T, 328, 456, r, 4, dt, kind=kind)
+
+
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+@pytest.mark.parametrize("T,K,N,r", [(65, 4096, 4096, 128), (257, 4096, 2048, 64), (300, 8200, 520, 128), (513, 6152, 3080, 24),
+                                     (1100, 2056, 2056, 64)])
+def test_few_tiles_share_their_k(T, K, N, r, dt):
+    # u in several parts, chunks that end inside a row
+    for kind in ("runs", "mixed"):
+        run(T, K, N, r, 5, dt, kind=kind)
 
 
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
@@ -102,12 +126,36 @@ def test_sizes(T, K, N, r, n, kind, dt):
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 @pytest.mark.parametrize("ydt", [hq.BF16, hq.F32])
 def test_types_and_epilogues(act, dt, ydt):
-    for T in (7, 90, 800):
+    for T in (7, 90, 2100):
         run(T, 72, 200, 16, 3, dt, ydt, act=act)
         run(T, 72, 200, 16, 3, dt, ydt, act=act, residual=True, gate_rows=T // 3 + 1)
         run(T, 72, 200, 16, 3, dt, ydt, act=act, residual=True, inplace="residual")
         run(T, 72, 200, 16, 3, dt, ydt, act=act, gate_rows=1, inplace="base")
         run(T, 72, 200, 16, 3, dt, ydt, act=act, scaled=False, based=False)
+
+
+@pytest.mark.parametrize("T", [3, 200, 2100])
+def test_large_base_is_added_once(T):
+    # what the adapter adds is summed by itself: a base a thousand times as large rounds it once
+    X, A, B, ids, scales, base, _ = make(T, 264, 392, 128, 3, hq.F32)
+    base = 1000.0 * base
+    y, tol = epilogue64(*adapted64(X, A, B, ids, scales, base), "none", hq.F32)
+    assert_within(hq.adapters(hq.AdapterDesc(264, 392, 128), X, A, B, ids, scales, base), y, tol, f"T={T}")
+
+
+@pytest.mark.parametrize("T", [2, 2100])
+def test_parts_of_u_are_exact(T):
+    # a bf16 product of u = a few large and a few small parts that cancel in B u: an error of 2^-16 or
+    # of 2^-8 of u would be all that is left
+    K, N, r = 64, 128, 16
+    X = torch.ones(T, K, device="cuda", dtype=torch.bfloat16)
+    A = torch.zeros(1, r, K, device="cuda", dtype=torch.bfloat16)
+    A[0, 0, 0], A[0, 0, 1], A[0, 0, 2] = 1.0, 2.0 ** -9, 2.0 ** -18
+    A[0, 1, 0], A[0, 1, 1] = 1.0, 2.0 ** -9
+    B = torch.zeros(1, N, r, device="cuda", dtype=torch.bfloat16)
+    B[0, :, 0], B[0, :, 1] = 1.0, -1.0
+    Y = hq.adapters(hq.AdapterDesc(K, N, r, hq.BF16, hq.BF16, hq.F32), X, A, B, torch.zeros(T, dtype=torch.int32, device="cuda"))
+    assert (Y == 2.0 ** -18).all()
 
 
 @pytest.mark.parametrize("T", [1, 40, 600, 3000])
@@ -127,7 +175,7 @@ def test_rows_without_an_adapter(T, dt):
     assert torch.equal(hq.adapters(desc, X, A[:0].contiguous(), B[:0].contiguous(), ids, None, base), base)
 
 
-@pytest.mark.parametrize("T", [40, 600])
+@pytest.mark.parametrize("T", [40, 600, 2100])
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 def test_non_finite_values_stay_in_their_row_and_adapter(T, dt):
     X, A, B, ids, scales, base, _ = make(T, 264, 392, 16, 4, dt, kind="mixed")
@@ -146,7 +194,8 @@ def test_non_finite_values_stay_in_their_row_and_adapter(T, dt):
     assert torch.isnan(got[ids == 1]).all() and torch.equal(got[ids != 1], ref[ids != 1])
 
 
-@pytest.mark.parametrize("T,K,N,r", [(1, 8, 8, 8), (5, 72, 136, 16), (33, 264, 200, 24), (700, 72, 136, 40)])
+@pytest.mark.parametrize("T,K,N,r", [(1, 8, 8, 8), (5, 72, 136, 16), (33, 264, 200, 24), (700, 72, 136, 40), (2049, 72, 136, 40),
+                                     (2063, 8, 8, 8), (2100, 264, 200, 72), (2049, 136, 264, 128)])
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 def test_memory_around_the_operands(T, K, N, r, dt):
     # what lies around X, A and B does not enter, what lies around Y and the workspace stays
@@ -182,7 +231,8 @@ def test_offsets_past_32_bits(dt, T, K, N):
         assert_within(Y[part], *epilogue64(*adapted64(X[part], A, B, ids[part], scales, None), "none", dt), f"rows from {at}")
 
 
-@pytest.mark.parametrize("T,K,N,r,kind", [(1, 1152, 4608, 16, "one"), (24, 4096, 1152, 16, "mixed"), (1000, 1160, 2312, 32, "runs")])
+@pytest.mark.parametrize("T,K,N,r,kind", [(1, 1152, 4608, 16, "one"), (24, 4096, 1152, 16, "mixed"), (1000, 1160, 2312, 32, "runs"),
+                                          (2500, 264, 520, 64, "mixed")])
 def test_streams_and_graph_replays(T, K, N, r, kind):
     desc = hq.AdapterDesc(K, N, r, hq.BF16, hq.BF16, hq.BF16)
     Xa, A, B, ids, scales, base, _ = make(T, K, N, r, 4, hq.BF16, kind=kind)
