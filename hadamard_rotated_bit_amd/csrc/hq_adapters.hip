@@ -2,10 +2,11 @@
 //
 //   Y[t] = R[t] + g[t / gate_rows] phi(base[t] + s_a B_a (A_a x[t])),   a = ids[t],
 //
-// A_a [rank, K], B_a [N, rank]; a row whose id names no adapter has base alone, and its
-// x is not read. Sums are fp32; u = s_a A_a x stays in fp32 between the two products.
-// Bound by memory: base is read and Y written once, x once, each adapter once per row or
-// tile that uses it (from the caches).
+// A_a [rank, K], B_a [N, rank]; a row whose id names no adapter has base alone. Sums are
+// fp32; u = s_a A_a x keeps 24 bits between the two products. Bound by memory: base is
+// read and Y written once, x once, each adapter once per row or tile that uses it (from
+// the caches). Few rows take one launch, a block per row (adapt_rows_kernel); many take
+// tiles of rows on the matrix units, a launch for each product.
 #include "hq_epilogue.h"
 #include "hq_gemm_kernel.h"
 #include "hq_internal.h"
@@ -47,8 +48,10 @@ __device__ __forceinline__ void get16(const uint4& q, float* v) {
 // Y of one row (block x) and a part of its columns (block y; each part takes the row's u
 // for itself: one launch). Eight waves share the rank indexes of u, JW each, all their
 // loads of U strips of K in flight; then 64 columns a wave at a time: B_a's rows pass
-// through the wave's own LDS, read in whole lines, so that each lane has a column.
-// 24 rows of 4096 -> 4096 rank 16: see the launcher.
+// through the wave's own LDS, read in whole lines, so that each lane has a column. Bound
+// by the chain of a launch, the id, A_a and x, B_a and the store for few rows (24 rows of
+// 4096 -> 4096 rank 16: 6.0 us) and by instruction issue for many: two or four rows a block
+// that share what they fetch are no faster (700 rows of 1024 -> 1024 rank 8: 7.7, 7.8, 8.7).
 template <typename TE, int JW, int U>
 __global__ __launch_bounds__(512) void adapt_rows_kernel(AdaptArgs k) {
   constexpr int PER = 16 / sizeof(TE);             // elements of 16 bytes
@@ -241,7 +244,9 @@ __device__ __forceinline__ int tile_id(const AdaptArgs& k, int64_t r0, int r) {
 // own order, 16 rows in consecutive lanes, costs the address unit four times as much),
 // passes it through its own part of the LDS (slot c ^ (r / 2) mod 8 of row r: 16 lanes
 // read 16 distinct positions of the 64 banks) and has the next chunk's loads in flight
-// meanwhile. The waves' sums are joined in LDS in wave order.
+// meanwhile. The waves' sums are joined in LDS in wave order. 8192 x 4096 rank 64: 27 us,
+// 7.3 TB/s of x and A_a through the L2s (2.5 TB/s of x from memory); tiles of 64 rows, which
+// halve A_a's part, 25 us but two parts of u to add; two chunks in flight no gain.
 template <typename TE, int MT, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
@@ -257,91 +262,89 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   const uint32_t ldb = uint32_t(k.K) * sizeof(TE);
   uint8_t* const mine = smem + w * LROWS * 128;
   const int urow = lane >> 3, piece = lane & 7;
-  {
-    const int64_t r0 = tile_of_block() * ROWS;
-    if (r0 >= k.T) return;
-    const int split = int(blockIdx.y);
-    const int c1 = int(int64_t(chunks) * (split + 1) / k.splits);
-    const int rows = int(min(k.T - r0, int64_t(ROWS)));
-    const uint8_t* const x = static_cast<const uint8_t*>(k.x) + r0 * ldb;
-    uint32_t off[UNITS];   // of the lane's rows of x and of A_a
+  const int64_t r0 = tile_of_block() * ROWS;
+  if (r0 >= k.T) return;
+  const int split = int(blockIdx.y);
+  const int c1 = int(int64_t(chunks) * (split + 1) / k.splits);
+  const int rows = int(min(k.T - r0, int64_t(ROWS)));
+  const uint8_t* const x = static_cast<const uint8_t*>(k.x) + r0 * ldb;
+  uint32_t off[UNITS];   // of the lane's rows of x and of A_a
 #pragma unroll
-    for (int n = 0; n < UNITS; ++n) {
-      const int r = 8 * n + urow;
-      off[n] = uint32_t(r < ROWS ? min(r, rows - 1) : min(r - ROWS, k.rank - 1)) * ldb + 16 * piece;
-    }
-    const int id = lane < ROWS ? tile_id(k, r0, lane) : -1;
-    for (uint64_t left = __ballot(id >= 0); left;) {   // the same for every wave
-      const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-      const uint64_t match = __ballot(id == a);
-      left &= ~match;
-      const uint8_t* const A = static_cast<const uint8_t*>(k.a) + int64_t(a) * k.rank * ldb;
-      uint4 st[UNITS];
-      auto load = [&](int c) {   // zeros past the end of a row
-        if (uint32_t(c + 1) * 128 <= ldb) {
+  for (int n = 0; n < UNITS; ++n) {
+    const int r = 8 * n + urow;
+    off[n] = uint32_t(r < ROWS ? min(r, rows - 1) : min(r - ROWS, k.rank - 1)) * ldb + 16 * piece;
+  }
+  const int id = lane < ROWS ? tile_id(k, r0, lane) : -1;
+  for (uint64_t left = __ballot(id >= 0); left;) {   // the same for every wave
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const uint64_t match = __ballot(id == a);
+    left &= ~match;
+    const uint8_t* const A = static_cast<const uint8_t*>(k.a) + int64_t(a) * k.rank * ldb;
+    uint4 st[UNITS];
+    auto load = [&](int c) {   // zeros past the end of a row
+      if (uint32_t(c + 1) * 128 <= ldb) {
 #pragma unroll
-          for (int n = 0; n < UNITS; ++n) st[n] = load16((n < 2 * MT ? x : A) + c * 128, off[n]);
-        } else {
-          const bool ok = uint32_t(c) * 128 + 16 * piece < ldb;
+        for (int n = 0; n < UNITS; ++n) st[n] = load16((n < 2 * MT ? x : A) + c * 128, off[n]);
+      } else {
+        const bool ok = uint32_t(c) * 128 + 16 * piece < ldb;
 #pragma unroll
-          for (int n = 0; n < UNITS; ++n)
-            st[n] = ok ? load16((n < 2 * MT ? x : A) + c * 128, off[n]) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      v4f acc[MT][RT] = {};
-      const int c0 = int(int64_t(chunks) * split / k.splits) + w;
-      const int nc = c0 < c1 ? (c1 - c0 + NW - 1) / NW : 0;
-      int jc = nc ? int(blockIdx.x % unsigned(nc)) : 0;   // row tiles start apart
-      if (nc) load(c0 + NW * jc);
-#pragma unroll 1
-      for (int n = 0; n < nc; ++n) {
-        jc = jc + 1 < nc ? jc + 1 : 0;
-#pragma unroll
-        for (int n = 0; n < UNITS; ++n) {
-          const int r = 8 * n + urow;
-          *reinterpret_cast<uint4*>(mine + r * 128 + 16 * (piece ^ ((r >> 1) & 7))) = st[n];
-        }
-        if (n + 1 < nc) load(c0 + NW * jc);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          F fx[MT], fa[RT];
-          const int slot = 16 * ((4 * s + g) ^ ((i >> 1) & 7));
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            fx[m].q = *reinterpret_cast<const uint4*>(mine + (16 * m + i) * 128 + slot);
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-            fa[t].q = *reinterpret_cast<const uint4*>(mine + (ROWS + 16 * t + i) * 128 + slot);
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) acc[m][t] = frag_mfma<TE>(fx[m], fa[t], acc[m][t]);
-        }
+        for (int n = 0; n < UNITS; ++n)
+          st[n] = ok ? load16((n < 2 * MT ? x : A) + c * 128, off[n]) : make_uint4(0, 0, 0, 0);
       }
-      float* const red = reinterpret_cast<float*>(smem);   // [NW][ROWS][RP]
-      float* const u = k.u + int64_t(split) * k.T * k.rank;
+    };
+    v4f acc[MT][RT] = {};
+    const int c0 = int(int64_t(chunks) * split / k.splits) + w;
+    const int nc = c0 < c1 ? (c1 - c0 + NW - 1) / NW : 0;
+    int jc = nc ? int(blockIdx.x % unsigned(nc)) : 0;   // row tiles start apart
+    if (nc) load(c0 + NW * jc);
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+      jc = jc + 1 < nc ? jc + 1 : 0;
 #pragma unroll
-      for (int t0 = 0; t0 < RT; t0 += RJ) {
-        lds_barrier();   // the chunks and the last sums are read
+      for (int n = 0; n < UNITS; ++n) {
+        const int r = 8 * n + urow;
+        *reinterpret_cast<uint4*>(mine + r * 128 + 16 * (piece ^ ((r >> 1) & 7))) = st[n];
+      }
+      if (c + 1 < nc) load(c0 + NW * jc);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        F fx[MT], fa[RT];
+        const int slot = 16 * ((4 * s + g) ^ ((i >> 1) & 7));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          fx[m].q = *reinterpret_cast<const uint4*>(mine + (16 * m + i) * 128 + slot);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          fa[t].q = *reinterpret_cast<const uint4*>(mine + (ROWS + 16 * t + i) * 128 + slot);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int t = 0; t < RJ; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              red[(w * ROWS + 16 * m + 4 * g + e) * RP + 16 * t + i] = acc[m][t0 + t][e];
-        lds_barrier();
-#pragma unroll 1
-        for (int o = int(threadIdx.x); o < ROWS * 16 * RJ; o += 64 * NW) {
-          const int row = o / (16 * RJ), j = o - row * (16 * RJ);
-          float s = red[row * RP + j];
-#pragma unroll
-          for (int n = 1; n < NW; ++n) s += red[(n * ROWS + row) * RP + j];
-          if (((match >> row) & 1) && 16 * t0 + j < k.rank) u[(r0 + row) * k.rank + 16 * t0 + j] = s;
-        }
+          for (int t = 0; t < RT; ++t) acc[m][t] = frag_mfma<TE>(fx[m], fa[t], acc[m][t]);
       }
-      lds_barrier();   // the sums are read
     }
+    float* const red = reinterpret_cast<float*>(smem);   // [NW][ROWS][RP]
+    float* const u = k.u + int64_t(split) * k.T * k.rank;
+#pragma unroll
+    for (int t0 = 0; t0 < RT; t0 += RJ) {
+      lds_barrier();   // the chunks and the last sums are read
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < RJ; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            red[(w * ROWS + 16 * m + 4 * g + e) * RP + 16 * t + i] = acc[m][t0 + t][e];
+      lds_barrier();
+#pragma unroll 1
+      for (int o = int(threadIdx.x); o < ROWS * 16 * RJ; o += 64 * NW) {
+        const int row = o / (16 * RJ), j = o - row * (16 * RJ);
+        float s = red[row * RP + j];
+#pragma unroll
+        for (int n = 1; n < NW; ++n) s += red[(n * ROWS + row) * RP + j];
+        if (((match >> row) & 1) && 16 * t0 + j < k.rank) u[(r0 + row) * k.rank + 16 * t0 + j] = s;
+      }
+    }
+    lds_barrier();   // the sums are read
   }
 }
 
@@ -350,9 +353,11 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
 // three bf16 parts, 24 bits). B_a goes slab by slab through registers and two buffers in
 // LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
-// with 256 bytes of a bf16 row: base, residual and Y move in whole lines. SU: k-steps of
-// the product. EXT: an activation, a gate or a residual (without them the kernel is a third
-// of the code, which a short launch has to fetch first).
+// with 256 bytes of a bf16 row: base, residual and Y move in whole lines. 8192 x 4096 rank
+// 64: 34 us, 3.9 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 41 us (the same
+// loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: an activation, a
+// gate or a residual (without them the kernel is a third of the code, which a short launch
+// has to fetch first).
 template <typename TE, typename TY, int SU, bool EXT>
 __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
@@ -636,27 +641,30 @@ hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
 
 // One row after the other or tiles of rows? Row by row each row fetches its adapter's
 // factors (from the caches), in tiles each adapter of a tile is fetched once, but there
-// are two launches and a chain of waits in each. With runs of rows the two cross where the
-// rows fetch 120 MB (us, rows / tiles: 700 rows of 1024 -> 1024 rank 8, 23 MB, 9.3 / 13.9;
-// 600 of 2048 -> 2048 rank 16, 79 MB, 11.3 / 13.4; 300 of 4096 -> 1152 rank 32, 101 MB,
-// 14.3 / 15.0; 1037 of 1160 -> 2312 rank 8 fp32, 115 MB, 19.1 / 20.5; 1000 of 1160 -> 2312 rank 32, 222 MB, 28 / 16.4) or where they are many
-// (4000 of 256 -> 512 rank 16, 98 MB, 19.5 / 13.3). With an adapter per row rows win by far
-// (256 rows of 2048 -> 2048, rank 32, 64 adapters: 14.4 / 105): the ids are on the device,
-// so batches of a decoding step's size count as mixed.
-bool by_rows(int64_t T, int K, int N, int rank, int esize) {
-  const double mb = double(T) * rank * (double(K) + N) * esize / 1e6;
-  return T <= 4 || (T <= 256 && mb <= 256.0) || (T <= 2048 && mb <= 120.0);
+// are two launches and a chain of waits in each. Rows are bound by issue, so the rule counts
+// products. With runs of rows the two cross at 40 million (us, rows / tiles, no epilogue:
+// 700 rows of 1024 -> 1024 rank 8 bf16, 11 million, 7.7 / 10.9; 600 of 2048 -> 2048 rank 16
+// bf16, 39 million, 10.9 / 11.0; 1037 of 2160 -> 2312 rank 8 fp32, 37 million, 20.4 / 19.7;
+// 300 of 4096 -> 1152 rank 32 bf16, 50 million, 13.7 / 12.2; 1000 of 1160 -> 2312 rank 32
+// bf16, 111 million, 24 / 12.3) or where the rows are many (4000 of 256 -> 512 rank 16 bf16
+// 19.2 / 10.8). With an adapter per row rows win by far (256 rows of 2048 -> 2048, rank 32,
+// 64 adapters: 14.2 / 80; 512 rows, 128 adapters: 21.6): the ids are on the device, so
+// batches of a decoding step's size count as mixed up to 2^27 products, 256 rows of
+// 4096 -> 4096 rank 64.
+bool by_rows(int64_t T, int K, int N, int rank) {
+  const double products = double(T) * rank * (double(K) + N);
+  return T <= 4 || (T <= 512 && products <= 0x1p27) || (T <= 2048 && products <= 40e6);
 }
 
 }  // namespace
 
 size_t adapters_part_bytes(int64_t T, int K, int N, int rank, int esize) {
-  if (by_rows(T, K, N, rank, esize)) return 0;
+  if (by_rows(T, K, N, rank)) return 0;
   return size_t(down_splits(T, K, esize)) * size_t(T) * size_t(rank) * 4;
 }
 
 hipError_t launch_adapters(const AdaptArgs& a, hipStream_t s) {
-  if (by_rows(a.T, a.K, a.N, a.rank, a.bf16 ? 2 : 4))
+  if (by_rows(a.T, a.K, a.N, a.rank))
     return a.bf16 ? launch_rows<uint16_t>(a, s) : launch_rows<float>(a, s);
   return a.bf16 ? launch_tiles<uint16_t>(a, s) : launch_tiles<float>(a, s);
 }

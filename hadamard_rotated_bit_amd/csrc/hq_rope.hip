@@ -104,7 +104,9 @@ __device__ __forceinline__ Raw8<TE> unit_load(const TE* p, uint32_t o0, uint32_t
 
 // A wave per token and part of its heads (`split` parts per token); a head's D / 8 units
 // of 8 channels go to D / 8 lanes, 64 / (D / 8) heads at a time, the next ones' loads in
-// flight meanwhile (and the first ones' during the angles).
+// flight meanwhile (and the first ones' during the angles). 24576 tokens of 32 heads of 128
+// bf16: 79 us, 5.1 TB/s; 8192 of 32 heads of 72, normed: 15.8 us, 4.8 TB/s (nine lanes a
+// head, whose sums pass through LDS); three tokens of 40 heads: 4.2 us.
 template <typename TE, typename TY, bool HALVES, bool NORM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
   __shared__ __attribute__((aligned(16))) float cs[4][2][ROPE_MAX_PAIRS];

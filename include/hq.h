@@ -533,14 +533,15 @@ size_t hq_adapters_workspace_bytes(const hq_adapter_desc* desc, int64_t T);
  * then the epilogue above: Y = residual + gate phi(V).
  *  X [T, d_in] x_dtype; A [count, rank, d_in], B [count, d_out, rank] w_dtype (NULL
  *  with count = 0); ids int32 [T] (4-byte aligned), any value outside 0 .. count - 1:
- *  no adapter (V = base, and X[t] is not read); scales f32 [count] or NULL (ones);
+ *  no adapter (V = base: X[t] takes no part); scales f32 [count] or NULL (ones);
  *  base [T, d_out] y_dtype or NULL (zeros), possibly Y itself; Y [T, d_out] y_dtype;
  *  epilogue NULL or as above; workspace at least hq_adapters_workspace_bytes(desc, T)
  *  bytes (NULL when that is 0), not shared with a concurrent call. T up to 2^26; T = 0
  *  is a no-op. Neither Y nor the workspace may overlap another operand or each other,
  *  but for base and residual, either of which may be Y. The products are summed in
- *  fp32 and A_a X[t] stays fp32 between them; the same inputs always give the same
- *  bits. NaN and infinities stay in their row. */
+ *  fp32 and A_a X[t] keeps 24 bits between them; the same inputs always give the same
+ *  bits (a row's depend on the T rows of its call only by the order of its sums). NaN
+ *  and infinities stay in their row. */
 int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const void* B,
                 int32_t count, const int32_t* ids, const float* scales, const void* base, int64_t T,
                 const hq_epilogue* epilogue, void* Y, void* workspace, size_t workspace_bytes,
