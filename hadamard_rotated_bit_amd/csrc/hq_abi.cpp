@@ -1254,7 +1254,8 @@ int hq_rope(const hq_rope_desc* desc, const void* X, int64_t ldx, const void* po
     return fail(HQ_ERR_INVALID_ARG, "positions must be 4-byte aligned");
   const size_t nx = size_t((T - 1) * ldx + width) * dtype_size(desc->x_dtype);
   const size_t ny = size_t((T - 1) * ldy + width) * dtype_size(desc->y_dtype);
-  const bool in_place = X == Y && ldx == ldy && desc->x_dtype == desc->y_dtype;
+  const bool in_place =   // the pitch of a single row has no meaning
+      X == Y && (ldx == ldy || T == 1) && desc->x_dtype == desc->y_dtype;
   if (!in_place && overlap(X, nx, Y, ny))
     return fail(HQ_ERR_INVALID_ARG,
                 "Y overlaps X (it may be X itself, in the same type and pitch)");

@@ -164,6 +164,17 @@ def test_in_place_in_a_packed_projection(dt, norm, layout):
     assert torch.equal(out, ref) and (buf[:, :8] == 3.0).all() and (buf[:, 8 + 7 * 72:] == 3.0).all()
 
 
+@pytest.mark.parametrize("T", [1, 2])
+def test_in_place_by_a_view_of_the_heads(T):
+    # X: the q and k columns of a packed row, out: the whole row
+    d = hq.RopeDesc(3, 1, 64, (16,), norm=True)
+    Z, pos, f, (gq, gk) = make(T, d, extra=64)
+    ref = hq.rope(d, Z, pos, f, gq, gk)
+    v = Z[:, 256:].clone()
+    hq.rope(d, Z[:, :256], pos, f, gq, gk, out=Z)
+    assert torch.equal(Z[:, :256], ref) and torch.equal(Z[:, 256:], v)
+
+
 def test_non_finite_values_stay_in_their_head():
     d = hq.RopeDesc(4, 2, 64, (16, 16), norm=True)
     X, pos, f, (gq, gk) = make(70, d)
