@@ -171,9 +171,22 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
         float q = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-        q = fmaf(run_sum(q, slot * U, U, u), inv, k.eps);
+        q = run_sum(q, slot * U, U, u);
+        const bool large = q == INFINITY;
+        q = fmaf(q, inv, k.eps);
         // rsq takes no squares below the smallest normal floats
-        const float rstd = q >= 0x1p-100f ? __builtin_amdgcn_rsqf(q) : 1.0f / sqrtf(q);
+        float rstd = q >= 0x1p-100f ? __builtin_amdgcn_rsqf(q) : 1.0f / sqrtf(q);
+        if (__any(large)) {   // squares past the largest float: once more, of x 2^-80
+          float z = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float t = v[e] * 0x1p-80f;
+            z = fmaf(t, t, z);
+            v[e] = large ? t : v[e];
+          }
+          z = run_sum(z, slot * U, U, u);
+          if (large) rstd = 1.0f / sqrtf(fmaf(z, inv, k.eps * 0x1p-80f * 0x1p-80f));
+        }
         const bool isq = head < k.Hq;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * (isq ? gq[e] : gk[e]);

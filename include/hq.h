@@ -507,8 +507,9 @@ int hq_rope_validate(const hq_rope_desc* desc);
  *  positions [T, axes] int32 or f32 (4-byte aligned); freqs f64 [pairs of all axes],
  *  radians per position; gamma_q, gamma_k f32 [head_dim] or NULL (ones; must be NULL
  *  without norm). T up to 2^26; T = 0 is a no-op.
- * Angles are reduced to a turn in 64 bits; cos, sin and all else are fp32. A position
- * that is not finite gives NaN in its row's rotated channels. */
+ * Angles are reduced to a turn in 64 bits; cos, sin and all else are fp32. Heads whose
+ * squares pass the largest float are normed like others; NaN and infinities stay in
+ * their head; a position that is not finite gives NaN in its row's rotated channels. */
 int hq_rope(const hq_rope_desc* desc, const void* X, int64_t ldx, const void* positions,
             const double* freqs, const float* gamma_q, const float* gamma_k, int64_t T, void* Y,
             int64_t ldy, void* stream);

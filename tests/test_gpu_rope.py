@@ -175,6 +175,18 @@ def test_in_place_by_a_view_of_the_heads(T):
     assert torch.equal(Z[:, :256], ref) and torch.equal(Z[:, 256:], v)
 
 
+@pytest.mark.parametrize("D,pairs", [(64, (16, 16)), (72, (20,)), (256, (64, 64))])
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+def test_squares_past_the_largest_float(D, pairs, dt):
+    # beside heads of ordinary size
+    d = hq.RopeDesc(5, 3, D, pairs, norm=True, x_dtype=dt, y_dtype=hq.F32)
+    X, pos, f, (gq, gk) = make(90, d)
+    v = X.view(90, 8, D)
+    v[:, 1], v[::2, 6] = v[:, 1] * 2.0 ** 80, v[::2, 6] * 2.0 ** 66
+    v[5:9, 4] = torch.where(v[5:9, 4] < 0, -3e38, 3e38)
+    within(hq.rope(d, X, pos, f, gq, gk), *rope64(d, X, pos, f, gq, gk), hq.F32, f"D={D} dt={dt}")
+
+
 def test_non_finite_values_stay_in_their_head():
     d = hq.RopeDesc(4, 2, 64, (16, 16), norm=True)
     X, pos, f, (gq, gk) = make(70, d)
