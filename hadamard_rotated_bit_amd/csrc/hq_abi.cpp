@@ -410,6 +410,9 @@ int check_positions(int64_t S, int64_t P) {
 
 // ---- RMS norm, rotary positions, adapters -------------------------------------
 
+// The least eps of a mean square: what fp32 loses of smaller squares does not tell beside it.
+constexpr float kLeastEps = 0x1p-100f;
+
 int check_rms_desc(const hq_rms_desc* d) {
   if (!d) return fail(HQ_ERR_INVALID_ARG, "desc is NULL");
   if (d->channels <= 0)
@@ -421,6 +424,8 @@ int check_rms_desc(const hq_rms_desc* d) {
     return fail(HQ_ERR_INVALID_ARG, "outputs must be a sum of HQ_RMS_* (got %d)", d->outputs);
   if (!(d->eps > 0.0f) || !std::isfinite(d->eps))
     return fail(HQ_ERR_INVALID_ARG, "eps must be finite and > 0 (got %g)", double(d->eps));
+  if (d->eps < kLeastEps)
+    return fail(HQ_ERR_UNSUPPORTED, "eps must be at least 2^-100 (got %g)", double(d->eps));
   if (d->channels % 8 || d->channels > hq::RMS_MAX_C)
     return fail(HQ_ERR_UNSUPPORTED, "channels must be a multiple of 8 up to %d (got %d)",
                 hq::RMS_MAX_C, d->channels);
@@ -456,6 +461,8 @@ int check_rope_desc(const hq_rope_desc* d) {
   if (st != HQ_OK) return st;
   if (d->norm && (!(d->eps > 0.0f) || !std::isfinite(d->eps)))
     return fail(HQ_ERR_INVALID_ARG, "eps must be finite and > 0 (got %g)", double(d->eps));
+  if (d->norm && d->eps < kLeastEps)
+    return fail(HQ_ERR_UNSUPPORTED, "eps must be at least 2^-100 (got %g)", double(d->eps));
   if (d->norm && d->inverse)
     return fail(HQ_ERR_UNSUPPORTED, "inverse takes no norm (it would not undo one)");
   if (d->q_heads > 1024 || d->k_heads > 1024 || d->q_heads + d->k_heads < 1 ||

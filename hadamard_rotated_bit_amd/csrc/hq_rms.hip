@@ -182,9 +182,8 @@ __global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(R
       }
       turn ^= 1;
     }
-    const float ms = fmaf(s2, k.inv_c, k.eps);
-    // rsq (one unit) takes no squares below the smallest normal floats
-    float rstd = ms >= 0x1p-100f ? __builtin_amdgcn_rsqf(ms) : 1.0f / sqrtf(ms);
+    // rsq is off by one unit; eps keeps it from the smallest floats, which it does not take
+    float rstd = __builtin_amdgcn_rsqf(fmaf(s2, k.inv_c, k.eps));
     if (__any(s2 == INFINITY)) {
       // squares past the largest float: once more, of h 2^-80 (the same branch for a
       // whole block where a block has one row)

@@ -173,9 +173,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
         for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
         q = run_sum(q, slot * U, U, u);
         const bool large = q == INFINITY;
-        q = fmaf(q, inv, k.eps);
-        // rsq takes no squares below the smallest normal floats
-        float rstd = q >= 0x1p-100f ? __builtin_amdgcn_rsqf(q) : 1.0f / sqrtf(q);
+        // rsq is off by one unit; eps keeps it from the smallest floats, which it does not take
+        float rstd = __builtin_amdgcn_rsqf(fmaf(q, inv, k.eps));
         if (__any(large)) {   // squares past the largest float: once more, of x 2^-80
           float z = 0.0f;
 #pragma unroll

@@ -432,7 +432,7 @@ int hq_group_norm_plan(const hq_norm_desc* desc, int64_t samples, int64_t positi
 
 /* RMS norm descriptor: channels a multiple of 8 up to 8192; outputs any of
  * HQ_RMS_* (at least one); x_dtype (X, residual, H) and y_dtype (Y) any
- * hq_dtype; eps > 0. */
+ * hq_dtype; eps from 2^-100 (8e-31). */
 typedef enum {
   HQ_RMS_Y = 1,      /* the norm, in y_dtype                                    */
   HQ_RMS_SUM = 2,    /* h = X + residual, in x_dtype                            */
@@ -463,7 +463,7 @@ int hq_rms_validate(const hq_rms_desc* desc);
  * may be X or residual where the types are the same; otherwise the outputs must not
  * overlap an input or each other. Rows whose squares pass the largest float are normed
  * like others; NaN and infinities stay in their row; a row with an h gamma that is not
- * a finite float has codes of 0 and a NaN scale. */
+ * a finite float has codes of 0 and a NaN scale (and a Y that is not finite there). */
 int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, const float* gamma,
                 int64_t T, void* H, void* Y, int8_t* codes, float* scales, void* stream);
 
@@ -476,7 +476,7 @@ int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, co
  *            behind them are not rotated).
  *  layout    HQ_ROPE_PAIRS: pair i is (2i, 2i + 1); HQ_ROPE_HALVES: (i, i + P), P the
  *            pairs of all axes.
- *  norm      1: an RMS norm of each head (eps > 0) before its rotation; 0: none.
+ *  norm      1: an RMS norm of each head (eps from 2^-100) before its rotation; 0: none.
  *  inverse   1: the opposite rotation (the transposed map; norm must be 0).
  *  pos_dtype HQ_POS_I32 or HQ_POS_F32.
  *  x_dtype, y_dtype  any hq_dtype. */

@@ -129,6 +129,16 @@ def test_constant_and_zero_rows(C):
         assert ((o.y[1] - 1.0).abs() < 1e-6).all() and ((o.y[6] - 1.0).abs() < 1e-6).all()
 
 
+@pytest.mark.parametrize("C", [40, 1152, 4096])
+@pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
+def test_smallest_eps(C, dt):
+    # rows whose squares are about eps, above it and below the smallest floats
+    x, _, gamma = make(60, C, dt)
+    x = x * torch.tensor([2.0 ** -50, 2.0 ** -40, 2.0 ** -75], device="cuda").repeat(20)[:, None].to(x.dtype)
+    o = hq.rms_norm(hq.RmsNormDesc(C, 2.0 ** -100, ALL, dt, hq.F32), x, gamma)
+    compare(o, x, None, gamma, 2.0 ** -100, hq.F32, f"C={C} dt={dt}")
+
+
 @pytest.mark.parametrize("C", [40, 512, 1152, 4096])
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 def test_cancelling_residual(C, dt):

@@ -175,6 +175,15 @@ def test_in_place_by_a_view_of_the_heads(T):
     assert torch.equal(Z[:, :256], ref) and torch.equal(Z[:, 256:], v)
 
 
+@pytest.mark.parametrize("D,pairs", [(64, (16, 16)), (72, (20,))])
+def test_smallest_eps(D, pairs):
+    # heads whose squares are about eps, above it and below the smallest floats
+    d = hq.RopeDesc(2, 1, D, pairs, norm=True, eps=2.0 ** -100)
+    X, pos, f, (gq, gk) = make(90, d)
+    X = (X.view(90, 3, D) * torch.tensor([2.0 ** -50, 2.0 ** -40, 2.0 ** -75], device="cuda")[:, None]).view(90, 3 * D)
+    within(hq.rope(d, X, pos, f, gq, gk), *rope64(d, X, pos, f, gq, gk), hq.F32, f"D={D}")
+
+
 @pytest.mark.parametrize("D,pairs", [(64, (16, 16)), (72, (20,)), (256, (64, 64))])
 @pytest.mark.parametrize("dt", [hq.BF16, hq.F32])
 def test_squares_past_the_largest_float(D, pairs, dt):

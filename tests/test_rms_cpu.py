@@ -19,7 +19,7 @@ def ref(channels=256, outputs=7, x_dtype=1, y_dtype=1, eps=1e-6):
 @pytest.mark.parametrize("kw,status", [
     (dict(channels=0), -1), (dict(channels=-8), -1), (dict(outputs=0), -1), (dict(outputs=8), -1), (dict(outputs=-1), -1),
     (dict(x_dtype=2), -1), (dict(y_dtype=-1), -1), (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1),
-    (dict(eps=float("inf")), -1), (dict(channels=252), -2), (dict(channels=8200), -2)])
+    (dict(eps=float("inf")), -1), (dict(eps=1e-31), -2), (dict(eps=1e-44), -2), (dict(channels=252), -2), (dict(channels=8200), -2)])
 def test_descriptor_refusals(kw, status):
     assert lib.hq_rms_validate(ref(**kw)) == status
     assert len(lib.hq_last_error()) > 0
@@ -30,7 +30,7 @@ def test_no_descriptor():
     assert lib.hq_rms_norm(None, None, None, None, 0, None, None, None, None, None) == -1
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(channels=8), dict(channels=8192), dict(outputs=1), dict(x_dtype=0, y_dtype=1)])
+@pytest.mark.parametrize("kw", [dict(), dict(channels=8), dict(channels=8192), dict(outputs=1), dict(eps=2.0 ** -100), dict(x_dtype=0, y_dtype=1)])
 def test_descriptor_accepts(kw):
     assert lib.hq_rms_validate(ref(**kw)) == 0
 

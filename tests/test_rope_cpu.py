@@ -21,7 +21,7 @@ def ref(q=4, k=2, dim=64, pairs=(8, 24), axes=None, layout=0, norm=0, inverse=0,
     (dict(q=-1), -1), (dict(k=-1), -1), (dict(dim=0), -1), (dict(axes=0), -1), (dict(axes=5), -1), (dict(pairs=(-4, 8)), -1),
     (dict(pairs=(1 << 30, 1 << 30)), -1), (dict(layout=2), -1), (dict(layout=-1), -1), (dict(norm=2), -1), (dict(inverse=-1), -1),
     (dict(pos=2), -1), (dict(x=2), -1), (dict(y=-1), -1), (dict(norm=1, eps=0.0), -1), (dict(norm=1, eps=float("nan")), -1),
-    (dict(norm=1, inverse=1), -2), (dict(q=0, k=0), -2), (dict(q=1025), -2), (dict(q=1000, k=25), -2),
+    (dict(norm=1, eps=1e-31), -2), (dict(norm=1, inverse=1), -2), (dict(q=0, k=0), -2), (dict(q=1025), -2), (dict(q=1000, k=25), -2),
     (dict(q=2 ** 31 - 1, k=2 ** 31 - 1), -2), (dict(dim=60), -2), (dict(dim=264), -2), (dict(pairs=(8, 28)), -2),
     (dict(pairs=(8, 6)), -2), (dict(pairs=(0, 0)), -2)])
 def test_descriptor_refusals(kw, status):
@@ -30,7 +30,7 @@ def test_descriptor_refusals(kw, status):
 
 
 @pytest.mark.parametrize("kw", [dict(), dict(pairs=(3, 5)), dict(pairs=(0, 4, 0, 0)), dict(dim=8, pairs=(4,)), dict(dim=256, pairs=(128,)),
-                                dict(q=0, k=1), dict(q=1024, k=0), dict(norm=1), dict(inverse=1), dict(dim=72, pairs=(18, 18))])
+                                dict(q=0, k=1), dict(q=1024, k=0), dict(norm=1), dict(norm=1, eps=2.0 ** -100), dict(eps=0.0), dict(inverse=1), dict(dim=72, pairs=(18, 18))])
 def test_descriptor_accepts(kw):
     assert lib.hq_rope_validate(ref(**kw)) == 0
 
