@@ -835,7 +835,8 @@ def adapters(desc: AdapterDesc, X: torch.Tensor, A: torch.Tensor, B: torch.Tenso
     ``base`` [T, d_out] (absent: zeros). X [T, d_in], A [count, rank, d_in], B [count,
     d_out, rank], ids int32 [T] (outside 0 .. count - 1: no adapter). ``out`` may be
     base itself; ``workspace`` (adapters_workspace_bytes(desc, T) bytes) is allocated
-    when it is needed and not given."""
+    when it is needed and not given. Calls of more than 512 rows do best with rows of
+    one adapter next to each other; rows of many requests may go in a call of their own."""
     if X.dim() != 2:
         raise ValueError(f"X must be [T, d_in], got {tuple(X.shape)}")
     T, wdt, ydt = X.shape[0], _TORCH[desc.w_dtype], _TORCH[desc.y_dtype]

@@ -540,9 +540,13 @@ size_t hq_adapters_workspace_bytes(const hq_adapter_desc* desc, int64_t T);
  *  bytes (NULL when that is 0), not shared with a concurrent call. T up to 2^26; T = 0
  *  is a no-op. Neither Y nor the workspace may overlap another operand or each other,
  *  but for base and residual, either of which may be Y. The products are summed in
- *  fp32 and A_a X[t] keeps 24 bits between them; the same inputs always give the same
- *  bits (a row's depend on the T rows of its call only by the order of its sums). NaN
- *  and infinities stay in their row. */
+ *  fp32 and A_a X[t] keeps 24 bits between them (of 2^-110 to 3e38); the same inputs
+ *  always give the same bits (a row's depend on the T rows of its call only by the order
+ *  of its sums). NaN and infinities stay in their row.
+ * A batch of requests may have an adapter per row up to 512 rows (2^27 products T rank
+ * (d_in + d_out)). Longer calls take tiles of rows, which make a pass for each adapter
+ * among their rows: give them rows of one adapter next to each other, and the rows of
+ * many requests a call of their own. */
 int hq_adapters(const hq_adapter_desc* desc, const void* X, const void* A, const void* B,
                 int32_t count, const int32_t* ids, const float* scales, const void* base, int64_t T,
                 const hq_epilogue* epilogue, void* Y, void* workspace, size_t workspace_bytes,
