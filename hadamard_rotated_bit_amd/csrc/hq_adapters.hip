@@ -348,6 +348,8 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   }
 }
 
+constexpr int EXT_NONE = -1, EXT_ANY = 100;
+
 // Y of 64 rows (block x) and every gridDim.y-th slab of 128 columns, 16 rows a wave. A wave
 // keeps its rows' u in registers, added over its parts and scaled (for bf16 products as
 // three bf16 parts, 24 bits). B_a goes slab by slab through registers and two buffers in
@@ -355,10 +357,11 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
 // with 256 bytes of a bf16 row: base, residual and Y move in whole lines. 8192 x 4096 rank
 // 64: 34 us, 3.9 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 41 us (the same
-// loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: an activation, a
-// gate or a residual (without them the kernel is a third of the code, which a short launch
-// has to fetch first).
-template <typename TE, typename TY, int SU, bool EXT>
+// loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: EXT_NONE (no
+// activation, gate or residual), an activation known here, or EXT_ANY: a short launch has to
+// fetch its code first, and the first kind is a third of the last (1500 x 1152 -> 2304 rank
+// 16: 9.4 us with any activation, 8.8 with SiLU or a tanh GELU alone).
+template <typename TE, typename TY, int SU, int EXT>
 __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
   constexpr int NP = sizeof(TE) == 2 ? 3 : 1;
@@ -467,9 +470,11 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
     asm volatile("" : "+v"(at));   // addresses made here, not kept over the slabs
     at += e * rowb + 128 * slab * EY;
     ok = ok && 128 * slab + 8 * i < k.N;
-    if constexpr (EXT) {
+    if constexpr (EXT != EXT_NONE) {
       float t[8];
-      apply_act<8, EY == 4>(v, k.ep.act);
+      ActCoef act = k.ep.act;
+      if constexpr (EXT != EXT_ANY) act.act = EXT;
+      apply_act<8, EY == 4>(v, act);
       if (k.ep.gate) {
         if (ok) raw_get(raw_load(static_cast<const TY*>(k.ep.gate) + 128 * slab + 8 * i +
                                  int64_t(uint32_t(w0 + 4 * g + e) / uint32_t(k.ep.gate_rows)) * k.ep.gate_ld), t);
@@ -594,10 +599,15 @@ hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t groups = std::max<int64_t>(12, 512 / tiles);
   a.slabs = int((slabs + groups - 1) / groups);
   const dim3 grid(unsigned(tiles + 7) / 8 * 8, unsigned((slabs + a.slabs - 1) / a.slabs));
-  if (a.ep.act.act != ACT_NONE || a.ep.gate || a.ep.residual)
-    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, true>), grid, dim3(256), 0, s, a);
+  const int act = a.ep.act.act;
+  if (act == ACT_NONE && !a.ep.gate && !a.ep.residual)
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, EXT_NONE>), grid, dim3(256), 0, s, a);
+  else if (act == ACT_SILU)
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, ACT_SILU>), grid, dim3(256), 0, s, a);
+  else if (act == ACT_GELU_TANH)
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, ACT_GELU_TANH>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((adapt_up_tile_kernel<TE, TY, SU, EXT_ANY>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <typename TE, typename TY>
