@@ -356,7 +356,7 @@ constexpr int EXT_NONE = -1, EXT_ANY = 100;
 // LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
 // with 256 bytes of a bf16 row: base, residual and Y move in whole lines. 8192 x 4096 rank
-// 64: 34 us, 3.9 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 41 us (the same
+// 64: 34 us, 3.9 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 38 us (the same
 // loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: EXT_NONE (no
 // activation, gate or residual), an activation known here, or EXT_ANY: a short launch has to
 // fetch its code first, and the first kind is a third of the last (1500 x 1152 -> 2304 rank
@@ -416,6 +416,25 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
 #pragma unroll
       for (int h = 0; h < H; ++h) bb[e][h] = buf_load16(base, at + e * rowb + 16 * h);
   };
+  // The wave's u goes through its part of the second buffer: read in whole lines, PARTS
+  // parts of K at a time, and added in their order (read as the products take it, a part
+  // after the other, 256 rows of 2776 -> 4448 rank 128 fp32 take 96 us, 68 so).
+  constexpr uint32_t UP = F::KS * SU * 4 + 32;   // bytes of a row there
+  constexpr int NU = SU * F::KS / 16;            // 16-byte pieces of a part per lane
+  constexpr int PARTS = NU > 4 ? 1 : SU > 1 ? 2 : 4;
+  static_assert(4 * 16 * UP <= sizeof(bs[1]), "u of four waves");
+  uint8_t* const us = bs[1] + w * 16 * UP;
+  float4 uq[PARTS][NU];
+  auto load_u = [&](int n) {
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) {
+      const __amdgpu_buffer_rsrc_t U = make_rsrc(reinterpret_cast<const uint8_t*>(k.u + ((n + j) * k.T + w0) * k.rank),
+                                                 n + j < k.splits ? wrows * k.rank * 4 : 0);
+#pragma unroll
+      for (int z = 0; z < NU; ++z) uq[j][z] = __builtin_bit_cast(float4, buf_load16(U, 16 * (lane + 64 * z)));
+    }
+  };
+  load_u(0);
   if (all) load_b(s0, all);
   load_base(s0);
   // row n of a slab is row (n mod 8) 16 + n / 8 in LDS: the 16 lanes of MFMA t read neighbours
@@ -425,28 +444,43 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
     const uint32_t q = threadIdx.x + 256 * z, n = q / ppr;
     to[z] = ((n & 7) * 16 + (n >> 3)) * PITCH + 16 * (q - n * ppr);
   }
-  if (brow < SU * 64) {   // rank indexes past the last one
-    for (uint32_t o = threadIdx.x; o < 2 * 128 * PITCH / 16; o += 256)
-      reinterpret_cast<uint4*>(bs)[o] = make_uint4(0, 0, 0, 0);
-  }
   F fu[SU][NP] = {};   // row i's u, rank indexes KS s + PER g ..
   {
     const int a = __shfl(id, 16 * w + i, 64);
     const float scale = a >= 0 && k.scales ? k.scales[a] : 1.0f;
-    const float* const p = k.u + (w0 + i) * k.rank + F::PER * g;
+    float4 sum[NU] = {};
+#pragma unroll 1
+    for (int n = 0;;) {
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j)
+#pragma unroll
+        for (int z = 0; z < NU; ++z) {
+          sum[z].x += uq[j][z].x; sum[z].y += uq[j][z].y; sum[z].z += uq[j][z].z; sum[z].w += uq[j][z].w;
+        }
+      n += PARTS;
+      if (n >= k.splits) break;
+      load_u(n);
+    }
+#pragma unroll
+    for (int z = 0; z < NU; ++z) {
+      const uint32_t q = 4 * (lane + 64 * z), r = q / uint32_t(k.rank);
+      if (r < 16) *reinterpret_cast<float4*>(us + r * UP + 4 * (q - r * k.rank)) = sum[z];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
     for (int s = 0; s < SU; ++s) {
-      if (a < 0 || F::KS * s + F::PER * g >= k.rank) continue;
-      float f[F::PER] = {};
-      for (int n = 0; n < k.splits; ++n) {
-        const float4* const q = reinterpret_cast<const float4*>(p + F::KS * s + n * k.T * k.rank);
+      float f[F::PER];
+      const bool has = a >= 0 && F::KS * s + F::PER * g < k.rank;
 #pragma unroll
-        for (int h = 0; h < F::PER / 4; ++h) {
-          f[4 * h] += q[h].x; f[4 * h + 1] += q[h].y; f[4 * h + 2] += q[h].z; f[4 * h + 3] += q[h].w;
-        }
+      for (int h = 0; h < F::PER / 4; ++h) {
+        const float4 q = *reinterpret_cast<const float4*>(us + i * UP + 4 * (F::KS * s + F::PER * g + 4 * h));
+        f[4 * h] = has ? q.x * scale : 0.0f;
+        f[4 * h + 1] = has ? q.y * scale : 0.0f;
+        f[4 * h + 2] = has ? q.z * scale : 0.0f;
+        f[4 * h + 3] = has ? q.w * scale : 0.0f;
       }
-#pragma unroll
-      for (int e = 0; e < F::PER; ++e) f[e] *= scale;
       if constexpr (NP == 1) {
         fu[s][0].q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
       } else {
@@ -463,6 +497,11 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
         }
       }
     }
+  }
+  if (brow < SU * 64) {   // rank indexes past the last one
+    lds_barrier();        // every wave has its u
+    for (uint32_t o = threadIdx.x; o < 2 * 128 * PITCH / 16; o += 256)
+      reinterpret_cast<uint4*>(bs)[o] = make_uint4(0, 0, 0, 0);
   }
   // Y of row 4 g + e of the wave in a slab, from v = base + what the adapter adds, where ok
   auto finish = [&](float (&v)[8], int e, int slab, bool ok) {
@@ -543,15 +582,19 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
     const uint64_t match = __ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
     const uint32_t here = uint32_t(match >> (16 * w)) & inside;   // the wave's rows that have it
     v4f d[8] = {};
+    // fp32 products take the matrix units long enough to leave them to waves that have rows of
+    // this adapter (5783 x 312 -> 3512 rank 32, runs of 88 rows: 66 -> 61 us; bf16 no gain)
+    if (sizeof(TE) == 2 || here) {
 #pragma unroll
-    for (int s = 0; s < SU; ++s) {
+      for (int s = 0; s < SU; ++s) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        F fb;
-        fb.q = *reinterpret_cast<const uint4*>(bs[buf] + (16 * t + i) * PITCH + 64 * s + 16 * g);
+        for (int t = 0; t < 8; ++t) {
+          F fb;
+          fb.q = *reinterpret_cast<const uint4*>(bs[buf] + (16 * t + i) * PITCH + 64 * s + 16 * g);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) d[t] = frag_mfma<TE>(fu[s][p], fb, d[t]);
-        if ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // four reads ahead, no more registers
+          for (int p = 0; p < NP; ++p) d[t] = frag_mfma<TE>(fu[s][p], fb, d[t]);
+          if ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // four reads ahead, no more registers
+        }
       }
     }
     float v[4][8];
