@@ -356,7 +356,7 @@ constexpr int EXT_NONE = -1, EXT_ANY = 100;
 // LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
 // with 256 bytes of a bf16 row: base, residual and Y move in whole lines. 8192 x 4096 rank
-// 64: 34 us, 3.9 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 38 us (the same
+// 64: 33 us, 4.1 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 38 us (the same
 // loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: EXT_NONE (no
 // activation, gate or residual), an activation known here, or EXT_ANY: a short launch has to
 // fetch its code first, and the first kind is a third of the last (1500 x 1152 -> 2304 rank
