@@ -143,6 +143,7 @@ __global__ __launch_bounds__(512) void adapt_rows_kernel(AdaptArgs k) {
           const uint32_t o = lane + 64 * z, r = o / sp;
           if (o < 64 * sp) *reinterpret_cast<uint4*>(bs[w] + r * PITCH + 16 * (o - r * sp)) = q[z];
         }
+        wave_lds_sync();   // the pieces are those of other lanes
         if (z0 + SP < ppr) load_b(n0, z0 + SP);
         else if (n0 + 8 < u1) load_b(n0 + 8, 0);
         for (uint32_t z = 0; z < sp; ++z) {
@@ -151,6 +152,7 @@ __global__ __launch_bounds__(512) void adapt_rows_kernel(AdaptArgs k) {
 #pragma unroll
           for (int e = 0; e < PER; ++e) d = fmaf(b[e], u[PER * (z0 + z) + e], d);
         }
+        wave_lds_sync();   // the next ones take their place
       }
     }
     if (n < k.N) finish1(b0 + d, t, n, k.N, k.ep);
@@ -305,6 +307,7 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
         const int r = 8 * n + urow;
         *reinterpret_cast<uint4*>(mine + r * 128 + 16 * (piece ^ ((r >> 1) & 7))) = st[n];
       }
+      wave_lds_sync();   // rows are read by other lanes
       if (c + 1 < nc) load(c0 + NW * jc);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -321,6 +324,7 @@ __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
 #pragma unroll
           for (int t = 0; t < RT; ++t) acc[m][t] = frag_mfma<TE>(fx[m], fa[t], acc[m][t]);
       }
+      wave_lds_sync();   // the next chunk takes their place
     }
     float* const red = reinterpret_cast<float*>(smem);   // [NW][ROWS][RP]
     float* const u = k.u + int64_t(split) * k.T * k.rank;
@@ -466,9 +470,7 @@ __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(Adap
       const uint32_t q = 4 * (lane + 64 * z), r = q / uint32_t(k.rank);
       if (r < 16) *reinterpret_cast<float4*>(us + r * UP + 4 * (q - r * k.rank)) = sum[z];
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_sync();
 #pragma unroll
     for (int s = 0; s < SU; ++s) {
       float f[F::PER];

@@ -109,6 +109,16 @@ __device__ __forceinline__ void lds_dma16(const void* gptr, void* lds) {
 #endif
 }
 
+// Orders a wave's accesses to LDS that its lanes share: what a lane stored before it, every
+// lane reads behind it, and what was read before it is not overwritten. The hardware keeps
+// a wave's LDS accesses in order, so this is the compiler's order alone: no instruction, and
+// loads from memory stay in flight.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // Cross-lane exchange on the VALU (no LDS traffic). lane_xor<M>(v) returns v
 // of lane (lane ^ M) for M in {1, 2, 4, 8} through DPP: quad_perm for 1 and
 // 2, row_ror:8 for 8, and row_half_mirror (i ^ 7) followed by

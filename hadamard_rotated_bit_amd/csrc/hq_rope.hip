@@ -154,14 +154,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
       cs[w][0][i] = c;
       cs[w][1][i] = k.inverse ? -s : s;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_sync();
     float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (turns) {
       load4(&cs[w][0][4 * u], c);
       load4(&cs[w][1][4 * u], s);
     }
+    wave_lds_sync();   // the next token's take their place
 #pragma unroll 1
     for (int it = h0; it < h1; it += slots, head += slots) {
       float v[8];
