@@ -27,14 +27,13 @@ namespace hq {
 namespace {
 
 constexpr float kBorder = 0.5f - 1e-4f;
-// Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats, and
-// above 2^125 the reciprocal does: all their codes are decided in fp64.
+// Rows whose maximum is below 2^-100 lose bits of v in fp32 to the smallest floats (all of
+// them where no v is as large as half of one), and above 2^125 the reciprocal does: all their
+// codes and their scale are made in fp64.
 constexpr float kTiny = 0x1p-100f, kHuge = 0x1p125f;
-// The least fp32 value that can be a row's largest in fp64: each carries 2^-23 of itself
-// (or half the smallest float), the fp32 maximum too.
-__device__ __forceinline__ float near_of(float top) {
-  return fmaxf(0.0f, fminf(top * (1.0f - 0x1p-21f), top - 0x1p-147f));
-}
+// Of the others, a value that can be the row's largest in fp64 is at least this part of the
+// fp32 maximum: each of the two carries 2^-23 of itself.
+constexpr float kNear = 1.0f - 0x1p-21f;
 
 // Maximum over the wave of a non-negative double that few lanes have.
 __device__ __forceinline__ double few_max(double v, bool mine) {
@@ -66,6 +65,15 @@ __device__ __forceinline__ uint32_t bits_max(uint32_t v) {
 }
 constexpr uint32_t kInf = 0x7f800000u;
 
+// Is any of eight values as loaded other than +-0?
+template <typename TE>
+__device__ __forceinline__ bool not_zero(const Raw8<TE>& r) {
+  uint32_t b = 0;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(TE) / 2; ++i) b |= r.q[i].x | r.q[i].y | r.q[i].z | r.q[i].w;
+  return (b & (sizeof(TE) == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0;
+}
+
 }  // namespace
 
 // L lanes per row (64 / L rows per wave) and W waves per row (W > 1: L = 64, a block
@@ -77,8 +85,10 @@ constexpr uint32_t kInf = 0x7f800000u;
 // codes: 9.0 us; one row of 4096: 2.6 us, all of it latency.
 // The least waves per SIMD keep the registers of the codes' rare path down (12288 x 256
 // fp32 9.9 -> 9.6 us, 8192 x 4096 bf16 61.6 -> 59.5; one more wave spills: 13.1, 70.9).
+// fp32 with codes takes one wave less at two pieces (8192 x 1024: 5 waves, which spill, 19.9
+// us, 4 waves 16.0); at four pieces fp32 spills 7 to 23 registers at 4 waves.
 template <typename TE, int L, int W, int R, bool Q>
-__global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(RmsArgs k) {
+__global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 && !(Q && sizeof(TE) == 4) ? 5 : 4) void rms_kernel(RmsArgs k) {
   static_assert(W == 1 || (W == 4 && L == 64), "a block per row or whole rows per wave");
   __shared__ float part[2][W], part_z[W];   // of rows in turn: one barrier for each
   __shared__ uint32_t part_bits[2][W];
@@ -144,21 +154,12 @@ __global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(R
     const float mine = __uint_as_float(tb);   // the lane's largest |h gamma|
     double top64 = 0.0;
     if constexpr (Q) tb = bits_max<L>(tb);
-    // The fp64 maximum of the values that are at least `near`, for every lane: of the wave's
-    // part of a row (W > 1) or of each row of the wave.
-    auto max64 = [&](float near) {
+    // The largest of the lanes' values `which` in fp64, for every lane: of the wave's part of
+    // a row (W > 1) or of each row of the wave.
+    auto max64 = [&](uint32_t which) {
       double m = 0.0;
-      const bool any = mine >= near && mine > 0.0f && mine < INFINITY;
-      if (any) {
-        uint32_t which = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if (sub + STEP * i >= nv) continue;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) which |= fabsf(v[i][e]) >= near ? 1u << (8 * i + e) : 0u;
-        }
-        for (; which; which &= which - 1) m = fmax(m, fabs(exact(__builtin_ctz(which))));
-      }
+      const bool any = which != 0;
+      for (; which; which &= which - 1) m = fmax(m, fabs(exact(__builtin_ctz(which))));
       if constexpr (L == 64) {
         m = few_max(m, any);
       } else {
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(R
       const bool plain = top >= kTiny && top <= kHuge;
       const float rcp = plain ? 127.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
       const float border = plain || !finite || top == 0.0f ? kBorder : -1.0f;
-      uint32_t again = 0;   // values next to a half-integer
+      uint32_t again = 0;   // values next to a half-integer; all of a row that is not plain
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (sub + STEP * i >= nv) continue;
@@ -230,23 +231,41 @@ __global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 ? 5 : 4) void rms_kernel(R
           for (int e = 0; e < 8; ++e)
             again |= fabsf(fmaf(v[i][e], rcp, -rintf(v[i][e] * rcp))) > border ? 1u << (8 * i + e) : 0u;
         }
+        // zeros, or products that are none but round to it
+        if (top == 0.0f && k.gamma && (not_zero(x[i]) || (k.r && not_zero(r[i])))) again |= 255u << (8 * i);
         *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) =
             finite ? make_uint2(d[0], d[1]) : make_uint2(0, 0);
       }
+      auto largest = [&] {   // the lane's values among which the row's fp64 maximum is
+        uint32_t which = plain ? 0u : again;
+        if (plain && mine >= top * kNear) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            if (sub + STEP * i >= nv) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) which |= fabsf(v[i][e]) >= top * kNear ? 1u << (8 * i + e) : 0u;
+          }
+        }
+        return which;
+      };
       // every wave of the row has to help where one needs the fp64 maximum
       if constexpr (W == 1) {
-        if (__any(again)) top64 = max64(near_of(top));
+        if (__any(again)) top64 = max64(largest());
       } else if (__syncthreads_or(again != 0)) {
-        top64 = max64(near_of(top));
+        top64 = max64(largest());
         if ((threadIdx.x & 63) == 0) part_top[int(threadIdx.x) >> 6] = top64;
         __syncthreads();
         top64 = fmax(fmax(part_top[0], part_top[1]), fmax(part_top[2], part_top[3]));
       }
       for (; again; again &= again - 1) {
         const int n = __builtin_ctz(again);
-        k.codes[base + 8 * STEP * (n >> 3) + (n & 7)] = uint8_t(int8_t(int(rint(exact(n) / (top64 / 127.0)))));
+        const double q = top64 > 0.0 ? rint(exact(n) / (top64 / 127.0)) : 0.0;
+        k.codes[base + 8 * STEP * (n >> 3) + (n & 7)] = uint8_t(int8_t(int(q)));
       }
-      if (sub == 0 && row < k.T) k.scales[row] = finite ? top * (1.0f / 127.0f) * rstd : __uint_as_float(0x7fc00000u);
+      if (sub == 0 && row < k.T)
+        k.scales[row] = !finite ? __uint_as_float(0x7fc00000u)
+                        : plain ? top * (1.0f / 127.0f) * rstd
+                                : float(top64 * double(rstd) * (1.0 / 127.0));
     }
     if (k.h) {
 #pragma unroll
