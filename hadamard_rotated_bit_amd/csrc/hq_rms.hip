@@ -34,6 +34,9 @@ constexpr float kTiny = 0x1p-100f, kHuge = 0x1p125f;
 // Of the others, a value that can be the row's largest in fp64 is at least this part of the
 // fp32 maximum: each of the two carries 2^-23 of itself.
 constexpr float kNear = 1.0f - 0x1p-21f;
+// The norm is v rstd: what v loses to the smallest floats (half of one, 2^-150) is below
+// 2^-126 of the norm up to this rstd. Beyond, gamma comes last.
+constexpr float kSteep = 0x1p24f;
 
 // Maximum over the wave of a non-negative double that few lanes have.
 __device__ __forceinline__ double few_max(double v, bool mine) {
@@ -85,10 +88,14 @@ __device__ __forceinline__ bool not_zero(const Raw8<TE>& r) {
 // codes: 9.0 us; one row of 4096: 2.6 us, all of it latency.
 // The least waves per SIMD keep the registers of the codes' rare path down (12288 x 256
 // fp32 9.9 -> 9.6 us, 8192 x 4096 bf16 61.6 -> 59.5; one more wave spills: 13.1, 70.9).
-// fp32 with codes takes one wave less at two pieces (8192 x 1024: 5 waves, which spill, 19.9
-// us, 4 waves 16.0); at four pieces fp32 spills 7 to 23 registers at 4 waves.
+// fp32 takes one wave less where it would spill: with codes at two pieces (8192 x 1024: 5
+// waves 19.9 us, 4 waves 16.0) and at four (2048 x 8192 norm and codes: 4 waves 45.7, 3 waves
+// 35.3; 4096 x 2048: 23.0, 18.1).
+constexpr int rms_waves(bool f32, int R, bool Q) {
+  return R == 1 ? 6 : R == 2 ? (f32 && Q ? 4 : 5) : R == 4 && f32 ? 3 : 4;
+}
 template <typename TE, int L, int W, int R, bool Q>
-__global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 && !(Q && sizeof(TE) == 4) ? 5 : 4) void rms_kernel(RmsArgs k) {
+__global__ __launch_bounds__(256, rms_waves(sizeof(TE) == 4, R, Q)) void rms_kernel(RmsArgs k) {
   static_assert(W == 1 || (W == 4 && L == 64), "a block per row or whole rows per wave");
   __shared__ float part[2][W], part_z[W];   // of rows in turn: one barrier for each
   __shared__ uint32_t part_bits[2][W];
@@ -277,12 +284,20 @@ __global__ __launch_bounds__(256, R == 1 ? 6 : R == 2 && !(Q && sizeof(TE) == 4)
       }
     }
     if (k.y) {
+      const bool steep = k.gamma && rstd > kSteep;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (sub + STEP * i >= nv) continue;
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd;
+        if (steep) {
+          float h[8], g[8];
+          load8(k.gamma + 8 * (sub + STEP * i), g);
+          sum_of(i, h);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd * g[e];
+        }
         if (k.y_bf16) store8(static_cast<uint16_t*>(k.y) + base + 8 * STEP * i, y);
         else store8(static_cast<float*>(k.y) + base + 8 * STEP * i, y);
       }

@@ -459,11 +459,14 @@ int hq_rms_validate(const hq_rms_desc* desc);
  *  H [T, channels] x_dtype, Y [T, channels] y_dtype, codes int8 [T, channels] with
  *  scales f32 [T]: those in desc->outputs are written, the others ignored.
  * The norm and the codes are those of the unrounded h; sums are fp32, and codes are
- * what 64-bit arithmetic gives them (scales are fp32). H may be X or residual, and Y
- * may be X or residual where the types are the same; otherwise the outputs must not
- * overlap an input or each other. Rows whose squares pass the largest float are normed
- * like others; NaN and infinities stay in their row; a row with an h gamma that is not
- * a finite float has codes of 0 and a NaN scale (and a Y that is not finite there). */
+ * what 64-bit arithmetic gives them: round(v / (max |v| / 127)) of v = h gamma (scales are
+ * fp32). Where h gamma is below the normal floats, scales and codes are as good as
+ * elsewhere and Y is off by 2^-126 more, the least normal float, at most. H may be X or
+ * residual, and Y may be X or residual where the types are the same; otherwise the
+ * outputs must not overlap an input or each other. Rows whose squares pass the largest
+ * float are normed like others; NaN and infinities stay in their row; a row with an h
+ * gamma that is not a finite float has codes of 0 and a NaN scale (and a Y that is not
+ * finite there). */
 int hq_rms_norm(const hq_rms_desc* desc, const void* X, const void* residual, const float* gamma,
                 int64_t T, void* H, void* Y, int8_t* codes, float* scales, void* stream);
 

@@ -78,3 +78,26 @@ def test_one_value_below_the_smallest_float(C):
     x[1, 3], x[4, C - 1] = 2.0 ** -80, -2.0 ** -90
     gamma = torch.full((C,), 2.0 ** -75, device="cuda")
     check_codes(x, gamma, 2.0 ** -100, f"C={C}")
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dt", [hq.F32, hq.BF16])
+@pytest.mark.parametrize("ydt", [hq.F32, hq.BF16])
+def test_norm_of_subnormal_products(C, dt, ydt):
+    # h gamma is subnormal or nothing in fp32, the norm an ordinary number (rstd up to 2^50); up to an
+    # rstd of 2^24 an error of half the smallest float of h gamma is at most 2^-126 of the norm
+    x, gamma = randn(C, 50, C), randn(C + 1, C) * 2.0 ** -85
+    x = (x * 2.0 ** -torch.linspace(15.0, 100.0, 50, device="cuda")[:, None]).to(DT[dt])
+    x[7], x[20] = 0.0, randn(C + 2, C).to(DT[dt])
+    r = (x.float() * 0.375).to(DT[dt])
+    for outputs in (hq.HQ_RMS_Y, hq.HQ_RMS_Y | hq.HQ_RMS_SUM | CODES):
+        for res in (None, r):
+            o = hq.rms_norm(hq.RmsNormDesc(C, 2.0 ** -100, outputs, dt, ydt), x, gamma, res)
+            y, _, _ = rms64(x, res, gamma, 2.0 ** -100)
+            half = torch.finfo(DT[ydt]).eps / 2
+            least = 2.0 ** -126 if ydt == hq.F32 else 2.0 ** -126 + 2.0 ** -134   # bf16's own smallest: 2^-133
+            assert_within(o.y, y, (28 * U32 * (1 + half) + half) * y.abs() + least, f"C={C} dt={dt} ydt={ydt} {outputs}")
+            big = (x.double() + (0 if res is None else res.double())).square().mean(1) < 2.0 ** -50
+            assert big.sum() > 20
+            assert_within(o.y[big], y[big], (28 * U32 * (1 + half) + half) * y[big].abs() + (2.0 ** -133 if ydt == hq.BF16 else 2.0 ** -148),
+                          f"C={C} dt={dt} ydt={ydt} {outputs} where rstd is past 2^24")
