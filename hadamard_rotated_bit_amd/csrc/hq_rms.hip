@@ -191,10 +191,11 @@ __global__ __launch_bounds__(256, rms_waves(sizeof(TE) == 4, R, Q)) void rms_ker
       turn ^= 1;
     }
     // rsq is off by one unit; eps keeps it from the smallest floats, which it does not take
-    float rstd = __builtin_amdgcn_rsqf(fmaf(s2, k.inv_c, k.eps));
-    if (__any(s2 == INFINITY)) {
-      // squares past the largest float: once more, of h 2^-80 (the same branch for a
-      // whole block where a block has one row)
+    const float ms = fmaf(s2, k.inv_c, k.eps);
+    float rstd = __builtin_amdgcn_rsqf(ms);
+    if (__any(ms == INFINITY)) {
+      // squares past the largest float, or with eps: once more, of h 2^-80 (the same branch
+      // for a whole block where a block has one row)
       float z2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(256, rms_waves(sizeof(TE) == 4, R, Q)) void rms_ker
         __syncthreads();
         z2 = (part_z[0] + part_z[1]) + (part_z[2] + part_z[3]);
       }
-      if (s2 == INFINITY) rstd = 0x1p-80f / sqrtf(z2 * k.inv_c + k.eps * 0x1p-80f * 0x1p-80f);
+      if (ms == INFINITY) rstd = 0x1p-80f / sqrtf(z2 * k.inv_c + k.eps * 0x1p-80f * 0x1p-80f);
     }
     if constexpr (Q) {
       const bool finite = tb < kInf;
