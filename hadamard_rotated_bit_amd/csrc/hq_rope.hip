@@ -171,10 +171,11 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs k) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
         q = run_sum(q, slot * U, U, u);
-        const bool large = q == INFINITY;
+        const float ms = fmaf(q, inv, k.eps);
+        const bool large = ms == INFINITY;
         // rsq is off by one unit; eps keeps it from the smallest floats, which it does not take
-        float rstd = __builtin_amdgcn_rsqf(fmaf(q, inv, k.eps));
-        if (__any(large)) {   // squares past the largest float: once more, of x 2^-80
+        float rstd = __builtin_amdgcn_rsqf(ms);
+        if (__any(large)) {   // squares past the largest float, or with eps: once more, of x 2^-80
           float z = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
