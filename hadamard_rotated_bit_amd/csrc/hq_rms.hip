@@ -14,9 +14,11 @@
 // carries two roundings of 2^-24 in v, two in the maximum, and 2^-23 + 2^-24 in 127
 // rcp(max): an error below 127 x 7 x 2^-24 = 5.3e-5. Where q is further
 // than 1e-4 from a half-integer its rounding is the exact one; the values nearer to one
-// (2 in 10^4) are decided again in fp64 with the row's fp64 maximum, which needs only
-// the values within 2^-21 of the fp32 maximum in fp64. A row with a v that is not a
-// finite float has codes 0 and a NaN scale.
+// (2 in 10^4) are decided again from v and the row's maximum in fp64, which needs only
+// the values within 2^-21 of the fp32 maximum in fp64. Ties are common where gamma is absent
+// (half of the largest value is 63.5 of the scale) and a rounded quotient misses them for 15
+// of the 128 bf16 mantissas, so products are compared (code_of). A row with a v that is not
+// a finite float has codes 0 and a NaN scale.
 #include "hq_epilogue.h"
 #include "hq_internal.h"
 
@@ -37,6 +39,16 @@ constexpr float kNear = 1.0f - 0x1p-21f;
 // The norm is v rstd: what v loses to the smallest floats (half of one, 2^-150) is below
 // 2^-126 of the norm up to this rstd. Beyond, gamma comes last.
 constexpr float kSteep = 0x1p24f;
+
+// 127 v / top rounded half to even, without the rounding of a quotient: the products that
+// decide between two codes are compared with what their roundings leave out.
+__device__ __forceinline__ int code_of(double v, double top) {
+  const double a = fabs(v), n = floor(127.0 * a / top), c = 2.0 * n + 1.0;
+  const double p = 254.0 * a, q = c * top;
+  const double over = (p - q) + (fma(254.0, a, -p) - fma(c, top, -q));   // of 254 |v| over c top
+  const int code = int(n) + (over > 0.0 || (over == 0.0 && (int(n) & 1)) ? 1 : 0);
+  return v < 0.0 ? -code : code;
+}
 
 // Maximum over the wave of a non-negative double that few lanes have.
 __device__ __forceinline__ double few_max(double v, bool mine) {
@@ -267,8 +279,7 @@ __global__ __launch_bounds__(256, rms_waves(sizeof(TE) == 4, R, Q)) void rms_ker
       }
       for (; again; again &= again - 1) {
         const int n = __builtin_ctz(again);
-        const double q = top64 > 0.0 ? rint(exact(n) / (top64 / 127.0)) : 0.0;
-        k.codes[base + 8 * STEP * (n >> 3) + (n & 7)] = uint8_t(int8_t(int(q)));
+        k.codes[base + 8 * STEP * (n >> 3) + (n & 7)] = uint8_t(top64 > 0.0 ? code_of(exact(n), top64) : 0);
       }
       if (sub == 0 && row < k.T)
         k.scales[row] = !finite ? __uint_as_float(0x7fc00000u)

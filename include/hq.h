@@ -459,7 +459,7 @@ int hq_rms_validate(const hq_rms_desc* desc);
  *  H [T, channels] x_dtype, Y [T, channels] y_dtype, codes int8 [T, channels] with
  *  scales f32 [T]: those in desc->outputs are written, the others ignored.
  * The norm and the codes are those of the unrounded h; sums are fp32, and codes are
- * what 64-bit arithmetic gives them: round(v / (max |v| / 127)) of v = h gamma (scales are
+ * round(127 v / max |v|) of v = h gamma in 64 bits, the quotient unrounded (scales are
  * fp32). Where h gamma is below the normal floats, scales and codes are as good as
  * elsewhere and Y is off by 2^-126 more, the least normal float, at most. H may be X or
  * residual, and Y may be X or residual where the types are the same; otherwise the
