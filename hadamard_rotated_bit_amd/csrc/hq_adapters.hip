@@ -44,14 +44,15 @@ __device__ __forceinline__ void get16(const uint4& q, float* v) {
 
 // ---- row by row ---------------------------------------------------------------
 
-
 // Y of one row (block x) and a part of its columns (block y; each part takes the row's u
 // for itself: one launch). Eight waves share the rank indexes of u, JW each, all their
 // loads of U strips of K in flight; then 64 columns a wave at a time: B_a's rows pass
 // through the wave's own LDS, read in whole lines, so that each lane has a column. Bound
 // by the chain of a launch, the id, A_a and x, B_a and the store for few rows (24 rows of
-// 4096 -> 4096 rank 16: 6.0 us) and by instruction issue for many: two or four rows a block
-// that share what they fetch are no faster (700 rows of 1024 -> 1024 rank 8: 7.7, 7.8, 8.7).
+// 4096 -> 4096 rank 16: 6.0 us). Many rows take several rounds of blocks, each with that
+// chain: 1037 of 1160 -> 2312 rank 8 fp32, 18.7 us, two rounds of 768 blocks, the vector ALU
+// busy half of the time, waves waiting 48 % of theirs. Two or four rows a block that share
+// what they fetch are no faster (700 rows of 1024 -> 1024 rank 8: 7.7, 7.8, 8.7).
 template <typename TE, int JW, int U>
 __global__ __launch_bounds__(512) void adapt_rows_kernel(AdaptArgs k) {
   constexpr int PER = 16 / sizeof(TE);             // elements of 16 bytes
@@ -247,8 +248,9 @@ __device__ __forceinline__ int tile_id(const AdaptArgs& k, int64_t r0, int r) {
 // passes it through its own part of the LDS (slot c ^ (r / 2) mod 8 of row r: 16 lanes
 // read 16 distinct positions of the 64 banks) and has the next chunk's loads in flight
 // meanwhile. The waves' sums are joined in LDS in wave order. 8192 x 4096 rank 64: 27 us,
-// 7.3 TB/s of x and A_a through the L2s (2.5 TB/s of x from memory); tiles of 64 rows, which
-// halve A_a's part, 25 us but two parts of u to add; two chunks in flight no gain.
+// 7.3 TB/s of x and A_a through the L2s (2.5 TB/s of x from memory); with tiles of 64 rows,
+// which halve A_a's part and make two of u, both products take 58.6 us against 59.5, at 2500
+// rows 29.2 against 27.3; two chunks in flight no gain.
 template <typename TE, int MT, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void adapt_down_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
@@ -360,11 +362,14 @@ constexpr int EXT_NONE = -1, EXT_ANY = 100;
 // LDS, its loads in flight during the slab before. MFMA t has the columns 8 j + t on its
 // lanes j, so that a lane ends with eight consecutive columns of four rows, and 16 lanes
 // with 256 bytes of a bf16 row: base, residual and Y move in whole lines. 8192 x 4096 rank
-// 64: 33 us, 4.1 TB/s of base and Y; 8192 x 4608 rank 32 with a tanh GELU: 38 us (the same
-// loads and stores alone 35 and 38 us). SU: k-steps of the product. EXT: EXT_NONE (no
-// activation, gate or residual), an activation known here, or EXT_ANY: a short launch has to
-// fetch its code first, and the first kind is a third of the last (1500 x 1152 -> 2304 rank
-// 16: 9.4 us with any activation, 8.8 with SiLU or a tanh GELU alone).
+// 64: 33 us, 4.1 TB/s of base and Y, waves waiting 43 % of their time; 8192 x 4608 rank 32
+// with a tanh GELU: 38 us, the vector ALU busy three quarters of it. SU: k-steps of the
+// product. EXT: EXT_NONE (no activation, gate or residual), an activation known here, or
+// EXT_ANY: a short launch has to fetch its code first, and the first kind is a third of the
+// last. As EXT_ANY and by themselves: 1500 x 1152 -> 2304 rank 16, nothing 8.1 and 6.7 us, SiLU
+// 8.8 and 8.2, tanh GELU 9.0 and 8.4; both products of 8192 x 4096 -> 4096 rank 64, nothing
+// 61.7 and 59.5, of 8192 x 1152 -> 4608 rank 32, SiLU 38.7 and 37.9, tanh GELU 39.2 and 38.5.
+// ReLU (8.5 and 37.1) and GELU (41.2), gates and residuals have no kernel of their own.
 template <typename TE, typename TY, int SU, int EXT>
 __global__ __launch_bounds__(256, SU > 2 ? 1 : 3) void adapt_up_tile_kernel(AdaptArgs k) {
   using F = Frag<TE>;
@@ -639,8 +644,9 @@ template <typename TE, typename TY, int SU>
 hipError_t launch_up(AdaptArgs a, hipStream_t s) {
   const int64_t tiles = (a.T + 63) / 64, slabs = (a.N + 127) / 128;
   // column groups: up to 12 per row tile, more where that leaves CUs without a block, whole
-  // slabs each (8192 rows, 36 slabs: 4 groups 62 us, 8 49, 12 43.6; 32 slabs rank 64: 4 43,
-  // 11 39, 16 41; 1000 rows, 19 slabs: 8 15.1, 12 11.1, 19 9.6)
+  // slabs each (both products, 8192 rows: 36 slabs rank 32, 4 groups 37.6 us, 8 36.8, 12 38.4,
+  // 36 40.8; 32 slabs rank 64, 4 63.4, 8 60.8, 12 59.5, 16 60.7, 32 63.4; this one, 1000 rows,
+  // 19 slabs: 8 8.9, 12 7.2, 19 6.6)
   const int64_t groups = std::max<int64_t>(12, 512 / tiles);
   a.slabs = int((slabs + groups - 1) / groups);
   const dim3 grid(unsigned(tiles + 7) / 8 * 8, unsigned((slabs + a.slabs - 1) / a.slabs));
@@ -696,16 +702,22 @@ hipError_t launch_rows(const AdaptArgs& a, hipStream_t s) {
 
 // One row after the other or tiles of rows? Row by row each row fetches its adapter's
 // factors (from the caches), in tiles each adapter of a tile is fetched once, but there
-// are two launches and a chain of waits in each. Rows are bound by issue, so the rule counts
-// products. With runs of rows the two cross at 40 million (us, rows / tiles, no epilogue:
-// 700 rows of 1024 -> 1024 rank 8 bf16, 11 million, 7.7 / 10.9; 600 of 2048 -> 2048 rank 16
-// bf16, 39 million, 10.9 / 11.0; 1037 of 2160 -> 2312 rank 8 fp32, 37 million, 20.4 / 19.7;
-// 300 of 4096 -> 1152 rank 32 bf16, 50 million, 13.7 / 12.2; 1000 of 1160 -> 2312 rank 32
-// bf16, 111 million, 24 / 12.3) or where the rows are many (4000 of 256 -> 512 rank 16 bf16
-// 19.2 / 10.8). With an adapter per row rows win by far (256 rows of 2048 -> 2048, rank 32,
-// 64 adapters: 14.2 / 80; 512 rows, 128 adapters: 21.6): the ids are on the device, so
-// batches of a decoding step's size count as mixed up to 2^27 products, 256 rows of
-// 4096 -> 4096 rank 64.
+// are two launches and a chain of waits in each. The ids are on the device, so the rule counts
+// products alone, and batches of a decoding step's size count as mixed up to 2^27 products, 256
+// rows of 4096 -> 4096 rank 64. Rows / tiles, a call among others, and the kernels alone (us,
+// no epilogue, bf16 but for the third):
+//   700 rows of 1024 -> 1024 rank 8, 11 million       9.0 / 13.3    7.8 / 10.0
+//   600 of 2048 -> 2048 rank 16, 39 million          11.4 / 13.1   12.0 / 9.8
+//   1037 of 2160 -> 2312 rank 8 fp32, 37 million     20.4 / 18.0   20.8 / 18.0
+//   300 of 4096 -> 1152 rank 32, 50 million          12.9 / 13.1   13.5 / 9.9
+//   1000 of 1160 -> 2312 rank 32, 111 million        24.1 / 13.1   25.0 / 12.5
+//   4000 of 256 -> 512 rank 16, 49 million                         21.6 / 9.9
+//   512 of 2048 -> 2048 rank 32, one adapter         13.6 / 13.0   14.7 / 8.7
+//   256 of 2048 -> 2048 rank 32, 64 adapters mixed   13.4 / 73     13.6 / 73
+//   512 of 2048 -> 2048 rank 32, 128 adapters mixed  21.3 / 94
+//   256 of 4096 -> 4096 rank 64, 64 adapters mixed   40.7 / 113; one adapter 27.0 / 12.8
+// Mixed rows past the limit take the tiles' passes: 128 rows of 4096 -> 14336 rank 64 with 32
+// adapters 146 us (row by row 50).
 bool by_rows(int64_t T, int K, int N, int rank) {
   const double products = double(T) * rank * (double(K) + N);
   return T <= 4 || (T <= 512 && products <= 0x1p27) || (T <= 2048 && products <= 40e6);

@@ -95,9 +95,10 @@ __device__ __forceinline__ bool not_zero(const Raw8<TE>& r) {
 // per row), R pieces of 8 channels per lane. Q: codes are wanted. Rows of up to 2048
 // channels take a wave or part of one, which needs no barrier; longer ones a block, which
 // keeps them in registers. 8192 x 4096 bf16, residual, sum, norm and codes: 54 to 59 us, 5.1
-// to 5.6 TB/s; 8192 x 1152, sum and codes: 16.4 us, 4.0 TB/s (a quarter of the lanes' third
-// pieces have channels; deciding codes again costs a tenth); 12288 x 256 fp32, norm and
-// codes: 9.0 us; one row of 4096: 2.6 us, all of it latency.
+// to 5.6 TB/s; 8192 x 1152, sum and codes: 16.6 us, 4.0 TB/s (a quarter of the lanes' third
+// pieces have channels; deciding codes again costs a tenth). fp32, norm and codes: 12288 x 256
+// 9.4 us, 8192 x 1024 16.1 (4.7 TB/s), 4096 x 2048 18.1, 2048 x 8192 35.4 (4.3); one row of
+// 4096: 2.6 us, all of it latency.
 // The least waves per SIMD keep the registers of the codes' rare path down (12288 x 256
 // fp32 9.9 -> 9.6 us, 8192 x 4096 bf16 61.6 -> 59.5; one more wave spills: 13.1, 70.9).
 // fp32 takes one wave less where it would spill: with codes at two pieces (8192 x 1024: 5
