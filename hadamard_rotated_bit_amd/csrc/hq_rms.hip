@@ -253,7 +253,9 @@ __global__ __launch_bounds__(256, rms_waves(sizeof(TE) == 4, R, Q)) void rms_ker
             again |= fabsf(fmaf(v[i][e], rcp, -rintf(v[i][e] * rcp))) > border ? 1u << (8 * i + e) : 0u;
         }
         // zeros, or products that are none but round to it
-        if (top == 0.0f && k.gamma && (not_zero(x[i]) || (k.r && not_zero(r[i])))) again |= 255u << (8 * i);
+        if (top == 0.0f && k.gamma && (not_zero(x[i]) || (k.r && not_zero(r[i]))) &&
+            not_zero(raw_load(k.gamma + 8 * (sub + STEP * i))))
+          again |= 255u << (8 * i);
         *reinterpret_cast<uint2*>(k.codes + base + 8 * STEP * i) =
             finite ? make_uint2(d[0], d[1]) : make_uint2(0, 0);
       }
